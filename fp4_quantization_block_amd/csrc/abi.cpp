@@ -413,4 +413,247 @@ mx_status mx_dequantize(const void* q, const uint8_t* scales, const float* tenso
     return hip_status(mx::launch_dequantize(j, (hipStream_t)stream));
 }
 
+namespace {
+
+uintptr_t elem_bytes(int32_t dtype) { return dtype == MX_SRC_F32 ? 4 : 2; }   // MX_OUT_* has the same values
+
+mx_status check_shape(int32_t src, int64_t rows, int64_t cols)
+{
+    if (src != MX_SRC_F32 && src != MX_SRC_BF16) return fail(MX_ERR_INVALID_ARG, "unknown source dtype");
+    if (rows <= 0 || cols <= 0) return fail(MX_ERR_INVALID_ARG, "rows and cols must be > 0");
+    if (rows >= (int64_t)1 << 31 || cols >= (int64_t)1 << 31) return fail(MX_ERR_INVALID_ARG, "rows and cols must be < 2^31");
+    return MX_OK;
+}
+
+// one matrix operand that is there
+mx_status check_matrix(const void* p, int64_t ld, int64_t cols, int32_t dtype, const char* what)
+{
+    char text[96];
+    if (ld < cols) {
+        std::snprintf(text, sizeof text, "the row stride of %s must be >= cols", what);
+        return fail(MX_ERR_INVALID_ARG, text);
+    }
+    if (reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) != 0) {
+        std::snprintf(text, sizeof text, "%s must be aligned to its element size", what);
+        return fail(MX_ERR_ALIGNMENT, text);
+    }
+    return MX_OK;
+}
+
+// one MX copy (codes and scales) that a call reads or writes, or neither
+mx_status check_copy(int32_t fmt, const void* q, const void* s, int64_t cols)
+{
+    if (!q && !s) return MX_OK;
+    if (!q || !s) return fail(MX_ERR_INVALID_ARG, "codes and scales of a copy must be given together");
+    if (fmt == MX_E2M1) return fail(MX_ERR_UNSUPPORTED, "copies of the activation operators are FP8 (E4M3 or E5M2)");
+    if (fmt != MX_E4M3 && fmt != MX_E5M2) return fail(MX_ERR_INVALID_ARG, "unknown element format");
+    if (cols % 32 != 0) return fail(MX_ERR_INVALID_ARG, "row blocks need cols % 32 == 0");
+    if (!aligned16(q)) return fail(MX_ERR_ALIGNMENT, "codes must be 16-byte aligned");
+    return MX_OK;
+}
+
+mx_status check_f32(const void* p)
+{
+    return reinterpret_cast<uintptr_t>(p) & 3u ? fail(MX_ERR_ALIGNMENT, "fp32 vectors must be 4-byte aligned") : MX_OK;
+}
+
+mx_status check_params(const void* weight, const void* bias, int32_t dtype)
+{
+    if (!weight && !bias) return MX_OK;
+    if (dtype != MX_SRC_F32 && dtype != MX_SRC_BF16) return fail(MX_ERR_INVALID_ARG, "unknown parameter dtype");
+    if ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(bias)) % elem_bytes(dtype) != 0)
+        return fail(MX_ERR_ALIGNMENT, "weight and bias must be aligned to their element size");
+    return MX_OK;
+}
+
+}  // namespace
+
+mx_status mx_norm_forward(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, int32_t src_dtype,
+                          int64_t rows, int64_t cols, int32_t kind, const void* weight, const void* bias,
+                          int32_t param_dtype, float eps, void* sum, int64_t ld_sum, void* y, int64_t ld_y,
+                          int32_t out_dtype, int32_t y_fmt, void* qy, uint8_t* sy, int32_t ckpt_fmt, void* qx,
+                          uint8_t* sx, float* mean, float* rstd, void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_shape(src_dtype, rows, cols);
+    if (s != MX_OK) return s;
+    if (!x) return fail(MX_ERR_INVALID_ARG, "x is NULL");
+    if ((s = check_matrix(x, ld_x, cols, src_dtype, "x")) != MX_OK) return s;
+    if ((residual != nullptr) != (sum != nullptr)) return fail(MX_ERR_INVALID_ARG, "residual and sum must be given together");
+    if (residual && (s = check_matrix(residual, ld_res, cols, src_dtype, "residual")) != MX_OK) return s;
+    if (residual && (s = check_matrix(sum, ld_sum, cols, src_dtype, "sum")) != MX_OK) return s;
+    if (kind != MX_NORM_LAYER && kind != MX_NORM_RMS) return fail(MX_ERR_INVALID_ARG, "unknown norm kind");
+    if ((s = check_params(weight, bias, param_dtype)) != MX_OK) return s;
+    if (!(eps >= 0.0f) || eps > 3.4028234663852886e38f) return fail(MX_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!y && !qy) return fail(MX_ERR_INVALID_ARG, "one of y and qy is needed");
+    if (y) {
+        if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return fail(MX_ERR_INVALID_ARG, "unknown output dtype");
+        if ((s = check_matrix(y, ld_y, cols, out_dtype, "y")) != MX_OK) return s;
+    }
+    if ((s = check_copy(y_fmt, qy, sy, cols)) != MX_OK) return s;
+    if ((s = check_copy(ckpt_fmt, qx, sx, cols)) != MX_OK) return s;
+    if ((s = check_f32(mean)) != MX_OK || (s = check_f32(rstd)) != MX_OK) return s;
+    mx::NormFwdJob j{};
+    j.x = x; j.ld_x = ld_x; j.residual = residual; j.ld_res = ld_res;
+    j.src = src_dtype; j.rows = rows; j.cols = cols; j.layer = kind == MX_NORM_LAYER;
+    j.weight = weight; j.bias = bias; j.param_f32 = param_dtype == MX_SRC_F32; j.eps = eps;
+    j.sum = sum; j.ld_sum = ld_sum;
+    j.y = y; j.ld_y = ld_y; j.out_f32 = out_dtype == MX_OUT_F32;
+    j.y_fmt = y_fmt; j.qy = (uint8_t*)qy; j.sy = sy;
+    j.ckpt_fmt = ckpt_fmt; j.qx = (uint8_t*)qx; j.sx = sx;
+    j.mean = j.layer ? mean : nullptr; j.rstd = rstd;
+    return hip_status(mx::launch_norm_fwd(j, (hipStream_t)stream));
+}
+
+int64_t mx_norm_backward_workspace_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0 || rows >= (int64_t)1 << 31 || cols >= (int64_t)1 << 31) return 0;
+    return mx::norm_bwd_partials(rows, cols) * cols * 2 * (int64_t)sizeof(float);
+}
+
+mx_status mx_norm_backward(const void* dy, int64_t ld_dy, int32_t src_dtype, int64_t rows, int64_t cols,
+                           const void* x, int64_t ld_x, int32_t ckpt_fmt, const void* qx, const uint8_t* sx,
+                           const float* mean, const float* rstd, int32_t kind, const void* weight,
+                           int32_t param_dtype, const void* dsum, int64_t ld_dsum, void* dx, int64_t ld_dx,
+                           float* dweight, float* dbias, void* work, int64_t work_bytes, void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_shape(src_dtype, rows, cols);
+    if (s != MX_OK) return s;
+    if (!dy || !dx) return fail(MX_ERR_INVALID_ARG, "dy and dx must not be NULL");
+    if ((s = check_matrix(dy, ld_dy, cols, src_dtype, "dy")) != MX_OK) return s;
+    if ((s = check_matrix(dx, ld_dx, cols, src_dtype, "dx")) != MX_OK) return s;
+    if ((s = check_copy(ckpt_fmt, qx, sx, cols)) != MX_OK) return s;
+    if ((x != nullptr) == (qx != nullptr)) return fail(MX_ERR_INVALID_ARG, "one of x and its checkpoint is needed");
+    if (x && (s = check_matrix(x, ld_x, cols, src_dtype, "x")) != MX_OK) return s;
+    if (kind != MX_NORM_LAYER && kind != MX_NORM_RMS) return fail(MX_ERR_INVALID_ARG, "unknown norm kind");
+    if (!rstd || (kind == MX_NORM_LAYER && !mean)) return fail(MX_ERR_INVALID_ARG, "rstd, and mean for the layer norm, must not be NULL");
+    if ((s = check_params(weight, nullptr, param_dtype)) != MX_OK) return s;
+    if (dsum && (s = check_matrix(dsum, ld_dsum, cols, src_dtype, "dsum")) != MX_OK) return s;
+    for (const void* p : {(const void*)mean, (const void*)rstd, (const void*)dweight, (const void*)dbias, (const void*)work})
+        if ((s = check_f32(p)) != MX_OK) return s;
+    if (dweight || dbias) {
+        if (!work) return fail(MX_ERR_INVALID_ARG, "dweight and dbias need work");
+        if (work_bytes < mx_norm_backward_workspace_bytes(rows, cols))
+            return fail(MX_ERR_INVALID_ARG, "work is smaller than mx_norm_backward_workspace_bytes()");
+    }
+    mx::NormBwdJob j{};
+    j.dy = dy; j.ld_dy = ld_dy; j.src = src_dtype; j.rows = rows; j.cols = cols;
+    j.x = x; j.ld_x = ld_x; j.ckpt_fmt = ckpt_fmt; j.qx = (const uint8_t*)qx; j.sx = sx;
+    j.layer = kind == MX_NORM_LAYER; j.mean = mean; j.rstd = rstd;
+    j.weight = weight; j.param_f32 = param_dtype == MX_SRC_F32;
+    j.dsum = dsum; j.ld_dsum = ld_dsum; j.dx = dx; j.ld_dx = ld_dx;
+    j.dweight = dweight; j.dbias = dbias; j.work = (float*)work;
+    return hip_status(mx::launch_norm_bwd(j, (hipStream_t)stream));
+}
+
+namespace {
+
+mx_status check_act(int32_t act)
+{
+    if (act != MX_ACT_SILU && act != MX_ACT_GELU && act != MX_ACT_GELU_TANH) return fail(MX_ERR_INVALID_ARG, "unknown gate function");
+    return MX_OK;
+}
+
+// dh and the gate and up of a backward call, from tensors or checkpoints
+mx_status check_glu_inputs(const void* dh, int64_t ld_dh, int32_t src, int64_t rows, int64_t cols, const void* gate,
+                           int64_t ld_gate, const void* up, int64_t ld_up, int32_t ckpt_fmt, const void* qg,
+                           const uint8_t* sg, const void* qu, const uint8_t* su, int32_t act)
+{
+    mx_status s = check_shape(src, rows, cols);
+    if (s != MX_OK) return s;
+    if (!dh) return fail(MX_ERR_INVALID_ARG, "dh is NULL");
+    if ((s = check_matrix(dh, ld_dh, cols, src, "dh")) != MX_OK) return s;
+    if ((s = check_copy(ckpt_fmt, qg, sg, cols)) != MX_OK || (s = check_copy(ckpt_fmt, qu, su, cols)) != MX_OK) return s;
+    if ((gate != nullptr) != (up != nullptr) || (qg != nullptr) != (qu != nullptr) || (gate != nullptr) == (qg != nullptr))
+        return fail(MX_ERR_INVALID_ARG, "gate and up, or the checkpoints of both, are needed");
+    if (gate && ((s = check_matrix(gate, ld_gate, cols, src, "gate")) != MX_OK ||
+                 (s = check_matrix(up, ld_up, cols, src, "up")) != MX_OK))
+        return s;
+    return check_act(act);
+}
+
+mx::GluBwdJob glu_job(const void* dh, int64_t ld_dh, int32_t src, int64_t rows, int64_t cols, const void* gate,
+                      int64_t ld_gate, const void* up, int64_t ld_up, int32_t ckpt_fmt, const void* qg,
+                      const uint8_t* sg, const void* qu, const uint8_t* su, int32_t act)
+{
+    mx::GluBwdJob j{};
+    j.dh = dh; j.ld_dh = ld_dh; j.src = src; j.rows = rows; j.cols = cols; j.act = act;
+    j.gate = gate; j.ld_gate = ld_gate; j.up = up; j.ld_up = ld_up;
+    j.ckpt_fmt = ckpt_fmt; j.qg = (const uint8_t*)qg; j.sg = sg; j.qu = (const uint8_t*)qu; j.su = su;
+    return j;
+}
+
+}  // namespace
+
+mx_status mx_glu_forward(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t src_dtype,
+                         int64_t rows, int64_t cols, int32_t act, void* h, int64_t ld_h, int32_t out_dtype,
+                         int32_t h_fmt, void* qh, uint8_t* sh, int32_t ckpt_fmt, void* qg, uint8_t* sg, void* qu,
+                         uint8_t* su, void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_shape(src_dtype, rows, cols);
+    if (s != MX_OK) return s;
+    if (!gate || !up) return fail(MX_ERR_INVALID_ARG, "gate and up must not be NULL");
+    if ((s = check_matrix(gate, ld_gate, cols, src_dtype, "gate")) != MX_OK) return s;
+    if ((s = check_matrix(up, ld_up, cols, src_dtype, "up")) != MX_OK) return s;
+    if ((s = check_act(act)) != MX_OK) return s;
+    if (!h && !qh) return fail(MX_ERR_INVALID_ARG, "one of h and qh is needed");
+    if (h) {
+        if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return fail(MX_ERR_INVALID_ARG, "unknown output dtype");
+        if ((s = check_matrix(h, ld_h, cols, out_dtype, "h")) != MX_OK) return s;
+    }
+    if ((s = check_copy(h_fmt, qh, sh, cols)) != MX_OK) return s;
+    if ((s = check_copy(ckpt_fmt, qg, sg, cols)) != MX_OK || (s = check_copy(ckpt_fmt, qu, su, cols)) != MX_OK) return s;
+    if ((qg != nullptr) != (qu != nullptr)) return fail(MX_ERR_INVALID_ARG, "gate and up are checkpointed together");
+    mx::GluFwdJob j{};
+    j.gate = gate; j.ld_gate = ld_gate; j.up = up; j.ld_up = ld_up;
+    j.src = src_dtype; j.rows = rows; j.cols = cols; j.act = act;
+    j.h = h; j.ld_h = ld_h; j.out_f32 = out_dtype == MX_OUT_F32;
+    j.h_fmt = h_fmt; j.qh = (uint8_t*)qh; j.sh = sh;
+    j.ckpt_fmt = ckpt_fmt; j.qg = (uint8_t*)qg; j.sg = sg; j.qu = (uint8_t*)qu; j.su = su;
+    return hip_status(mx::launch_glu_fwd(j, (hipStream_t)stream));
+}
+
+mx_status mx_glu_backward(const void* dh, int64_t ld_dh, int32_t src_dtype, int64_t rows, int64_t cols,
+                          const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t ckpt_fmt,
+                          const void* qg, const uint8_t* sg, const void* qu, const uint8_t* su, int32_t act,
+                          void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup, void* h, int64_t ld_h,
+                          void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_glu_inputs(dh, ld_dh, src_dtype, rows, cols, gate, ld_gate, up, ld_up, ckpt_fmt, qg, sg, qu, su, act);
+    if (s != MX_OK) return s;
+    if (!dgate || !dup) return fail(MX_ERR_INVALID_ARG, "dgate and dup must not be NULL");
+    if ((s = check_matrix(dgate, ld_dgate, cols, src_dtype, "dgate")) != MX_OK) return s;
+    if ((s = check_matrix(dup, ld_dup, cols, src_dtype, "dup")) != MX_OK) return s;
+    if (h && (s = check_matrix(h, ld_h, cols, src_dtype, "h")) != MX_OK) return s;
+    mx::GluBwdJob j = glu_job(dh, ld_dh, src_dtype, rows, cols, gate, ld_gate, up, ld_up, ckpt_fmt, qg, sg, qu, su, act);
+    j.dgate = dgate; j.ld_dgate = ld_dgate; j.dup = dup; j.ld_dup = ld_dup;
+    j.h = h; j.ld_h = ld_h;
+    return hip_status(mx::launch_glu_bwd(j, (hipStream_t)stream));
+}
+
+mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src_dtype, int64_t rows, int64_t cols,
+                                      const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                                      int32_t ckpt_fmt, const void* qg, const uint8_t* sg, const void* qu,
+                                      const uint8_t* su, int32_t act, int32_t fmt, void* q_row, uint8_t* s_row,
+                                      void* q_col, uint8_t* s_col, int32_t h_fmt, void* qh, uint8_t* sh,
+                                      void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_glu_inputs(dh, ld_dh, src_dtype, rows, cols, gate, ld_gate, up, ld_up, ckpt_fmt, qg, sg, qu, su, act);
+    if (s != MX_OK) return s;
+    if (rows % 32 != 0 || cols % 32 != 0) return fail(MX_ERR_INVALID_ARG, "dual layout needs rows % 32 == 0 and cols % 32 == 0");
+    if ((rows + 127) / 128 * ((cols + 31) / 32) >= (int64_t)1 << 31)
+        return fail(MX_ERR_INVALID_ARG, "rows x cols must be fewer than 2^31 tiles of 128 x 32");
+    if (!q_row || !s_row || !q_col || !s_col) return fail(MX_ERR_INVALID_ARG, "an output pointer is NULL");
+    if ((s = check_copy(fmt, q_row, s_row, cols)) != MX_OK || (s = check_copy(fmt, q_col, s_col, cols)) != MX_OK) return s;
+    if ((s = check_copy(h_fmt, qh, sh, cols)) != MX_OK) return s;
+    mx::GluBwdJob j = glu_job(dh, ld_dh, src_dtype, rows, cols, gate, ld_gate, up, ld_up, ckpt_fmt, qg, sg, qu, su, act);
+    j.fmt = fmt; j.q_row = (uint8_t*)q_row; j.s_row = s_row; j.q_col = (uint8_t*)q_col; j.s_col = s_col;
+    j.h_fmt = h_fmt; j.qh = (uint8_t*)qh; j.sh = sh;
+    return hip_status(mx::launch_glu_bwd_dual(j, (hipStream_t)stream));
+}
+
 }  // extern "C"

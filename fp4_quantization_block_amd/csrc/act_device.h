@@ -1,0 +1,259 @@
+// act_device.h -- device helpers shared by the activation operators (norm.hip,
+// glu.hip): elements loaded and stored in chunks of eight per lane, MX row
+// blocks encoded and decoded by the four lanes that hold them, wave and
+// workgroup sums in a fixed order, and the gate functions with their slopes.
+//
+// Chunks.  VEC kernels (row lengths that are a multiple of 8) give a lane
+// eight consecutive elements, 16 bytes of bf16 or 32 of fp32; rows may start
+// at any element, since the loads and stores are declared with the element's
+// alignment and gfx950 takes 16-byte accesses at any of them.  The other
+// kernels give lane t the elements t, t + T, ... t + 7T, so that a wave's
+// 2- or 4-byte accesses are consecutive whatever the row length.
+#pragma once
+#include "mx_device.h"
+
+namespace mx {
+
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+template <int SRC> struct ElemT;
+template <> struct ElemT<SRC_BF16> { typedef uint16_t raw; static constexpr int bytes = 2, dwords = 4; };
+template <> struct ElemT<SRC_F32> { typedef float raw; static constexpr int bytes = 4, dwords = 8; };
+
+// two fp32 values rounded to nearest even, as a bf16 pair
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
+}
+
+// eight consecutive elements as raw dwords (bf16: 4, fp32: 8)
+template <int SRC> struct Chunk { uint32_t w[ElemT<SRC>::dwords]; };
+
+template <int SRC>
+__device__ __forceinline__ Chunk<SRC> load_chunk(const void* base, int64_t elem)
+{
+    Chunk<SRC> c;
+    const typename ElemT<SRC>::raw* p = (const typename ElemT<SRC>::raw*)base + elem;
+    __builtin_memcpy(&c, p, sizeof c);       // 16-byte accesses with the element's alignment
+    return c;
+}
+
+template <int SRC>
+__device__ __forceinline__ float chunk_value(const Chunk<SRC>& c, int i)
+{
+    if constexpr (SRC == SRC_BF16) return (i & 1) ? bf16_hi(c.w[i >> 1]) : bf16_lo(c.w[i >> 1]);
+    else return __uint_as_float(c.w[i]);
+}
+
+template <int SRC>
+__device__ __forceinline__ Chunk<SRC> make_chunk(const float (&v)[8])
+{
+    Chunk<SRC> c;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        if constexpr (SRC == SRC_F32) c.w[i] = __float_as_uint(v[i]);
+        else if ((i & 1) == 0) c.w[i >> 1] = pack_bf16(v[i], v[i + 1]);
+    }
+    return c;
+}
+
+template <int SRC>
+__device__ __forceinline__ void store_chunk(void* base, int64_t elem, const Chunk<SRC>& c)
+{
+    __builtin_memcpy((typename ElemT<SRC>::raw*)base + elem, &c, sizeof c);
+}
+
+// one element
+template <int SRC>
+__device__ __forceinline__ float load_elem(const void* base, int64_t elem)
+{
+    if constexpr (SRC == SRC_BF16) return __uint_as_float((uint32_t)((const uint16_t*)base)[elem] << 16);
+    else return ((const float*)base)[elem];
+}
+
+template <int SRC>
+__device__ __forceinline__ void store_elem(void* base, int64_t elem, float v)
+{
+    if constexpr (SRC == SRC_BF16) ((uint16_t*)base)[elem] = (uint16_t)pack_bf16(v, v);
+    else ((float*)base)[elem] = v;
+}
+
+// a value rounded to the element type
+template <int SRC>
+__device__ __forceinline__ float rounded(float v)
+{
+    if constexpr (SRC == SRC_BF16) return bf16_lo(pack_bf16(v, v));
+    else return v;
+}
+
+// ---------------------------------------------------------------------
+// Sums.  The order is fixed by the lane and wave numbers, so a result does
+// not change from run to run.  All lanes of the wave take part.
+// ---------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+enum : int { DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_HALF_MIRROR = 0x141, DPP_MIRROR = 0x140,
+             DPP_BCAST15 = 0x142, DPP_BCAST31 = 0x143 };
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) { return v + __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add_rows(float v)
+{
+    return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = dpp_add<DPP_XOR1>(v);
+    v = dpp_add<DPP_XOR2>(v);
+    v = dpp_add<DPP_HALF_MIRROR>(v);
+    v = dpp_add<DPP_MIRROR>(v);
+    v = dpp_add_rows<DPP_BCAST15, 0xA>(v);     // rows 1 and 3 of 16 lanes take rows 0 and 2
+    v = dpp_add_rows<DPP_BCAST31, 0xC>(v);     // rows 2 and 3 take lane 31: lane 63 has all
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// the sum over T lanes (a wave, or a workgroup of T / 64 waves through `red`,
+// T / 64 floats of LDS that no other sum uses before the next barrier)
+template <int T>
+__device__ __forceinline__ float group_sum(float v, float* red)
+{
+    v = wave_sum(v);
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int i = 1; i < T / 64; i++) v += red[i];
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------
+// MX row blocks of 32, eight elements in each of four consecutive lanes
+// ---------------------------------------------------------------------
+__device__ __forceinline__ uint32_t chunk_key(const float (&v)[8])
+{
+    uint32_t k = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) k = max(k, abs_key(v[i]));
+    return k;
+}
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t k)
+{
+    k = max(k, dpp<DPP_XOR1>(k));
+    return max(k, dpp<DPP_XOR2>(k));
+}
+
+struct Codes8 { uint32_t lo, hi, scale; };
+
+// eight values of a block whose |max| key is `key`: codes and scale byte as
+// mx_quantize writes them (round to nearest even, saturating; a block with a
+// NaN or an Inf: 0x7F everywhere and byte 0xFF)
+template <int FMT>
+__device__ __forceinline__ Codes8 encode8(const float (&v)[8], uint32_t key)
+{
+    const int e = block_exponent<FMT>(key);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[i] = clamp_fmax<FMT>(scale_by(v[i], e));
+    const bool bad = key >= 0x7F800000u;
+    return Codes8{bad ? 0x7F7F7F7Fu : cvt4_fp8<FMT>(y[0], y[1], y[2], y[3]),
+                  bad ? 0x7F7F7F7Fu : cvt4_fp8<FMT>(y[4], y[5], y[6], y[7]), bad ? 0xFFu : (uint32_t)(e + 127)};
+}
+
+__device__ __forceinline__ Codes8 encode8(int fmt, const float (&v)[8], uint32_t key)
+{
+    return fmt == E4M3 ? encode8<E4M3>(v, key) : encode8<E5M2>(v, key);
+}
+
+// the four lanes' part of one block of a row copy: codes of elements elem ..
+// elem + 7 (row-major, dense) and the block's scale byte.  `valid` is the
+// same for the four lanes.
+__device__ __forceinline__ void encode_row_chunk(int fmt, const float (&v)[8], bool valid, int64_t elem, uint8_t* q,
+                                                 uint8_t* s)
+{
+    const Codes8 c = encode8(fmt, v, quad_max(chunk_key(v)));
+    if (valid) {
+        *(uint2*)(q + elem) = make_uint2(c.lo, c.hi);
+        if ((threadIdx.x & 3) == 0) s[elem >> 5] = (uint8_t)c.scale;
+    }
+}
+
+// 2^(byte - 127) as mx_dequantize takes it: byte 0 is 2^-127 (an fp32
+// subnormal), byte 255 is NaN
+__device__ __forceinline__ float scale_value(uint32_t byte)
+{
+    const uint32_t bits = byte == 0xFFu ? 0x7FC00000u : byte << 23;
+    return __uint_as_float(byte == 0 ? 0x00400000u : bits);
+}
+
+// eight checkpointed values: codes lo, hi and the block's scale byte
+__device__ __forceinline__ void decode8(int fmt, uint2 c, uint32_t byte, float (&v)[8])
+{
+    const float s = scale_value(byte);
+    f32x2_t p[4];
+    if (fmt == E4M3) {
+        p[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
+        p[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+        p[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
+        p[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+    } else {
+        p[0] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.x, false);
+        p[1] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.x, true);
+        p[2] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.y, false);
+        p[3] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.y, true);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = p[i >> 1][i & 1] * s;
+}
+
+// ---------------------------------------------------------------------
+// Gate functions a = act(x) and their slopes d = act'(x).
+//   SILU       a = x s,  s = 1 / (1 + e^-x);  d = s + a (1 - s)
+//   GELU       a = x P(x), P the normal distribution function;
+//              d = P(x) + x e^(-x^2/2) / sqrt(2 pi)
+//   GELU_TANH  x/2 (1 + tanh z) with z = sqrt(2/pi) (x + 0.044715 x^3).
+//              (1 + tanh z) / 2 = 1 / (1 + e^-2z) = s, so a = x s and
+//              d = s + a (1 - s) z2',  z2' = 2 dz/dx
+// Exponentials are the hardware's base-2 one, divisions its reciprocal, each
+// within 1 ulp; the product with log2 e is rounded once, so e^-x is off by a
+// relative |x| 2^-24 more.  e^-x overflows to Inf for x < -88 and s becomes 0.
+// ---------------------------------------------------------------------
+enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
+
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ void gate(float x, float& a, float& d)
+{
+    constexpr float LOG2E = 1.44269504f;
+    if constexpr (ACT == ACT_SILU) {
+        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * x));
+        a = x * s;
+        if constexpr (SLOPE) d = __builtin_fmaf(a, 1.0f - s, s);
+    } else if constexpr (ACT == ACT_GELU) {
+        const float p = 0.5f * erfcf(-0.70710678f * x);
+        a = x * p;
+        if constexpr (SLOPE) {
+            const float e = __builtin_amdgcn_exp2f((-0.5f * LOG2E) * x * x);
+            d = __builtin_fmaf(0.39894228f * x, e, p);
+        }
+    } else {
+        // x^2 is held below 2^40, where s is 0 or 1 for long: no overflow to
+        // Inf, which the vanishing 1 - s would turn into NaN
+        constexpr float Z = 1.59576912f, C = 0.044715f;            // 2 sqrt(2/pi)
+        const float x2 = fminf(x * x, 0x1p40f);
+        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * __builtin_fmaf(-LOG2E * Z * C, x2, -LOG2E * Z)));
+        a = x * s;
+        if constexpr (SLOPE) d = __builtin_fmaf(a * (1.0f - s), __builtin_fmaf(3.0f * Z * C, x2, Z), s);
+    }
+}
+
+}  // namespace mx

@@ -90,4 +90,70 @@ hipError_t launch_gemm(const GemmJob& j, hipStream_t stream);
 // codes, 4-byte aligned scale arrays
 bool gemm_w4_eligible(const GemmJob& j);
 
+// norm forward: s = x (+ residual, rounded; written to sum), its statistics,
+// y and / or the row copy of y, and the checkpoint (row copy) of s
+struct NormFwdJob {
+    const void* x; int64_t ld_x;
+    const void* residual; int64_t ld_res;   // nullptr: none (sum is then unused)
+    int src;                // SRC_F32 / SRC_BF16: x, residual, sum
+    int64_t rows, cols;
+    bool layer;             // layer norm; otherwise RMS norm
+    const void* weight; const void* bias; bool param_f32;   // nullptr: 1 / 0
+    float eps;
+    void* sum; int64_t ld_sum;
+    void* y; int64_t ld_y; bool out_f32;    // nullptr: not written
+    int y_fmt; uint8_t* qy; uint8_t* sy;    // row copy of y (nullptr: not written)
+    int ckpt_fmt; uint8_t* qx; uint8_t* sx; // checkpoint (nullptr: not written)
+    float* mean; float* rstd;               // nullptr: not written
+};
+
+hipError_t launch_norm_fwd(const NormFwdJob& j, hipStream_t stream);
+
+struct NormBwdJob {
+    const void* dy; int64_t ld_dy;
+    int src;                // dy, x, dsum, dx
+    int64_t rows, cols;
+    const void* x; int64_t ld_x;            // or, with qx, the checkpoint
+    int ckpt_fmt; const uint8_t* qx; const uint8_t* sx;
+    const float* mean; const float* rstd;
+    bool layer;
+    const void* weight; bool param_f32;
+    const void* dsum; int64_t ld_dsum;      // nullptr: none
+    void* dx; int64_t ld_dx;
+    float* dweight; float* dbias;           // nullptr: not wanted
+    float* work;            // partial rows of dweight, then of dbias
+};
+
+// partial rows that launch_norm_bwd writes, at most, for each of dweight and dbias
+int64_t norm_bwd_partials(int64_t rows, int64_t cols);
+hipError_t launch_norm_bwd(const NormBwdJob& j, hipStream_t stream);
+
+// gated activation h = act(gate) * up
+struct GluFwdJob {
+    const void* gate; int64_t ld_gate; const void* up; int64_t ld_up;
+    int src; int64_t rows, cols; int act;
+    void* h; int64_t ld_h; bool out_f32;    // nullptr: not written
+    int h_fmt; uint8_t* qh; uint8_t* sh;    // row copy of h (nullptr: not written)
+    int ckpt_fmt; uint8_t* qg; uint8_t* sg; uint8_t* qu; uint8_t* su;   // checkpoints (nullptr: not written)
+};
+
+hipError_t launch_glu_fwd(const GluFwdJob& j, hipStream_t stream);
+
+// its gradients; gate and up from tensors or (qg) from checkpoints
+struct GluBwdJob {
+    const void* dh; int64_t ld_dh;
+    int src; int64_t rows, cols; int act;
+    const void* gate; int64_t ld_gate; const void* up; int64_t ld_up;
+    int ckpt_fmt; const uint8_t* qg; const uint8_t* sg; const uint8_t* qu; const uint8_t* su;
+    void* dgate; int64_t ld_dgate; void* dup; int64_t ld_dup;
+    void* h; int64_t ld_h;                  // nullptr: not recomputed
+    // the dual-layout form: row copy [rows][2 cols] and column copy
+    // [2 cols][rows] of [dgate | dup], column copy [cols][rows] of h
+    int fmt; uint8_t* q_row; uint8_t* s_row; uint8_t* q_col; uint8_t* s_col;
+    int h_fmt; uint8_t* qh; uint8_t* sh;    // nullptr: not written
+};
+
+hipError_t launch_glu_bwd(const GluBwdJob& j, hipStream_t stream);
+hipError_t launch_glu_bwd_dual(const GluBwdJob& j, hipStream_t stream);
+
 }  // namespace mx

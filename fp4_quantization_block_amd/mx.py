@@ -7,7 +7,7 @@ immediately; there is no fallback implementation.
 """
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -22,13 +22,19 @@ MX_TSCALE_COMPUTE, MX_TSCALE_PROVIDED = 0, 1
 MX_RNE, MX_SR = 0, 1
 MX_AXIS_ROW, MX_AXIS_COL = 0, 1
 MX_OUT_F32, MX_OUT_BF16 = 0, 1
+MX_NORM_LAYER, MX_NORM_RMS = 0, 1
+MX_ACT_SILU, MX_ACT_GELU, MX_ACT_GELU_TANH = 0, 1, 2
 
 FMTS = {"e4m3": MX_E4M3, "e5m2": MX_E5M2, "e2m1": MX_E2M1}
+NORMS = {"layer": MX_NORM_LAYER, "rms": MX_NORM_RMS}
+ACTS = {"silu": MX_ACT_SILU, "gelu": MX_ACT_GELU, "gelu_tanh": MX_ACT_GELU_TANH}
 EXPORTED = ("mx_quantize", "mx_quantize_dual_layout", "mx_gemm", "mx_dequantize",
             "mx_status_string", "mx_last_error_message",
             "mx_predict_tensor_scale", "mx_predict_workspace_bytes", "mx_gemm_quantized",
             "mx_predict_tensor_scale_noalloc", "mx_quantize_optstate", "mx_dequantize_optstate",
-            "mx_quantize_nvfp", "mx_dequantize_nvfp", "mx_gemm_nvfp")
+            "mx_quantize_nvfp", "mx_dequantize_nvfp", "mx_gemm_nvfp",
+            "mx_norm_forward", "mx_norm_backward", "mx_norm_backward_workspace_bytes",
+            "mx_glu_forward", "mx_glu_backward", "mx_glu_backward_dual_layout")
 NV_PANEL = 32                      # stored rows per CTA-local nvfp scale domain
 
 
@@ -90,6 +96,23 @@ def load() -> ctypes.CDLL:
     L.mx_gemm_nvfp.restype = _i32
     L.mx_gemm_nvfp.argtypes = [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64, _i64, ctypes.c_float,
                                _vp, _i32, _i64, _vp]
+    L.mx_norm_forward.restype = _i32
+    L.mx_norm_forward.argtypes = [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i32, _vp, _vp, _i32, ctypes.c_float,
+                                  _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]
+    L.mx_norm_backward.restype = _i32
+    L.mx_norm_backward.argtypes = [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp,
+                                   _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]
+    L.mx_norm_backward_workspace_bytes.restype = _i64
+    L.mx_norm_backward_workspace_bytes.argtypes = [_i64, _i64]
+    L.mx_glu_forward.restype = _i32
+    L.mx_glu_forward.argtypes = [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _vp,
+                                 _i32, _vp, _vp, _vp, _vp, _vp]
+    L.mx_glu_backward.restype = _i32
+    L.mx_glu_backward.argtypes = [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp,
+                                  _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+    L.mx_glu_backward_dual_layout.restype = _i32
+    L.mx_glu_backward_dual_layout.argtypes = [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp,
+                                              _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
     L.mx_predict_workspace_bytes.restype = _i64
     L.mx_predict_workspace_bytes.argtypes = []
     L.mx_status_string.restype = ctypes.c_char_p
@@ -331,3 +354,272 @@ def mx_gemm_nvfp(qa, sa, ta, local_a: bool, qb, sb, tb, local_b: bool, M: int, N
     _check(load().mx_gemm_nvfp(_ptr(qa), _ptr(sa), _ptr(ta), int(bool(local_a)), _ptr(qb), _ptr(sb), _ptr(tb),
                                int(bool(local_b)), M, N, K, float(alpha), _ptr(c), out_dtype, ldc, _stream(stream)))
     return c
+
+
+# ---------------------------------------------------------------------------
+# activation operators (norm, gated activation) with 8-bit checkpoints
+# ---------------------------------------------------------------------------
+class Checkpoint(NamedTuple):
+    """An MX row copy kept for the backward pass: element format, codes
+    [rows][cols] and scale bytes [rows][cols / 32] (uint8, dense)."""
+    fmt: int
+    q: torch.Tensor
+    s: torch.Tensor
+
+
+class NormForward(NamedTuple):
+    y: Optional[torch.Tensor]
+    sum: Optional[torch.Tensor]
+    qy: Optional[torch.Tensor]
+    sy: Optional[torch.Tensor]
+    qx: Optional[torch.Tensor]
+    sx: Optional[torch.Tensor]
+    mean: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+
+
+class NormBackward(NamedTuple):
+    dx: torch.Tensor
+    dweight: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+
+
+class GluForward(NamedTuple):
+    h: Optional[torch.Tensor]
+    qh: Optional[torch.Tensor]
+    sh: Optional[torch.Tensor]
+    qg: Optional[torch.Tensor]
+    sg: Optional[torch.Tensor]
+    qu: Optional[torch.Tensor]
+    su: Optional[torch.Tensor]
+
+
+class GluBackward(NamedTuple):
+    dgate: torch.Tensor
+    dup: torch.Tensor
+    h: Optional[torch.Tensor]
+
+
+class GluBackwardDual(NamedTuple):
+    q_row: torch.Tensor
+    s_row: torch.Tensor
+    q_col: torch.Tensor
+    s_col: torch.Tensor
+    qh_col: Optional[torch.Tensor]
+    sh_col: Optional[torch.Tensor]
+
+
+def checkpoint(fmt, q: torch.Tensor, s: torch.Tensor) -> Checkpoint:
+    """Codes and scales as mx_quantize (MX_AXIS_ROW) or a forward call wrote them."""
+    return Checkpoint(_fmt(fmt), q, s)
+
+
+def _fits(t: torch.Tensor, shape, dtype, name: str, dense: bool = False) -> torch.Tensor:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if not (t.is_contiguous() if dense else t.shape[-1] <= 1 or t.stride(-1) == 1):
+        raise ValueError(f"{name} must be contiguous" if dense else f"{name} must have unit column stride")
+    return t
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _ld(t: Optional[torch.Tensor]) -> int:
+    """Row stride in elements (that of a single row is its length)."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _out(t, shape, dtype, device, name: str, dense: bool = True) -> torch.Tensor:
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _fits(t, shape, dtype, name, dense)
+
+
+def _copy_out(fmt, q, s, shape, device, name: str):
+    """(format, codes, scales) of a row copy to be written; (0, None, None) without a format."""
+    if fmt is None:
+        if q is not None or s is not None:
+            raise ValueError(f"{name} needs a format")
+        return 0, None, None
+    rows, cols = shape
+    return (_fmt(fmt), _out(q, shape, torch.uint8, device, f"{name} codes"),
+            _out(s, (rows, cols // 32), torch.uint8, device, f"{name} scales"))
+
+
+def _copy_in(c: Optional[Checkpoint], shape, name: str):
+    if c is None:
+        return 0, None, None
+    rows, cols = shape
+    return (c.fmt, _fits(c.q, shape, torch.uint8, f"{name} codes", True),
+            _fits(c.s, (rows, cols // 32), torch.uint8, f"{name} scales", True))
+
+
+def _matrix(x: torch.Tensor, name: str) -> int:
+    """Source dtype code of a 2-D operand."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
+    if x.dtype == torch.bfloat16:
+        return MX_SRC_BF16
+    if x.dtype == torch.float32:
+        return MX_SRC_F32
+    raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _params(weight, bias, cols: int) -> int:
+    """Common dtype code of the parameters."""
+    given = [p for p in (weight, bias) if p is not None]
+    if not given:
+        return 0
+    dtype = given[0].dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("weight and bias must be float32 or bfloat16")
+    for p in given:
+        _fits(p, (cols,), dtype, "weight and bias", True)
+    return MX_SRC_F32 if dtype == torch.float32 else MX_SRC_BF16
+
+
+def mx_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                    eps: float = 1e-5, kind: str = "rms", residual: Optional[torch.Tensor] = None,
+                    write_y: bool = True, out_dtype: Optional[torch.dtype] = None, y_fmt=None, ckpt_fmt=None,
+                    stats: bool = True, sum_out=None, y=None, qy=None, sy=None, qx=None, sx=None, mean=None,
+                    rstd=None, stream=None) -> NormForward:
+    """RMS norm or layer norm of x (+ residual), with y as a tensor, as an MX
+    row copy (y_fmt) or both, and the 8-bit checkpoint (ckpt_fmt) of what was
+    normalised.  stats: also mean (layer norm) and rstd for the backward."""
+    src = _matrix(x, "x")
+    shape, dev, k = x.shape, x.device, NORMS[kind]
+    if residual is not None:
+        _fits(residual, shape, x.dtype, "residual")
+        sum_out = _out(sum_out, shape, x.dtype, dev, "sum_out", False)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    y = _out(y, shape, out_dtype, dev, "y", False) if write_y else None
+    yf, qy, sy = _copy_out(y_fmt, qy, sy, shape, dev, "y")
+    cf, qx, sx = _copy_out(ckpt_fmt, qx, sx, shape, dev, "checkpoint")
+    if stats:
+        rstd = _out(rstd, shape[:1], torch.float32, dev, "rstd")
+        mean = _out(mean, shape[:1], torch.float32, dev, "mean") if k == MX_NORM_LAYER else None
+    else:
+        mean = rstd = None
+    _check(load().mx_norm_forward(
+        _at(x), _ld(x), _at(residual), _ld(residual), src, shape[0], shape[1], k, _at(weight), _at(bias),
+        _params(weight, bias, shape[1]), eps, _at(sum_out), _ld(sum_out), _at(y), _ld(y),
+        MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, yf, _at(qy), _at(sy), cf, _at(qx), _at(sx),
+        _at(mean), _at(rstd), _stream(stream)))
+    return NormForward(y, sum_out, qy, sy, qx, sx, mean, rstd)
+
+
+def mx_norm_backward(dy: torch.Tensor, rstd: torch.Tensor, x: Optional[torch.Tensor] = None,
+                     ckpt: Optional[Checkpoint] = None, mean: Optional[torch.Tensor] = None,
+                     weight: Optional[torch.Tensor] = None, kind: str = "rms",
+                     dsum: Optional[torch.Tensor] = None, want_dweight: bool = True, want_dbias: bool = False,
+                     dx=None, dweight=None, dbias=None, work=None, stream=None) -> NormBackward:
+    """Gradients of mx_norm_forward from what it normalised (x) or from its
+    checkpoint; dsum is a gradient of the same tensor from elsewhere, added
+    to dx.  dweight and dbias are float32."""
+    src = _matrix(dy, "dy")
+    shape, dev, k = dy.shape, dy.device, NORMS[kind]
+    if x is not None:
+        _fits(x, shape, dy.dtype, "x")
+    cf, qx, sx = _copy_in(ckpt, shape, "checkpoint")
+    _fits(rstd, shape[:1], torch.float32, "rstd", True)
+    if k == MX_NORM_LAYER and mean is not None:
+        _fits(mean, shape[:1], torch.float32, "mean", True)
+    if dsum is not None:
+        _fits(dsum, shape, dy.dtype, "dsum")
+    dx = _out(dx, shape, dy.dtype, dev, "dx", False)
+    dweight = _out(dweight, shape[1:], torch.float32, dev, "dweight") if want_dweight else None
+    dbias = _out(dbias, shape[1:], torch.float32, dev, "dbias") if want_dbias else None
+    L, nbytes = load(), 0
+    if want_dweight or want_dbias:
+        if work is None:
+            nbytes = int(L.mx_norm_backward_workspace_bytes(shape[0], shape[1]))
+            work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:
+            nbytes = work.numel() * work.element_size()
+    _check(L.mx_norm_backward(
+        _at(dy), _ld(dy), src, shape[0], shape[1], _at(x), _ld(x), cf, _at(qx), _at(sx), _at(mean), _at(rstd), k,
+        _at(weight), _params(weight, None, shape[1]), _at(dsum), _ld(dsum), _at(dx), _ld(dx), _at(dweight),
+        _at(dbias), _at(work), nbytes, _stream(stream)))
+    return NormBackward(dx, dweight, dbias)
+
+
+def mx_glu_forward(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", write_h: bool = True,
+                   out_dtype: Optional[torch.dtype] = None, h_fmt=None, ckpt_fmt=None, h=None, qh=None, sh=None,
+                   qg=None, sg=None, qu=None, su=None, stream=None) -> GluForward:
+    """h = act(gate) * up as a tensor, as an MX row copy (h_fmt) or both, and
+    the 8-bit checkpoints (ckpt_fmt) of gate and up."""
+    src = _matrix(gate, "gate")
+    shape, dev = gate.shape, gate.device
+    _fits(up, shape, gate.dtype, "up")
+    out_dtype = gate.dtype if out_dtype is None else out_dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    h = _out(h, shape, out_dtype, dev, "h", False) if write_h else None
+    hf, qh, sh = _copy_out(h_fmt, qh, sh, shape, dev, "h")
+    cf, qg, sg = _copy_out(ckpt_fmt, qg, sg, shape, dev, "gate checkpoint")
+    _, qu, su = _copy_out(ckpt_fmt, qu, su, shape, dev, "up checkpoint")
+    _check(load().mx_glu_forward(
+        _at(gate), _ld(gate), _at(up), _ld(up), src, shape[0], shape[1], ACTS[act], _at(h), _ld(h),
+        MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, hf, _at(qh), _at(sh), cf, _at(qg), _at(sg),
+        _at(qu), _at(su), _stream(stream)))
+    return GluForward(h, qh, sh, qg, sg, qu, su)
+
+
+def _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act):
+    """The shared leading arguments of the backward calls."""
+    src = _matrix(dh, "dh")
+    shape = dh.shape
+    if gate is not None:
+        _fits(gate, shape, dh.dtype, "gate")
+    if up is not None:
+        _fits(up, shape, dh.dtype, "up")
+    gf, qg, sg = _copy_in(gate_ckpt, shape, "gate checkpoint")
+    uf, qu, su = _copy_in(up_ckpt, shape, "up checkpoint")
+    if gate_ckpt is not None and up_ckpt is not None and gf != uf:
+        raise ValueError("the checkpoints of gate and up must have one format")
+    return (_at(dh), _ld(dh), src, shape[0], shape[1], _at(gate), _ld(gate), _at(up), _ld(up), gf, _at(qg),
+            _at(sg), _at(qu), _at(su), ACTS[act])
+
+
+def mx_glu_backward(dh: torch.Tensor, gate: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None,
+                    act: str = "silu", gate_ckpt: Optional[Checkpoint] = None,
+                    up_ckpt: Optional[Checkpoint] = None, recompute_h: bool = False, dgate=None, dup=None, h=None,
+                    stream=None) -> GluBackward:
+    """Gradients of mx_glu_forward from gate and up, or from their
+    checkpoints; recompute_h: also h = act(gate) * up."""
+    head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
+    shape, dev = dh.shape, dh.device
+    dgate = _out(dgate, shape, dh.dtype, dev, "dgate", False)
+    dup = _out(dup, shape, dh.dtype, dev, "dup", False)
+    h = _out(h, shape, dh.dtype, dev, "h", False) if recompute_h else None
+    _check(load().mx_glu_backward(*head, _at(dgate), _ld(dgate), _at(dup), _ld(dup), _at(h), _ld(h),
+                                  _stream(stream)))
+    return GluBackward(dgate, dup, h)
+
+
+def mx_glu_backward_dual_layout(dh: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                                up: Optional[torch.Tensor] = None, act: str = "silu",
+                                gate_ckpt: Optional[Checkpoint] = None, up_ckpt: Optional[Checkpoint] = None,
+                                fmt="e5m2", h_fmt=None, q_row=None, s_row=None, q_col=None, s_col=None,
+                                qh_col=None, sh_col=None, stream=None) -> GluBackwardDual:
+    """mx_glu_backward straight into the backward GEMMs' operands: the row and
+    column copies of [dgate | dup] and (h_fmt) the column copy of h."""
+    head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
+    (rows, cols), dev = dh.shape, dh.device
+    f, q_row, s_row = _copy_out(fmt, q_row, s_row, (rows, 2 * cols), dev, "row copy")
+    _, q_col, s_col = _copy_out(fmt, q_col, s_col, (2 * cols, rows), dev, "column copy")
+    hf, qh_col, sh_col = _copy_out(h_fmt, qh_col, sh_col, (cols, rows), dev, "column copy of h")
+    _check(load().mx_glu_backward_dual_layout(*head, f, _at(q_row), _at(s_row), _at(q_col), _at(s_col), hf,
+                                              _at(qh_col), _at(sh_col), _stream(stream)))
+    return GluBackwardDual(q_row, s_row, q_col, s_col, qh_col, sh_col)

@@ -7,7 +7,8 @@
  *          (blog.zhiliyouxian.com)
  *   [FAF]  "格式感知融合:让FP4预训练提速两倍的工程实践" (kongchang.com)
  *   [COAT] write-up of "COAT: Compressing Optimizer States and Activation
- *          for memory efficient FP8 Training" (dignews.cc)
+ *          for memory efficient FP8 Training" (dignews.cc): optimizer
+ *          states and activation checkpoints in 8 bits
  *   Element encodings and the shared-exponent rule: OCP Microscaling (MX)
  *   Formats specification v1.0.
  *
@@ -73,8 +74,15 @@ enum { MX_RNE = 0, MX_SR = 1 };
  * the low nibble of byte j.  Stored rows are dense (no padding). */
 enum { MX_AXIS_ROW = 0, MX_AXIS_COL = 1 };
 
-/* output dtype of mx_gemm / mx_dequantize */
+/* output dtype of mx_gemm / mx_dequantize and of the activation operators */
 enum { MX_OUT_F32 = 0, MX_OUT_BF16 = 1 };
+
+/* mx_norm_forward / mx_norm_backward: layer norm (mean and variance) or RMS
+ * norm (mean square) */
+enum { MX_NORM_LAYER = 0, MX_NORM_RMS = 1 };
+
+/* mx_glu_*: the gate function */
+enum { MX_ACT_SILU = 0, MX_ACT_GELU = 1, MX_ACT_GELU_TANH = 2 };
 
 typedef struct {
     int32_t fmt;        /* MX_E4M3 / MX_E5M2 / MX_E2M1 */
@@ -374,6 +382,136 @@ mx_status mx_gemm_nvfp(const uint8_t* qa, const uint8_t* sa, const float* ta, in
                        const uint8_t* qb, const uint8_t* sb, const float* tb, int32_t local_b,
                        int64_t M, int64_t N, int64_t K, float alpha, void* c, int32_t out_dtype,
                        int64_t ldc, void* stream);
+
+/*
+ * Activation operators: what stands between the GEMMs of a pre-norm gated
+ * MLP block, with its activations kept for the backward pass in 8 bits
+ * ([COAT, "FP8啟用"]: the inputs of non-linear layers are stored as FP8 in
+ * per-group scaled form; the group here is the MX block).
+ *
+ * An activation checkpoint of a rows x cols tensor is its row copy exactly
+ * as mx_quantize writes it with MX_AXIS_ROW, MX_SCALE_E8M0 and MX_RNE: codes
+ * [rows][cols] and scale bytes [rows][cols / 32], MX_E4M3 or MX_E5M2 (MX_E2M1
+ * is MX_ERR_UNSUPPORTED).  A backward call that takes one reads the value
+ * decode(code) * 2^(byte - 127) in place of the element.  The quantized
+ * outputs below encode the fp32 value in the same way.
+ *
+ * Common to these calls: matrices are rows x cols with a row stride of ld_*
+ * >= cols elements, of fp32 or bf16 and aligned to their element size; any
+ * cols >= 1, odd ones too, unless a checkpoint or quantized output is taken,
+ * which needs cols % 32 == 0 and a 16-byte aligned code array.  0 < rows,
+ * cols < 2^31.  Arithmetic is fp32, each output rounded once (to nearest
+ * even); sums are in an order fixed by the shape, with no atomics, so results
+ * repeat bit for bit.  NaN and Inf follow the formulas.  Outputs must not
+ * overlap inputs or each other, except where said.  Errors as mx_quantize.
+ */
+
+/*
+ * mx_norm_forward -- layer norm or RMS norm of each row:
+ *   s = x, or x + residual rounded to the source type (written to `sum`);
+ *   mu = mean(s) (MX_NORM_RMS: 0);  r = 1 / sqrt(mean((s - mu)^2) + eps);
+ *   y = (s - mu) * r * weight + bias.
+ * x, residual, sum: `src_dtype`.  residual NULL: s = x, and sum must be NULL.
+ *        sum may be x or residual themselves (same pointer and stride).
+ * weight, bias: cols values of `param_dtype` (MX_SRC_F32 / MX_SRC_BF16), or
+ *        NULL (1 and 0; param_dtype is then ignored).
+ * eps:   finite, >= 0.
+ * y:     `out_dtype` matrix, or NULL.   qy, sy: y as a row copy of format
+ *        y_fmt (the next GEMM's A operand), or both NULL.  At least one of y
+ *        and qy.
+ * qx, sx: checkpoint of s in ckpt_fmt, or both NULL.
+ * mean, rstd: rows fp32 each, mu and r for the backward pass, or NULL; mean
+ *        is not written for MX_NORM_RMS.
+ */
+mx_status mx_norm_forward(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, int32_t src_dtype,
+                          int64_t rows, int64_t cols, int32_t kind, const void* weight, const void* bias,
+                          int32_t param_dtype, float eps, void* sum, int64_t ld_sum, void* y, int64_t ld_y,
+                          int32_t out_dtype, int32_t y_fmt, void* qy, uint8_t* sy, int32_t ckpt_fmt, void* qx,
+                          uint8_t* sx, float* mean, float* rstd, void* stream);
+
+/*
+ * mx_norm_backward -- gradients of mx_norm_forward:
+ *   h = (s - mu) * r,  g = dy * weight,
+ *   dx = r * (g - mean(g) - h * mean(g * h)) + dsum   (MX_NORM_RMS: no mean(g)),
+ *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy.
+ * dx is the gradient of s: of x, and of residual.
+ * dy, dx, dsum: `src_dtype`.
+ * x:     what was normalised (s), `src_dtype`; or NULL and its checkpoint qx,
+ *        sx in ckpt_fmt.  One of the two.
+ * mean, rstd: rows fp32 each, as mx_norm_forward wrote them; mean is ignored
+ *        for MX_NORM_RMS.
+ * weight, param_dtype: as in the forward call.
+ * dsum:  a gradient of s from elsewhere (the residual path), or NULL.  dx may
+ *        be dsum or dy themselves (same pointer and stride) for cols <= 16384.
+ * dweight, dbias: cols fp32 each, or NULL.
+ * work:  at least mx_norm_backward_workspace_bytes(rows, cols) bytes, 4-byte
+ *        aligned, for the partial sums of dweight and dbias (may be NULL if
+ *        neither is wanted); contents undefined afterwards.
+ */
+mx_status mx_norm_backward(const void* dy, int64_t ld_dy, int32_t src_dtype, int64_t rows, int64_t cols,
+                           const void* x, int64_t ld_x, int32_t ckpt_fmt, const void* qx, const uint8_t* sx,
+                           const float* mean, const float* rstd, int32_t kind, const void* weight,
+                           int32_t param_dtype, const void* dsum, int64_t ld_dsum, void* dx, int64_t ld_dx,
+                           float* dweight, float* dbias, void* work, int64_t work_bytes, void* stream);
+
+/* Bytes of workspace mx_norm_backward needs for both dweight and dbias (0
+ * for a shape it refuses). */
+int64_t mx_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * mx_glu_forward -- the gated activation h = act(gate) * up:
+ *   MX_ACT_SILU       act(g) = g / (1 + e^-g)
+ *   MX_ACT_GELU       act(g) = g * P(g), P the normal distribution function
+ *   MX_ACT_GELU_TANH  act(g) = g/2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
+ * gate, up: `src_dtype`, strides of their own (e.g. the halves of one fused
+ *        projection's output).
+ * h:     `out_dtype` matrix, or NULL.   qh, sh: h as a row copy of format
+ *        h_fmt (the down projection's A operand), or both NULL.  At least
+ *        one of h and qh.
+ * qg, sg, qu, su: checkpoints of gate and up in ckpt_fmt; all four or none.
+ */
+mx_status mx_glu_forward(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t src_dtype,
+                         int64_t rows, int64_t cols, int32_t act, void* h, int64_t ld_h, int32_t out_dtype,
+                         int32_t h_fmt, void* qh, uint8_t* sh, int32_t ckpt_fmt, void* qg, uint8_t* sg, void* qu,
+                         uint8_t* su, void* stream);
+
+/*
+ * mx_glu_backward -- gradients of mx_glu_forward:
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate),
+ * and, if h is not NULL, h = act(gate) * up again.
+ * dh, dgate, dup, h: `src_dtype`.
+ * gate, up: `src_dtype`; or both NULL and their checkpoints qg, sg, qu, su in
+ *        ckpt_fmt.  dgate and dup may be gate and up themselves (same pointer
+ *        and stride), dgate or dup may be dh.
+ */
+mx_status mx_glu_backward(const void* dh, int64_t ld_dh, int32_t src_dtype, int64_t rows, int64_t cols,
+                          const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t ckpt_fmt,
+                          const void* qg, const uint8_t* sg, const void* qu, const uint8_t* su, int32_t act,
+                          void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup, void* h, int64_t ld_h,
+                          void* stream);
+
+/*
+ * mx_glu_backward_dual_layout -- mx_glu_backward whose gradients are written
+ * as the operands of the backward GEMMs ([FAF, "格式感知融合的设计思路"]),
+ * with D = [dgate | dup], rows x 2 cols:
+ *   q_row, s_row: row copy of D (dgrad's A): codes [rows][2 cols], scales
+ *        [rows][2 cols / 32];
+ *   q_col, s_col: column copy of D (wgrad): codes [2 cols][rows], scales
+ *        [2 cols][rows / 32];
+ *   qh, sh: column copy of the recomputed h (the down projection's wgrad):
+ *        codes [cols][rows], scales [cols][rows / 32], format h_fmt; or both
+ *        NULL.
+ * Each block encodes the fp32 values that mx_glu_backward rounds, as
+ * mx_quantize_dual_layout does with MX_SCALE_E8M0 and MX_RNE.
+ * fmt, h_fmt: MX_E4M3 or MX_E5M2.  Needs rows % 32 == 0 and cols % 32 == 0.
+ * Inputs as mx_glu_backward.
+ */
+mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src_dtype, int64_t rows, int64_t cols,
+                                      const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                                      int32_t ckpt_fmt, const void* qg, const uint8_t* sg, const void* qu,
+                                      const uint8_t* su, int32_t act, int32_t fmt, void* q_row, uint8_t* s_row,
+                                      void* q_col, uint8_t* s_col, int32_t h_fmt, void* qh, uint8_t* sh,
+                                      void* stream);
 
 /* Static text for a status code. */
 const char* mx_status_string(mx_status status);
