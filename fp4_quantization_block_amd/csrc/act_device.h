@@ -18,8 +18,8 @@ typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 template <int SRC> struct ElemT;
-template <> struct ElemT<SRC_BF16> { typedef uint16_t raw; static constexpr int bytes = 2, dwords = 4; };
-template <> struct ElemT<SRC_F32> { typedef float raw; static constexpr int bytes = 4, dwords = 8; };
+template <> struct ElemT<SRC_BF16> { typedef uint16_t raw; static constexpr int bytes = 2; };
+template <> struct ElemT<SRC_F32> { typedef float raw; static constexpr int bytes = 4; };
 
 // two fp32 values rounded to nearest even, as a bf16 pair
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
@@ -27,20 +27,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
 }
 
-// eight consecutive elements as raw dwords (bf16: 4, fp32: 8)
-template <int SRC> struct Chunk { uint32_t w[ElemT<SRC>::dwords]; };
+// N (eight, or four) consecutive elements as raw dwords
+template <int SRC, int N = 8> struct Chunk { uint32_t w[N * ElemT<SRC>::bytes / 4]; };
 
-template <int SRC>
-__device__ __forceinline__ Chunk<SRC> load_chunk(const void* base, int64_t elem)
+template <int SRC, int N = 8>
+__device__ __forceinline__ Chunk<SRC, N> load_chunk(const void* base, int64_t elem)
 {
-    Chunk<SRC> c;
+    Chunk<SRC, N> c;
     const typename ElemT<SRC>::raw* p = (const typename ElemT<SRC>::raw*)base + elem;
     __builtin_memcpy(&c, p, sizeof c);       // 16-byte accesses with the element's alignment
     return c;
 }
 
-template <int SRC>
-__device__ __forceinline__ float chunk_value(const Chunk<SRC>& c, int i)
+template <int SRC, int N>
+__device__ __forceinline__ float chunk_value(const Chunk<SRC, N>& c, int i)
 {
     if constexpr (SRC == SRC_BF16) return (i & 1) ? bf16_hi(c.w[i >> 1]) : bf16_lo(c.w[i >> 1]);
     else return __uint_as_float(c.w[i]);
@@ -139,12 +139,21 @@ __device__ __forceinline__ float group_sum(float v, float* red)
 // ---------------------------------------------------------------------
 // MX row blocks of 32, eight elements in each of four consecutive lanes
 // ---------------------------------------------------------------------
-__device__ __forceinline__ uint32_t chunk_key(const float (&v)[8])
+// |max| key of three values: their largest magnitude's bits, a NaN's where one
+// is NaN (v_maximum3_f32, the maximum of IEEE 754-2019)
+__device__ __forceinline__ float abs_max3(float a, float b, float c)
 {
-    uint32_t k = 0;
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b)), __builtin_fabsf(c));
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t chunk_key(const float (&v)[N])
+{
+    static_assert(N % 2 == 0, "pairs");
+    float k = __builtin_elementwise_maximum(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
 #pragma unroll
-    for (int i = 0; i < 8; i++) k = max(k, abs_key(v[i]));
-    return k;
+    for (int i = 2; i < N; i += 2) k = abs_max3(k, v[i], v[i + 1]);
+    return __float_as_uint(k);
 }
 
 __device__ __forceinline__ uint32_t quad_max(uint32_t k)
@@ -152,6 +161,46 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t k)
     k = max(k, dpp<DPP_XOR1>(k));
     return max(k, dpp<DPP_XOR2>(k));
 }
+
+// Shared exponent of a block from its |max| key, in the forms the converters
+// take: the E8M0 byte max(exponent field - emax, 0) (the exponent rule with
+// its clamp at -127, which takes zero and subnormal maxima too), 2^e as an
+// fp32 whose exponent field is that byte, and Fmax 2^e.
+template <int FMT>
+struct BlockScale {
+    uint32_t byte;
+    float scale, top;
+    __device__ __forceinline__ explicit BlockScale(uint32_t key)
+    {
+        constexpr uint32_t TOP = FMT == E4M3 ? (8u << 23) | 0x600000u : (15u << 23) | 0x600000u;   // Fmax = 1.75 2^emax
+        byte = __builtin_elementwise_sub_sat(key >> 23, (uint32_t)Fmt<FMT>::emax);
+        scale = __uint_as_float(byte << 23);
+        top = __uint_as_float((byte << 23) + TOP);
+    }
+    __device__ __forceinline__ float clamped(float v) const { return __builtin_amdgcn_fmed3f(v, -top, top); }
+};
+
+// Four codes of a finite block.  The scaled converters return RNE(x / 2^e),
+// the scale's exponent field read as E8M0, and do not saturate: the values are
+// clamped to +-Fmax 2^e first.  (Equal to scaling, clamping and converting
+// for every block exponent over 28 binades below it, and 1.5 instructions an
+// element instead of 2.5.)
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(const BlockScale<FMT>& b, float v0, float v1, float v2, float v3)
+{
+    short2v d = {0, 0};
+    const float c0 = b.clamped(v0), c1 = b.clamped(v1), c2 = b.clamped(v2), c3 = b.clamped(v3);
+    if constexpr (FMT == E4M3) {
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(d, c0, c1, b.scale, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(d, c2, c3, b.scale, true);
+    } else {
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(d, c0, c1, b.scale, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(d, c2, c3, b.scale, true);
+    }
+    return __builtin_bit_cast(uint32_t, d);
+}
+
+constexpr uint32_t NONFINITE = 0x7F800000u;      // keys from here on: a block with a NaN or an Inf
 
 struct Codes8 { uint32_t lo, hi, scale; };
 
@@ -161,13 +210,10 @@ struct Codes8 { uint32_t lo, hi, scale; };
 template <int FMT>
 __device__ __forceinline__ Codes8 encode8(const float (&v)[8], uint32_t key)
 {
-    const int e = block_exponent<FMT>(key);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) y[i] = clamp_fmax<FMT>(scale_by(v[i], e));
-    const bool bad = key >= 0x7F800000u;
-    return Codes8{bad ? 0x7F7F7F7Fu : cvt4_fp8<FMT>(y[0], y[1], y[2], y[3]),
-                  bad ? 0x7F7F7F7Fu : cvt4_fp8<FMT>(y[4], y[5], y[6], y[7]), bad ? 0xFFu : (uint32_t)(e + 127)};
+    const BlockScale<FMT> b(key);
+    Codes8 c{encode4<FMT>(b, v[0], v[1], v[2], v[3]), encode4<FMT>(b, v[4], v[5], v[6], v[7]), b.byte};
+    if (key >= NONFINITE) c = Codes8{0x7F7F7F7Fu, 0x7F7F7F7Fu, 0xFFu};
+    return c;
 }
 
 __device__ __forceinline__ Codes8 encode8(int fmt, const float (&v)[8], uint32_t key)
@@ -188,33 +234,35 @@ __device__ __forceinline__ void encode_row_chunk(int fmt, const float (&v)[8], b
     }
 }
 
-// 2^(byte - 127) as mx_dequantize takes it: byte 0 is 2^-127 (an fp32
-// subnormal), byte 255 is NaN
-__device__ __forceinline__ float scale_value(uint32_t byte)
+// Checkpointed values: two codes (the low or high half of c) times 2^(byte -
+// 127) by one converter, which reads the scale's exponent field as E8M0, byte
+// 0 as 2^-127 and byte 255 as NaN, as mx_dequantize does (equal to it for
+// every code and byte).
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t c, uint32_t byte, float* v)
 {
-    const uint32_t bits = byte == 0xFFu ? 0x7FC00000u : byte << 23;
-    return __uint_as_float(byte == 0 ? 0x00400000u : bits);
+    const float s = __uint_as_float(byte << 23);
+    f32x2_t a, b;
+    if constexpr (FMT == E4M3) {
+        a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, s, false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, s, true);
+    } else {
+        a = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(c, s, false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(c, s, true);
+    }
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// eight checkpointed values: codes lo, hi and the block's scale byte
-__device__ __forceinline__ void decode8(int fmt, uint2 c, uint32_t byte, float (&v)[8])
+template <int FMT>
+__device__ __forceinline__ void decode8(uint2 c, uint32_t byte, float (&v)[8])
 {
-    const float s = scale_value(byte);
-    f32x2_t p[4];
-    if (fmt == E4M3) {
-        p[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
-        p[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
-        p[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
-        p[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
-    } else {
-        p[0] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.x, false);
-        p[1] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.x, true);
-        p[2] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.y, false);
-        p[3] = __builtin_amdgcn_cvt_pk_f32_bf8((int)c.y, true);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = p[i >> 1][i & 1] * s;
+    decode4<FMT>(c.x, byte, v);
+    decode4<FMT>(c.y, byte, v + 4);
 }
+
+// Where a backward kernel reads an input: from its tensor, or from a
+// checkpoint of one of the formats
+enum : int { FROM_TENSOR = -1, FROM_E4M3 = E4M3, FROM_E5M2 = E5M2 };
 
 // ---------------------------------------------------------------------
 // Gate functions a = act(x) and their slopes d = act'(x).

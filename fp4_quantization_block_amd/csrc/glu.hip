@@ -13,10 +13,8 @@
 // Kernels
 //   k_glu_fwd, k_glu_bwd   one chunk of eight elements per thread, in order
 //                    over rows and columns: each byte read and written once.
-//   k_glu_bwd_dual   a wave takes 32 rows by 64 columns, a lane four rows by
-//                    eight columns, so that row blocks end inside four lanes
-//                    and column blocks inside eight; the gradients never
-//                    leave registers before they are codes.
+//   k_glu_bwd_dual   tiles whose gradients never leave registers before they
+//                    are codes, in both layouts.
 #include "act_device.h"
 #include "mx_internal.h"
 
@@ -114,18 +112,18 @@ __global__ __launch_bounds__(256) void k_glu_fwd(GluFwdJob a, FastDiv per_row, u
     }
 }
 
-template <int SRC, int ACT, bool CKPT, bool VEC>
+template <int SRC, int ACT, int FROM, bool VEC>
 __global__ __launch_bounds__(256) void k_glu_bwd(GluBwdJob a, FastDiv per_row, uint32_t units)
 {
     const Place<VEC> at(per_row, units);
     float d[8], g[8], u[8], h[8];
     at.template load<SRC>(a.dh, a.ld_dh, d);
-    if constexpr (CKPT) {
+    if constexpr (FROM != FROM_TENSOR) {
         const int64_t e = at.dense(a.cols);
         const uint2 cg = *(const uint2*)(a.qg + e), cu = *(const uint2*)(a.qu + e);
         const uint32_t bg = a.sg[e >> 5], bu = a.su[e >> 5];
-        decode8(a.ckpt_fmt, cg, bg, g);
-        decode8(a.ckpt_fmt, cu, bu, u);
+        decode8<FROM>(cg, bg, g);
+        decode8<FROM>(cu, bu, u);
     } else {
         at.template load<SRC>(a.gate, a.ld_gate, g);
         at.template load<SRC>(a.up, a.ld_up, u);
@@ -182,7 +180,7 @@ hipError_t run_fwd(const GluFwdJob& job, hipStream_t s)
     });
 }
 
-template <int SRC, int ACT, bool CKPT, bool VEC>
+template <int SRC, int ACT, int FROM, bool VEC>
 hipError_t run_bwd(const GluBwdJob& job, hipStream_t s)
 {
     return sliced<VEC>(job.rows, job.cols, [&](int64_t r, int64_t n, FastDiv d, uint32_t units, dim3 grid) {
@@ -197,7 +195,7 @@ hipError_t run_bwd(const GluBwdJob& job, hipStream_t s)
         advance(j.h, r * j.ld_h * B);
         for (const uint8_t** q : {&j.qg, &j.qu}) advance(*q, r * j.cols);
         for (const uint8_t** q : {&j.sg, &j.su}) advance(*q, r * (j.cols / 32));
-        k_glu_bwd<SRC, ACT, CKPT, VEC><<<grid, dim3(256), 0, s>>>(j, d, units);
+        k_glu_bwd<SRC, ACT, FROM, VEC><<<grid, dim3(256), 0, s>>>(j, d, units);
     });
 }
 
@@ -210,28 +208,34 @@ hipError_t by_act(int act, F&& f)
 }
 
 // ---------------------------------------------------------------------------
-// k_glu_bwd_dual: workgroups of four waves take tiles of 128 rows by 64
-// columns of h, wave w the rows 32 w .. 32 w + 31.  Lane 8 k + m holds rows
-// 4 m .. 4 m + 3 and columns 8 k .. 8 k + 7: a column block is spread over the
-// eight lanes 8 k .. 8 k + 7, a row block over four lanes 8 apart.  Row codes
-// are stored at once, eight bytes a lane; a lane's column codes are four rows
-// of a column, one dword, and go through LDS to leave as whole runs of 128
-// bytes a column.
+// k_glu_bwd_dual: workgroups of WR x WC waves walk tiles of 32 WR rows by
+// 32 WC columns of h; a wave takes 32 x 32 of them.  Lane 8 k + m holds rows
+// 4 m .. 4 m + 3 and columns 4 k .. 4 k + 3: a column block is spread over
+// eight neighbouring lanes, a row block over eight lanes 8 apart, so both
+// maxima are three cross-lane steps on registers.  A lane's codes of a row
+// (four columns) or of a column (four rows) are one dword, and go through LDS
+// to leave as whole runs of a row or a column.  The next tile's inputs are
+// loaded into registers while the current tile is encoded.
+//
+// Tiles are 128 x 128, so that every input and output line of codes is a
+// whole 128-byte line of one tile: an L2 (4 MiB for 32 CUs) keeps a line for
+// some microseconds at this kernel's rate, too short to wait for the tile
+// that has the other half.  A row's scale bytes are 4 per tile; a workgroup
+// takes its tiles along the rows, and reads and writes the scale bytes of up
+// to 16 tiles at a time through LDS.
 // ---------------------------------------------------------------------------
-constexpr int DR = 128, DC = 64;
 
-// LDS byte of (column, 16-byte chunk of its 128 rows): chunks are permuted by
-// the column's lane, so that a wave's writes spread over the banks
-__device__ __forceinline__ int dual_at(int col, int chunk) { return col * DR + ((chunk ^ (col >> 3)) << 4); }
-
-// the largest key of the four lanes 8 apart that hold a row block's chunks:
-// lanes l, l ^ 8 (in the 16-lane row) and l ^ 16
+// the largest key of the eight lanes 8 apart: l ^ 8 (in the 16-lane row), l ^ 16, l ^ 32
 __device__ __forceinline__ uint32_t row_block_max(uint32_t k)
 {
     k = max(k, dpp<0x128>(k));                 // rotate by 8 in a row of 16
-    return max(k, (uint32_t)__shfl_xor((int)k, 16));
+    auto p = __builtin_amdgcn_permlane16_swap(k, k, false, false);
+    k = max((uint32_t)p[0], (uint32_t)p[1]);
+    auto q = __builtin_amdgcn_permlane32_swap(k, k, false, false);
+    return max((uint32_t)q[0], (uint32_t)q[1]);
 }
 
+// the largest key of eight neighbouring lanes
 __device__ __forceinline__ uint32_t oct_max(uint32_t k)
 {
     k = max(k, dpp<DPP_XOR1>(k));
@@ -239,105 +243,317 @@ __device__ __forceinline__ uint32_t oct_max(uint32_t k)
     return max(k, dpp<DPP_HALF_MIRROR>(k));
 }
 
-// Column codes of one tensor's 4 x 8 values per lane into `stage` and scale
-// bytes (packed by column, one byte per wave) into `scales`
-template <int FMT>
-__device__ __forceinline__ void stage_columns(const float (&v)[4][8], uint8_t* stage, uint8_t* scales, int wave, int lane)
+// Waits for this wave's LDS traffic only (its global loads and stores stay in
+// flight), then meets the workgroup.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// the inputs of one lane's 4 x 4 values, as they are in memory
+template <int SRC, bool TENSOR> struct DualRaw;
+template <int SRC> struct DualRaw<SRC, true> { Chunk<SRC, 4> d[4], g[4], u[4]; };
+template <int SRC> struct DualRaw<SRC, false> { Chunk<SRC, 4> d[4]; uint32_t g[4], u[4]; };
+
+// Accesses at base + offset, base the same for the whole wave and offset a
+// lane's, in the form of one scalar address and a 32-bit vector offset.  (The
+// compiler would otherwise add a loop-invariant offset to the tensor's base
+// first, and hold a 64-bit address in vector registers for every access.)
+// V: an integer, or a vector of 32-bit ones, at any alignment.
+#define MX_GLOBAL __attribute__((address_space(1)))
+typedef uint32_t dwords2 __attribute__((ext_vector_type(2)));
+typedef uint32_t dwords4 __attribute__((ext_vector_type(4)));
+template <class V> struct __attribute__((packed)) Unaligned { V v; };
+
+template <class V>
+__device__ __forceinline__ MX_GLOBAL Unaligned<V>* lane_at(const void* base, uint32_t offset)
 {
-    const int m = lane & 7, k = lane >> 3;
-#pragma unroll
-    for (int c = 0; c < 8; c++) {
-        uint32_t key = 0;
-#pragma unroll
-        for (int r = 0; r < 4; r++) key = max(key, abs_key(v[r][c]));
-        key = oct_max(key);
-        const int e = block_exponent<FMT>(key);
-        float y[4];
-#pragma unroll
-        for (int r = 0; r < 4; r++) y[r] = clamp_fmax<FMT>(scale_by(v[r][c], e));
-        const bool bad = key >= 0x7F800000u;
-        const int col = 8 * k + c;
-        *(uint32_t*)(stage + dual_at(col, wave * 2 + (m >> 2)) + (m & 3) * 4) =
-            bad ? 0x7F7F7F7Fu : cvt4_fp8<FMT>(y[0], y[1], y[2], y[3]);
-        if (m == c) scales[col * 4 + wave] = bad ? 0xFF : (uint8_t)(e + 127);
-    }
+    MX_GLOBAL uint8_t* b = (MX_GLOBAL uint8_t*)base;
+    asm("" : "+s"(b));
+    asm("" : "+v"(offset));
+    return (MX_GLOBAL Unaligned<V>*)(b + offset);
 }
 
-__device__ __forceinline__ void stage_columns(int fmt, const float (&v)[4][8], uint8_t* stage, uint8_t* scales, int wave,
-                                              int lane)
+template <int SRC>
+__device__ __forceinline__ Chunk<SRC, 4> lane_chunk(const void* base, uint32_t offset)
 {
-    if (fmt == E4M3) stage_columns<E4M3>(v, stage, scales, wave, lane);
-    else stage_columns<E5M2>(v, stage, scales, wave, lane);
+    typedef std::conditional_t<SRC == SRC_BF16, dwords2, dwords4> V;
+    return __builtin_bit_cast(Chunk<SRC, 4>, V(lane_at<V>(base, offset)->v));
 }
 
-// the runs of one staged tensor: nc columns of nr rows to the column copy
-// whose stored row 0 is the tile's first column
-__device__ __forceinline__ void store_columns(const uint8_t* stage, const uint8_t* scales, uint8_t* q, uint8_t* s,
-                                              int64_t rows, int64_t r0, int nr, int nc)
-{
-    for (int id = (int)threadIdx.x; id < DC * (DR / 16); id += 256) {
-        const int col = id / (DR / 16), ch = id % (DR / 16);
-        if (col < nc && ch * 16 < nr) *(uint4*)(q + col * rows + r0 + ch * 16) = *(const uint4*)(stage + dual_at(col, ch));
-    }
-    const int col = (int)threadIdx.x / 4, blk = (int)threadIdx.x % 4;
-    if (col < nc && blk * 32 < nr) s[col * (rows / 32) + r0 / 32 + blk] = scales[col * 4 + blk];
-}
+// Places of a lane in the tiles' inputs: byte offsets from a tile's first
+// element, 32 bits of them (row strides are at most 2^23), so that the loads
+// share one address register a tensor, with the row added to the scalar base
+struct DualAt { uint32_t d, g, u, q; };
 
-template <int SRC, int ACT, bool CKPT>
-__global__ __launch_bounds__(256) void k_glu_bwd_dual(GluBwdJob a, uint32_t col_tiles)
+template <int SRC, bool TENSOR>
+__device__ __forceinline__ void dual_load(const GluBwdJob& a, int64_t row, int64_t col, const DualAt& at,
+                                          DualRaw<SRC, TENSOR>& r)
 {
-    __shared__ __align__(16) uint8_t stage[3][DC * DR];
-    __shared__ uint8_t scales[3][DC * 4];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int64_t r0 = (int64_t)(blockIdx.x / col_tiles) * DR, c0 = (int64_t)(blockIdx.x % col_tiles) * DC;
-    const int nr = (int)min((int64_t)DR, a.rows - r0), nc = (int)min((int64_t)DC, a.cols - c0);
-    const int lr = wave * 32 + (lane & 7) * 4, lc = (lane >> 3) * 8;
-    const bool ok = lr < nr && lc < nc;        // the same for the lanes of a block: rows and columns end at multiples of 32
-    float g[4][8], u[4][8], h[4][8];
+    constexpr int B = ElemT<SRC>::bytes;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const int64_t row = r0 + (ok ? lr : 0) + i, col = c0 + (ok ? lc : 0);
-        const Chunk<SRC> d = load_chunk<SRC>(a.dh, row * a.ld_dh + col);
-        if constexpr (CKPT) {
-            const int64_t e = row * a.cols + col;
-            decode8(a.ckpt_fmt, *(const uint2*)(a.qg + e), a.sg[e >> 5], g[i]);
-            decode8(a.ckpt_fmt, *(const uint2*)(a.qu + e), a.su[e >> 5], u[i]);
+        r.d[i] = lane_chunk<SRC>((const uint8_t*)a.dh + ((row + i) * a.ld_dh + col) * B, at.d);
+        if constexpr (!TENSOR) {
+            const int64_t e = (row + i) * a.cols + col;
+            r.g[i] = lane_at<uint32_t>(a.qg + e, at.q)->v;
+            r.u[i] = lane_at<uint32_t>(a.qu + e, at.q)->v;
         } else {
-            const Chunk<SRC> cg = load_chunk<SRC>(a.gate, row * a.ld_gate + col);
-            const Chunk<SRC> cu = load_chunk<SRC>(a.up, row * a.ld_up + col);
-#pragma unroll
-            for (int k = 0; k < 8; k++) g[i][k] = chunk_value<SRC>(cg, k), u[i][k] = chunk_value<SRC>(cu, k);
+            r.g[i] = lane_chunk<SRC>((const uint8_t*)a.gate + ((row + i) * a.ld_gate + col) * B, at.g);
+            r.u[i] = lane_chunk<SRC>((const uint8_t*)a.up + ((row + i) * a.ld_up + col) * B, at.u);
         }
+    }
+}
+
+// Blocks of four values per lane: v[j] are the four of block j, key[j] the
+// block's |max| key in every lane that holds a part of it.  Codes and scale
+// bytes of the four blocks.
+template <int FMT>
+__device__ __forceinline__ void encode_blocks(const float (&v)[4][4], const uint32_t (&key)[4], uint32_t (&code)[4],
+                                              uint32_t (&byte)[4])
+{
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const float dh = chunk_value<SRC>(d, k);
-            float act, slope;
-            gate<ACT, true>(g[i][k], act, slope);
-            h[i][k] = act * u[i][k];
-            g[i][k] = dh * u[i][k] * slope;
-            u[i][k] = dh * act;
+    for (int j = 0; j < 4; j++) {
+        const BlockScale<FMT> b(key[j]);
+        code[j] = encode4<FMT>(b, v[j][0], v[j][1], v[j][2], v[j][3]);
+        byte[j] = b.byte;
+    }
+    if (max(max(key[0], key[1]), max(key[2], key[3])) >= NONFINITE) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (key[j] >= NONFINITE) code[j] = 0x7F7F7F7Fu, byte[j] = 0xFFu;
+    }
+}
+
+// Staged lines of LB code bytes are LB + 8 bytes apart: the eight lines that
+// a wave writes dwords of at once are four lines apart, and start in eight
+// different groups of eight banks.
+template <int LB> constexpr int line_bytes() { return LB + 8; }
+
+// codes of the row blocks (v[row][column]) or column blocks (v[column][row])
+// of one tensor: four lines from line0 on, at byte `at` of each; scale bytes
+// of the lines' blocks, SPL to a line, by the lanes that `writes`
+template <int FMT, int LB, int SPL, bool COLUMNS>
+__device__ __forceinline__ void stage_blocks(const float (&v)[4][4], uint8_t* stage, uint8_t* scales, int line0, int at,
+                                             int block, bool writes)
+{
+    uint32_t key[4], code[4], byte[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) key[j] = COLUMNS ? oct_max(chunk_key(v[j])) : row_block_max(chunk_key(v[j]));
+    encode_blocks<FMT>(v, key, code, byte);
+#pragma unroll
+    for (int j = 0; j < 4; j++) *(uint32_t*)(stage + (line0 + j) * line_bytes<LB>() + at) = code[j];
+    if (writes) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) scales[(line0 + j) * SPL + block] = (uint8_t)byte[j];
+    }
+}
+
+// n scale bytes, 1 <= n <= N, staged at src, to base + offset
+template <int N>
+__device__ __forceinline__ void store_scale_bytes(uint8_t* base, uint32_t offset, const uint8_t* src, int n)
+{
+    if (N == 4 && n == 4) {
+        lane_at<uint32_t>(base, offset)->v = *(const uint32_t*)src;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (i < n) lane_at<uint8_t>(base, offset + i)->v = src[i];
+    }
+}
+
+// A thread's number, in a form that the compiler computes with where it is
+// used: what a tile's stores derive from it is cheap, and would otherwise be
+// held in registers all through the loop over tiles (and spilled).
+__device__ __forceinline__ int thread_here()
+{
+    int t = (int)threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+// One staged tensor to its copy: `lines` of LB bytes, of which `bytes` are in
+// the tensor, to stored rows q, q + stride, ...
+template <int LB, int LINES, int NT>
+__device__ __forceinline__ void store_lines(int tid, const uint8_t* stage, uint8_t* q, uint32_t stride, int lines, int bytes)
+{
+    constexpr int CH = LB / 16;
+#pragma unroll
+    for (int k = 0; k < (LINES * CH + NT - 1) / NT; k++) {
+        const int id = tid + k * NT, line = id / CH, ch = id % CH;
+        if (line < lines && ch * 16 < bytes) {
+            const dwords2* p = (const dwords2*)(stage + line * line_bytes<LB>() + ch * 16);
+            lane_at<dwords4>(q, (uint32_t)line * stride + ch * 16)->v = __builtin_shufflevector(p[0], p[1], 0, 1, 2, 3);
         }
-        // row copies: dgate in columns 0 .. cols - 1, dup after them
-        const Codes8 cg = encode8(a.fmt, g[i], row_block_max(chunk_key(g[i])));
-        const Codes8 cu = encode8(a.fmt, u[i], row_block_max(chunk_key(u[i])));
-        if (ok) {
-            const int64_t e = row * 2 * a.cols + col;
-            *(uint2*)(a.q_row + e) = make_uint2(cg.lo, cg.hi);
-            *(uint2*)(a.q_row + e + a.cols) = make_uint2(cu.lo, cu.hi);
-            if ((lane >> 3 & 3) == 0) {
-                a.s_row[e >> 5] = (uint8_t)cg.scale;
-                a.s_row[(e + a.cols) >> 5] = (uint8_t)cu.scale;
+    }
+}
+
+// Scale bytes of the rows of a window of tiles: WB bytes a line in LDS, of
+// which n are in the tensor, from or to rows g, g + stride, ...  at any
+// alignment; 16 bytes a thread.  The lines are 16 bytes more apart, so that
+// lanes four lines apart use different banks.
+constexpr int WINDOW = 16;              // tiles
+
+template <int WB, int LINES, int NT, bool STORE>
+__device__ __forceinline__ void move_row_scales(int tid, uint8_t* lds, uint8_t* g, uint32_t stride, int lines, int n)
+{
+    constexpr int CH = WB / 16;
+#pragma unroll
+    for (int k = 0; k < (LINES * CH + NT - 1) / NT; k++) {
+        const int id = tid + k * NT, line = id / CH, at = id % CH * 16;
+        const uint32_t to = (uint32_t)line * stride + at;
+        uint8_t* l = lds + line * (WB + 16) + at;
+        if (line < lines && at + 16 <= n) {
+            if constexpr (STORE) lane_at<dwords4>(g, to)->v = *(const dwords4*)l;
+            else *(dwords4*)l = lane_at<dwords4>(g, to)->v;
+        } else if (line < lines) {
+            for (int i = 0; at + i < n; i++) {
+                if constexpr (STORE) lane_at<uint8_t>(g, to + i)->v = l[i];
+                else l[i] = lane_at<uint8_t>(g, to + i)->v;
             }
         }
     }
-    stage_columns(a.fmt, g, stage[0], scales[0], wave, lane);
-    stage_columns(a.fmt, u, stage[1], scales[1], wave, lane);
-    if (a.qh) stage_columns(a.h_fmt, h, stage[2], scales[2], wave, lane);
-    __syncthreads();
-    const int64_t sr = a.rows / 32;
-    store_columns(stage[0], scales[0], a.q_col + c0 * a.rows, a.s_col + c0 * sr, a.rows, r0, nr, nc);
-    store_columns(stage[1], scales[1], a.q_col + (a.cols + c0) * a.rows, a.s_col + (a.cols + c0) * sr, a.rows, r0, nr, nc);
-    if (a.qh) store_columns(stage[2], scales[2], a.qh + c0 * a.rows, a.sh + c0 * sr, a.rows, r0, nr, nc);
+}
+
+struct DualTiles { uint32_t nx, ny; };
+
+constexpr int WAIT_VMEM = 0x0F70;       // s_waitcnt vmcnt(0): expcnt and lgkmcnt at their largest
+
+template <int SRC, int ACT, int FROM, int FMT, int WR, int WC>
+__global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, DualTiles tiles)
+{
+    constexpr int TR = 32 * WR, TC = 32 * WC, NT = 64 * WR * WC, WB = WINDOW * WC, WS = WB + 16;
+    constexpr bool TENSOR = FROM == FROM_TENSOR;
+    static_assert(NT >= TC, "a thread per column for its scale bytes");
+    __shared__ __align__(16) uint8_t cols[3][TC * line_bytes<TR>()], rows[2][TR * line_bytes<TC>()];
+    __shared__ __align__(16) uint8_t col_scales[3][TC * WR], row_scales[2][TR * WS], in_scales[2][TENSOR ? 16 : TR * WS];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, band = wave % WR, part = wave / WR;
+    const int m = lane & 7, k8 = lane >> 3, lr = band * 32 + m * 4, lc = part * 32 + k8 * 4;
+    const uint32_t sr = (uint32_t)(a.rows / 32), sc = (uint32_t)(a.cols / 32);
+    // this workgroup's run of tiles, along the rows of tiles
+    const uint64_t all = (uint64_t)tiles.nx * tiles.ny;
+    uint32_t tile = (uint32_t)(all * blockIdx.x / gridDim.x);
+    const uint32_t end = (uint32_t)(all * (blockIdx.x + 1) / gridDim.x);
+    uint32_t ty = tile / tiles.nx, tx = tile - ty * tiles.nx;
+    constexpr uint32_t B = ElemT<SRC>::bytes;
+    const DualAt place{(uint32_t)(lr * a.ld_dh + lc) * B, (uint32_t)(lr * a.ld_gate + lc) * B, (uint32_t)(lr * a.ld_up + lc) * B,
+                       (uint32_t)(lr * a.cols + lc)};
+    DualRaw<SRC, TENSOR> raw;
+    // a lane past the tensor's end reads the tile's first places instead (its
+    // whole blocks lie outside: rows and cols are multiples of 32)
+    auto fetch = [&](uint32_t y, uint32_t x) {
+        const int64_t r = (int64_t)y * TR, c = (int64_t)x * TC;
+        const bool in = r + lr < a.rows && c + lc < a.cols;
+        dual_load(a, r, c, in ? place : DualAt{}, raw);
+    };
+    if (tile < end) fetch(ty, tx);
+    __builtin_amdgcn_s_waitcnt(WAIT_VMEM);     // as inside the loop: no load is in flight where it begins again
+    uint32_t first = tx, left = 0;             // the window's first tile column, its tiles still to do
+    while (tile < end) {
+        const int64_t r0 = (int64_t)ty * TR, c0 = (int64_t)tx * TC;
+        const int nr = (int)min((int64_t)TR, a.rows - r0), nc = (int)min((int64_t)TC, a.cols - c0);
+        if (left == 0) {
+            first = tx;
+            left = min(min((uint32_t)WINDOW, tiles.nx - tx), end - tile);
+            if constexpr (!TENSOR) {
+                const int tid = thread_here();
+                const int64_t at = r0 * sc + c0 / 32;
+                const int n = (int)min((int64_t)left * WC, (int64_t)sc - c0 / 32);
+                move_row_scales<WB, TR, NT, false>(tid, in_scales[0], (uint8_t*)a.sg + at, sc, nr, n);
+                move_row_scales<WB, TR, NT, false>(tid, in_scales[1], (uint8_t*)a.su + at, sc, nr, n);
+                lds_barrier();
+            }
+        }
+        const int block = (int)(tx - first) * WC + part;        // this wave's block of the window's rows
+        float g[4][4], u[4][4], h[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if constexpr (!TENSOR) {
+                decode4<FROM>(raw.g[i], in_scales[0][(lr + i) * WS + block], g[i]);
+                decode4<FROM>(raw.u[i], in_scales[1][(lr + i) * WS + block], u[i]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; c++) g[i][c] = chunk_value(raw.g[i], c), u[i][c] = chunk_value(raw.u[i], c);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const float dh = chunk_value(raw.d[i], c);
+                float act, slope;
+                gate<ACT, true>(g[i][c], act, slope);
+                h[i][c] = act * u[i][c];
+                g[i][c] = dh * u[i][c] * slope;
+                u[i][c] = dh * act;
+            }
+        }
+        uint32_t y1 = ty, x1 = tx + 1;
+        if (x1 == tiles.nx) x1 = 0, y1++;
+        if (tile + 1 < end) fetch(y1, x1);
+        auto transposed = [](const float (&v)[4][4], float (&t)[4][4]) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) t[i & 3][i >> 2] = v[i >> 2][i & 3];
+        };
+        float t[4][4];
+        stage_blocks<FMT, TC, WS, false>(g, rows[0], row_scales[0], lr, lc, block, k8 == 0);
+        stage_blocks<FMT, TC, WS, false>(u, rows[1], row_scales[1], lr, lc, block, k8 == 0);
+        transposed(g, t);
+        stage_blocks<FMT, TR, WR, true>(t, cols[0], col_scales[0], lc, lr, band, m == 0);
+        transposed(u, t);
+        stage_blocks<FMT, TR, WR, true>(t, cols[1], col_scales[1], lc, lr, band, m == 0);
+        if (a.qh) {
+            transposed(h, t);
+            if (a.h_fmt == E4M3) stage_blocks<E4M3, TR, WR, true>(t, cols[2], col_scales[2], lc, lr, band, m == 0);
+            else stage_blocks<E5M2, TR, WR, true>(t, cols[2], col_scales[2], lc, lr, band, m == 0);
+        }
+        // The next tile's inputs have landed, most of a tile's work after they
+        // were asked for: waited for here, ahead of this tile's stores, since
+        // loads and stores complete in one count and a wait for the loads
+        // behind the stores would be one for the stores too.
+        __builtin_amdgcn_s_waitcnt(WAIT_VMEM);
+        lds_barrier();                         // the tile is staged
+        const int tid = thread_here();
+        // row copy: dgate in columns 0 .. cols - 1, dup after them
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            store_lines<TC, TR, NT>(tid, rows[w], a.q_row + (2 * r0 + w) * a.cols + c0, 2 * (uint32_t)a.cols, nr, nc);
+            store_lines<TR, TC, NT>(tid, cols[w], a.q_col + (w * a.cols + c0) * a.rows + r0, (uint32_t)a.rows, nc, nr);
+        }
+        if (a.qh) store_lines<TR, TC, NT>(tid, cols[2], a.qh + c0 * a.rows + r0, (uint32_t)a.rows, nc, nr);
+        if (const int line = tid; line < nc) {
+            const int64_t at = c0 * sr + r0 / 32;
+            store_scale_bytes<WR>(a.s_col + at, (uint32_t)line * sr, &col_scales[0][line * WR], nr / 32);
+            store_scale_bytes<WR>(a.s_col + a.cols * sr + at, (uint32_t)line * sr, &col_scales[1][line * WR], nr / 32);
+            if (a.qh) store_scale_bytes<WR>(a.sh + at, (uint32_t)line * sr, &col_scales[2][line * WR], nr / 32);
+        }
+        if (--left == 0) {
+            const int64_t at = 2 * r0 * sc + (int64_t)first * WC;
+            const int n = (int)min((int64_t)(tx - first + 1) * WC, (int64_t)sc - (int64_t)first * WC);
+            move_row_scales<WB, TR, NT, true>(tid, row_scales[0], a.s_row + at, 2 * sc, nr, n);
+            move_row_scales<WB, TR, NT, true>(tid, row_scales[1], a.s_row + at + sc, 2 * sc, nr, n);
+        }
+        lds_barrier();                         // the staged tile has been read
+        tile++;
+        ty = y1;
+        tx = x1;
+    }
+}
+
+template <int SRC, int ACT, int FROM, int FMT, int WR, int WC>
+hipError_t run_dual(const GluBwdJob& j, hipStream_t s)
+{
+    const DualTiles n{(uint32_t)((j.cols + 32 * WC - 1) / (32 * WC)), (uint32_t)((j.rows + 32 * WR - 1) / (32 * WR))};
+    int dev = 0, cus = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return e;
+    const int64_t all = (int64_t)n.nx * n.ny, most = (int64_t)cus * (16 / (WR * WC)), grid = all < most ? all : most;
+    k_glu_bwd_dual<SRC, ACT, FROM, FMT, WR, WC><<<dim3((unsigned)grid), dim3(64 * WR * WC), 0, s>>>(j, n);
+    return hipGetLastError();
+}
+
+// f(where gate and up come from)
+template <class F>
+hipError_t by_source(const GluBwdJob& j, F&& f)
+{
+    if (!j.qg) return f(std::integral_constant<int, FROM_TENSOR>());
+    if (j.ckpt_fmt == E4M3) return f(std::integral_constant<int, FROM_E4M3>());
+    return f(std::integral_constant<int, FROM_E5M2>());
 }
 
 }  // namespace
@@ -353,31 +569,25 @@ hipError_t launch_glu_fwd(const GluFwdJob& j, hipStream_t s)
 
 hipError_t launch_glu_bwd(const GluBwdJob& j, hipStream_t s)
 {
-    const bool vec = j.cols % 8 == 0;
     return by_act(j.act, [&](auto A) {
-        if (j.src == SRC_F32) {
-            if (j.qg) return run_bwd<SRC_F32, A, true, true>(j, s);
-            return vec ? run_bwd<SRC_F32, A, false, true>(j, s) : run_bwd<SRC_F32, A, false, false>(j, s);
-        }
-        if (j.qg) return run_bwd<SRC_BF16, A, true, true>(j, s);
-        return vec ? run_bwd<SRC_BF16, A, false, true>(j, s) : run_bwd<SRC_BF16, A, false, false>(j, s);
+        return by_source(j, [&](auto from) {
+            if constexpr (from == FROM_TENSOR) {
+                if (j.cols % 8 != 0) return j.src == SRC_F32 ? run_bwd<SRC_F32, A, from, false>(j, s) : run_bwd<SRC_BF16, A, from, false>(j, s);
+            }
+            return j.src == SRC_F32 ? run_bwd<SRC_F32, A, from, true>(j, s) : run_bwd<SRC_BF16, A, from, true>(j, s);
+        });
     });
 }
 
 hipError_t launch_glu_bwd_dual(const GluBwdJob& j, hipStream_t s)
 {
-    const int64_t ct = (j.cols + DC - 1) / DC, rt = (j.rows + DR - 1) / DR;
     return by_act(j.act, [&](auto A) {
-        const dim3 grid((unsigned)(ct * rt)), block(256);
-        const uint32_t c = (uint32_t)ct;
-        if (j.src == SRC_F32) {
-            if (j.qg) k_glu_bwd_dual<SRC_F32, A, true><<<grid, block, 0, s>>>(j, c);
-            else k_glu_bwd_dual<SRC_F32, A, false><<<grid, block, 0, s>>>(j, c);
-        } else {
-            if (j.qg) k_glu_bwd_dual<SRC_BF16, A, true><<<grid, block, 0, s>>>(j, c);
-            else k_glu_bwd_dual<SRC_BF16, A, false><<<grid, block, 0, s>>>(j, c);
-        }
-        return hipGetLastError();
+        return by_source(j, [&](auto from) {
+            auto fmt = [&](auto F) {
+                return j.src == SRC_F32 ? run_dual<SRC_F32, A, from, F, 4, 4>(j, s) : run_dual<SRC_BF16, A, from, F, 4, 4>(j, s);
+            };
+            return j.fmt == E4M3 ? fmt(std::integral_constant<int, E4M3>()) : fmt(std::integral_constant<int, E5M2>());
+        });
     });
 }
 

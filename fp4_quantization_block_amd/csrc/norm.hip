@@ -232,13 +232,13 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormFwdJob a)
 // ---------------------------------------------------------------------------
 
 // chunk j of the normalised input (s - m) r, from the tensor or the checkpoint
-template <int SRC, bool CKPT, bool VEC, int T>
+template <int SRC, int FROM, bool VEC, int T>
 __device__ __forceinline__ void load_unit(const NormBwdJob& a, int64_t row, int64_t j, int t, float mean, float rstd,
                                           float (&h)[8])
 {
-    if constexpr (CKPT) {
+    if constexpr (FROM != FROM_TENSOR) {
         const int64_t c = col_of<VEC, T>(j, t, 0), e = row * a.cols + (c < a.cols ? c : 0);
-        decode8(a.ckpt_fmt, *(const uint2*)(a.qx + e), a.sx[e >> 5], h);
+        decode8<FROM>(*(const uint2*)(a.qx + e), a.sx[e >> 5], h);
     } else {
         load_row<SRC, VEC, T>(row_of<SRC>(a.x, row, a.ld_x), j, t, a.cols, h);
     }
@@ -263,7 +263,7 @@ __device__ __forceinline__ void store_dx(const NormBwdJob& a, int64_t row, int64
     store_row<SRC, VEC, T>((void*)row_of<SRC>(a.dx, row, a.ld_dx), j, t, a.cols, d);
 }
 
-template <int SRC, bool CKPT, bool VEC, int T, int N>
+template <int SRC, int FROM, bool VEC, int T, int N>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_bwd(NormBwdJob a)
 {
     constexpr int RPB = T < 256 ? 256 / T : 1;
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_bwd(NormBwdJob a)
 #pragma unroll
         for (int j = 0; j < N; j++) load_row<SRC, VEC, T>(row_of<SRC>(a.dy, row, a.ld_dy), j, t, a.cols, g[j]);
 #pragma unroll
-        for (int j = 0; j < N; j++) load_unit<SRC, CKPT, VEC, T>(a, row, j, t, mean, rstd, h[j]);
+        for (int j = 0; j < N; j++) load_unit<SRC, FROM, VEC, T>(a, row, j, t, mean, rstd, h[j]);
 #pragma unroll
         for (int j = 0; j < N; j++) {
 #pragma unroll
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_bwd(NormBwdJob a)
     }
 }
 
-template <int SRC, bool CKPT, bool VEC>
+template <int SRC, int FROM, bool VEC>
 __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormBwdJob a)
 {
     constexpr int T = 1024;
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormBwdJob a)
     for (int64_t j = 0; j < steps; j++) {
         float g[8], h[8];
         gradient(j, g);
-        load_unit<SRC, CKPT, VEC, T>(a, row, j, t, mean, rstd, h);
+        load_unit<SRC, FROM, VEC, T>(a, row, j, t, mean, rstd, h);
         pgh += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return g[i] * h[i]; });
         pg += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return g[i]; });
     }
@@ -343,14 +343,14 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormBwdJob a)
     for (int64_t j = 0; j < steps; j++) {
         float g[8], h[8];
         gradient(j, g);
-        load_unit<SRC, CKPT, VEC, T>(a, row, j, t, mean, rstd, h);
+        load_unit<SRC, FROM, VEC, T>(a, row, j, t, mean, rstd, h);
         store_dx<SRC, VEC, T>(a, row, j, t, g, h, rstd, mg, mgh);
     }
 }
 
 // Partial sums of dw and db over the rows of one part, a strip of 512
 // columns per wave: grid (strips / 4, parts)
-template <int SRC, bool CKPT, bool VEC>
+template <int SRC, int FROM, bool VEC>
 __global__ __launch_bounds__(256) void k_norm_cols(NormBwdJob a, int64_t rows_per_part)
 {
     constexpr int T = 64;
@@ -362,7 +362,7 @@ __global__ __launch_bounds__(256) void k_norm_cols(NormBwdJob a, int64_t rows_pe
     for (int64_t row = part * rows_per_part; row < end; row++) {
         float dy[8], h[8];
         load_row<SRC, VEC, T>(row_of<SRC>(a.dy, row, a.ld_dy), j, t, a.cols, dy);
-        load_unit<SRC, CKPT, VEC, T>(a, row, j, t, a.layer ? a.mean[row] : 0.0f, a.rstd[row], h);
+        load_unit<SRC, FROM, VEC, T>(a, row, j, t, a.layer ? a.mean[row] : 0.0f, a.rstd[row], h);
 #pragma unroll
         for (int i = 0; i < 8; i++) dw[i] += dy[i] * h[i], db[i] += dy[i];
     }
@@ -427,24 +427,24 @@ int64_t bwd_groups(int64_t rows, int64_t cols)
 
 int64_t wide_parts(int64_t rows) { return rows < 64 ? rows : 64; }
 
-template <int SRC, bool CKPT, bool VEC>
+template <int SRC, int FROM, bool VEC>
 hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
 {
     int64_t parts = 0;
     if (j.cols > WIDE) {
-        k_norm_bwd_wide<SRC, CKPT, VEC><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
+        k_norm_bwd_wide<SRC, FROM, VEC><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         if (j.dweight || j.dbias) {
             parts = wide_parts(j.rows);
             const int64_t per = (j.rows + parts - 1) / parts;
             parts = (j.rows + per - 1) / per;
-            k_norm_cols<SRC, CKPT, VEC><<<dim3((unsigned)((j.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s>>>(j, per);
+            k_norm_cols<SRC, FROM, VEC><<<dim3((unsigned)((j.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s>>>(j, per);
         }
     } else {
         const int64_t groups = bwd_groups(j.rows, j.cols);
         const hipError_t e = by_width(j.cols, [&](auto T, auto N) {
             constexpr int B = T < 256 ? 256 : (int)T;
-            k_norm_bwd<SRC, CKPT, VEC, T, N><<<dim3((unsigned)groups), dim3(B), 0, s>>>(j);
+            k_norm_bwd<SRC, FROM, VEC, T, N><<<dim3((unsigned)groups), dim3(B), 0, s>>>(j);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
@@ -475,10 +475,11 @@ hipError_t launch_norm_fwd(const NormFwdJob& j, hipStream_t s)
 
 hipError_t launch_norm_bwd(const NormBwdJob& j, hipStream_t s)
 {
-    const bool vec = j.cols % 8 == 0;
-    if (j.qx) return j.src == SRC_F32 ? launch_bwd<SRC_F32, true, true>(j, s) : launch_bwd<SRC_BF16, true, true>(j, s);
-    if (j.src == SRC_F32) return vec ? launch_bwd<SRC_F32, false, true>(j, s) : launch_bwd<SRC_F32, false, false>(j, s);
-    return vec ? launch_bwd<SRC_BF16, false, true>(j, s) : launch_bwd<SRC_BF16, false, false>(j, s);
+    auto run = [&](auto src) {
+        if (j.qx) return j.ckpt_fmt == E4M3 ? launch_bwd<src, FROM_E4M3, true>(j, s) : launch_bwd<src, FROM_E5M2, true>(j, s);
+        return j.cols % 8 == 0 ? launch_bwd<src, FROM_TENSOR, true>(j, s) : launch_bwd<src, FROM_TENSOR, false>(j, s);
+    };
+    return j.src == SRC_F32 ? run(std::integral_constant<int, SRC_F32>()) : run(std::integral_constant<int, SRC_BF16>());
 }
 
 }  // namespace mx
