@@ -188,7 +188,7 @@ struct BlockScale {
 template <int FMT>
 __device__ __forceinline__ uint32_t encode4(const BlockScale<FMT>& b, float v0, float v1, float v2, float v3)
 {
-    short2v d = {0, 0};
+    short2v d = __builtin_nondeterministic_value(short2v{});    // both halves are written
     const float c0 = b.clamped(v0), c1 = b.clamped(v1), c2 = b.clamped(v2), c3 = b.clamped(v3);
     if constexpr (FMT == E4M3) {
         d = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(d, c0, c1, b.scale, false);

@@ -209,13 +209,14 @@ hipError_t by_act(int act, F&& f)
 
 // ---------------------------------------------------------------------------
 // k_glu_bwd_dual: workgroups of WR x WC waves walk tiles of 32 WR rows by
-// 32 WC columns of h; a wave takes 32 x 32 of them.  Lane 8 k + m holds rows
-// 4 m .. 4 m + 3 and columns 4 k .. 4 k + 3: a column block is spread over
-// eight neighbouring lanes, a row block over eight lanes 8 apart, so both
-// maxima are three cross-lane steps on registers.  A lane's codes of a row
-// (four columns) or of a column (four rows) are one dword, and go through LDS
-// to leave as whole runs of a row or a column.  The next tile's inputs are
-// loaded into registers while the current tile is encoded.
+// 64 WC columns of h; a wave takes 32 x 64 of them.  Lane 8 k + m holds rows
+// 4 m .. 4 m + 3 and columns 8 k .. 8 k + 7, so that a wave's loads of bf16
+// rows are whole 128-byte lines: a column block is spread over eight
+// neighbouring lanes, a row block over four lanes 8 apart, and both maxima
+// are two or three cross-lane steps on registers.  A lane's codes of a row
+// (eight columns) or of a column (four rows) are two dwords or one, and go
+// through LDS to leave as whole runs of a row or a column.  The next tile's
+// inputs are loaded into registers before the current tile is worked on.
 //
 // Tiles are 128 x 128, so that every input and output line of codes is a
 // whole 128-byte line of one tile: an L2 (4 MiB for 32 CUs) keeps a line for
@@ -225,14 +226,13 @@ hipError_t by_act(int act, F&& f)
 // to 16 tiles at a time through LDS.
 // ---------------------------------------------------------------------------
 
-// the largest key of the eight lanes 8 apart: l ^ 8 (in the 16-lane row), l ^ 16, l ^ 32
+// the largest key of the four lanes 8 apart that hold a row block: l ^ 8 (in
+// the 16-lane row) and l ^ 16
 __device__ __forceinline__ uint32_t row_block_max(uint32_t k)
 {
     k = max(k, dpp<0x128>(k));                 // rotate by 8 in a row of 16
     auto p = __builtin_amdgcn_permlane16_swap(k, k, false, false);
-    k = max((uint32_t)p[0], (uint32_t)p[1]);
-    auto q = __builtin_amdgcn_permlane32_swap(k, k, false, false);
-    return max((uint32_t)q[0], (uint32_t)q[1]);
+    return max((uint32_t)p[0], (uint32_t)p[1]);
 }
 
 // the largest key of eight neighbouring lanes
@@ -247,10 +247,10 @@ __device__ __forceinline__ uint32_t oct_max(uint32_t k)
 // flight), then meets the workgroup.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// the inputs of one lane's 4 x 4 values, as they are in memory
+// the inputs of one lane's 4 x 8 values, as they are in memory
 template <int SRC, bool TENSOR> struct DualRaw;
-template <int SRC> struct DualRaw<SRC, true> { Chunk<SRC, 4> d[4], g[4], u[4]; };
-template <int SRC> struct DualRaw<SRC, false> { Chunk<SRC, 4> d[4]; uint32_t g[4], u[4]; };
+template <int SRC> struct DualRaw<SRC, true> { Chunk<SRC> d[4], g[4], u[4]; };
+template <int SRC> struct DualRaw<SRC, false> { Chunk<SRC> d[4]; uint2 g[4], u[4]; };
 
 // Accesses at base + offset, base the same for the whole wave and offset a
 // lane's, in the form of one scalar address and a 32-bit vector offset.  (The
@@ -272,10 +272,14 @@ __device__ __forceinline__ MX_GLOBAL Unaligned<V>* lane_at(const void* base, uin
 }
 
 template <int SRC>
-__device__ __forceinline__ Chunk<SRC, 4> lane_chunk(const void* base, uint32_t offset)
+__device__ __forceinline__ Chunk<SRC> lane_chunk(const void* base, uint32_t offset)
 {
-    typedef std::conditional_t<SRC == SRC_BF16, dwords2, dwords4> V;
-    return __builtin_bit_cast(Chunk<SRC, 4>, V(lane_at<V>(base, offset)->v));
+    if constexpr (SRC == SRC_BF16) {
+        return __builtin_bit_cast(Chunk<SRC>, dwords4(lane_at<dwords4>(base, offset)->v));
+    } else {
+        struct { dwords4 lo, hi; } w = {lane_at<dwords4>(base, offset)->v, lane_at<dwords4>(base, offset + 16)->v};
+        return __builtin_bit_cast(Chunk<SRC>, w);
+    }
 }
 
 // Places of a lane in the tiles' inputs: byte offsets from a tile's first
@@ -293,32 +297,12 @@ __device__ __forceinline__ void dual_load(const GluBwdJob& a, int64_t row, int64
         r.d[i] = lane_chunk<SRC>((const uint8_t*)a.dh + ((row + i) * a.ld_dh + col) * B, at.d);
         if constexpr (!TENSOR) {
             const int64_t e = (row + i) * a.cols + col;
-            r.g[i] = lane_at<uint32_t>(a.qg + e, at.q)->v;
-            r.u[i] = lane_at<uint32_t>(a.qu + e, at.q)->v;
+            r.g[i] = __builtin_bit_cast(uint2, dwords2(lane_at<dwords2>(a.qg + e, at.q)->v));
+            r.u[i] = __builtin_bit_cast(uint2, dwords2(lane_at<dwords2>(a.qu + e, at.q)->v));
         } else {
             r.g[i] = lane_chunk<SRC>((const uint8_t*)a.gate + ((row + i) * a.ld_gate + col) * B, at.g);
             r.u[i] = lane_chunk<SRC>((const uint8_t*)a.up + ((row + i) * a.ld_up + col) * B, at.u);
         }
-    }
-}
-
-// Blocks of four values per lane: v[j] are the four of block j, key[j] the
-// block's |max| key in every lane that holds a part of it.  Codes and scale
-// bytes of the four blocks.
-template <int FMT>
-__device__ __forceinline__ void encode_blocks(const float (&v)[4][4], const uint32_t (&key)[4], uint32_t (&code)[4],
-                                              uint32_t (&byte)[4])
-{
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const BlockScale<FMT> b(key[j]);
-        code[j] = encode4<FMT>(b, v[j][0], v[j][1], v[j][2], v[j][3]);
-        byte[j] = b.byte;
-    }
-    if (max(max(key[0], key[1]), max(key[2], key[3])) >= NONFINITE) {
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (key[j] >= NONFINITE) code[j] = 0x7F7F7F7Fu, byte[j] = 0xFFu;
     }
 }
 
@@ -327,22 +311,34 @@ __device__ __forceinline__ void encode_blocks(const float (&v)[4][4], const uint
 // different groups of eight banks.
 template <int LB> constexpr int line_bytes() { return LB + 8; }
 
-// codes of the row blocks (v[row][column]) or column blocks (v[column][row])
-// of one tensor: four lines from line0 on, at byte `at` of each; scale bytes
-// of the lines' blocks, SPL to a line, by the lanes that `writes`
-template <int FMT, int LB, int SPL, bool COLUMNS>
-__device__ __forceinline__ void stage_blocks(const float (&v)[4][4], uint8_t* stage, uint8_t* scales, int line0, int at,
-                                             int block, bool writes)
+// Row codes of one tensor's 4 x 8 values per lane to `stage`, eight bytes from
+// `at` in lines line0 .. line0 + 3, and the blocks' scale bytes
+template <int FMT, int LB, int SPL>
+__device__ __forceinline__ void stage_rows(const float (&v)[4][8], uint8_t* stage, uint8_t* scales, int line0, int at,
+                                           int block, bool writes)
 {
-    uint32_t key[4], code[4], byte[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) key[j] = COLUMNS ? oct_max(chunk_key(v[j])) : row_block_max(chunk_key(v[j]));
-    encode_blocks<FMT>(v, key, code, byte);
+    for (int i = 0; i < 4; i++) {
+        const Codes8 c = encode8<FMT>(v[i], row_block_max(chunk_key(v[i])));
+        *(uint2*)(stage + (line0 + i) * line_bytes<LB>() + at) = make_uint2(c.lo, c.hi);
+        if (writes) scales[(line0 + i) * SPL + block] = (uint8_t)c.scale;
+    }
+}
+
+// Column codes: four bytes from `at` in lines line0 .. line0 + 7
+template <int FMT, int LB, int SPL>
+__device__ __forceinline__ void stage_columns(const float (&v)[4][8], uint8_t* stage, uint8_t* scales, int line0, int at,
+                                              int block, bool writes)
+{
 #pragma unroll
-    for (int j = 0; j < 4; j++) *(uint32_t*)(stage + (line0 + j) * line_bytes<LB>() + at) = code[j];
-    if (writes) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) scales[(line0 + j) * SPL + block] = (uint8_t)byte[j];
+    for (int c = 0; c < 8; c++) {
+        const float w[4] = {v[0][c], v[1][c], v[2][c], v[3][c]};
+        const uint32_t key = oct_max(chunk_key(w));
+        const BlockScale<FMT> b(key);
+        uint32_t code = encode4<FMT>(b, w[0], w[1], w[2], w[3]), byte = b.byte;
+        if (key >= NONFINITE) code = 0x7F7F7F7Fu, byte = 0xFFu;
+        *(uint32_t*)(stage + (line0 + c) * line_bytes<LB>() + at) = code;
+        if (writes) scales[(line0 + c) * SPL + block] = (uint8_t)byte;
     }
 }
 
@@ -419,13 +415,14 @@ constexpr int WAIT_VMEM = 0x0F70;       // s_waitcnt vmcnt(0): expcnt and lgkmcn
 template <int SRC, int ACT, int FROM, int FMT, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, DualTiles tiles)
 {
-    constexpr int TR = 32 * WR, TC = 32 * WC, NT = 64 * WR * WC, WB = WINDOW * WC, WS = WB + 16;
+    constexpr int TR = 32 * WR, TC = 64 * WC, NT = 64 * WR * WC, WB = WINDOW * 2 * WC, WS = WB + 16;
     constexpr bool TENSOR = FROM == FROM_TENSOR;
     static_assert(NT >= TC, "a thread per column for its scale bytes");
+    constexpr bool EARLY = !(TENSOR && SRC == SRC_F32);    // two tiles' inputs fit the registers
     __shared__ __align__(16) uint8_t cols[3][TC * line_bytes<TR>()], rows[2][TR * line_bytes<TC>()];
     __shared__ __align__(16) uint8_t col_scales[3][TC * WR], row_scales[2][TR * WS], in_scales[2][TENSOR ? 16 : TR * WS];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, band = wave % WR, part = wave / WR;
-    const int m = lane & 7, k8 = lane >> 3, lr = band * 32 + m * 4, lc = part * 32 + k8 * 4;
+    const int m = lane & 7, k8 = lane >> 3, lr = band * 32 + m * 4, lc = part * 64 + k8 * 8;
     const uint32_t sr = (uint32_t)(a.rows / 32), sc = (uint32_t)(a.cols / 32);
     // this workgroup's run of tiles, along the rows of tiles
     const uint64_t all = (uint64_t)tiles.nx * tiles.ny;
@@ -455,26 +452,30 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
             if constexpr (!TENSOR) {
                 const int tid = thread_here();
                 const int64_t at = r0 * sc + c0 / 32;
-                const int n = (int)min((int64_t)left * WC, (int64_t)sc - c0 / 32);
+                const int n = (int)min((int64_t)left * 2 * WC, (int64_t)sc - c0 / 32);
                 move_row_scales<WB, TR, NT, false>(tid, in_scales[0], (uint8_t*)a.sg + at, sc, nr, n);
                 move_row_scales<WB, TR, NT, false>(tid, in_scales[1], (uint8_t*)a.su + at, sc, nr, n);
                 lds_barrier();
             }
         }
-        const int block = (int)(tx - first) * WC + part;        // this wave's block of the window's rows
-        float g[4][4], u[4][4], h[4][4];
+        const int block = ((int)(tx - first) * WC + part) * 2 + (k8 >> 2);     // the lane's block of the window's rows
+        const DualRaw<SRC, TENSOR> now = raw;
+        uint32_t y1 = ty, x1 = tx + 1;
+        if (x1 == tiles.nx) x1 = 0, y1++;
+        if (EARLY && tile + 1 < end) fetch(y1, x1);
+        float g[4][8], u[4][8], h[4][8];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             if constexpr (!TENSOR) {
-                decode4<FROM>(raw.g[i], in_scales[0][(lr + i) * WS + block], g[i]);
-                decode4<FROM>(raw.u[i], in_scales[1][(lr + i) * WS + block], u[i]);
+                decode8<FROM>(now.g[i], in_scales[0][(lr + i) * WS + block], g[i]);
+                decode8<FROM>(now.u[i], in_scales[1][(lr + i) * WS + block], u[i]);
             } else {
 #pragma unroll
-                for (int c = 0; c < 4; c++) g[i][c] = chunk_value(raw.g[i], c), u[i][c] = chunk_value(raw.u[i], c);
+                for (int c = 0; c < 8; c++) g[i][c] = chunk_value(now.g[i], c), u[i][c] = chunk_value(now.u[i], c);
             }
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                const float dh = chunk_value(raw.d[i], c);
+            for (int c = 0; c < 8; c++) {
+                const float dh = chunk_value(now.d[i], c);
                 float act, slope;
                 gate<ACT, true>(g[i][c], act, slope);
                 h[i][c] = act * u[i][c];
@@ -482,24 +483,15 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
                 u[i][c] = dh * act;
             }
         }
-        uint32_t y1 = ty, x1 = tx + 1;
-        if (x1 == tiles.nx) x1 = 0, y1++;
-        if (tile + 1 < end) fetch(y1, x1);
-        auto transposed = [](const float (&v)[4][4], float (&t)[4][4]) {
-#pragma unroll
-            for (int i = 0; i < 16; i++) t[i & 3][i >> 2] = v[i >> 2][i & 3];
-        };
-        float t[4][4];
-        stage_blocks<FMT, TC, WS, false>(g, rows[0], row_scales[0], lr, lc, block, k8 == 0);
-        stage_blocks<FMT, TC, WS, false>(u, rows[1], row_scales[1], lr, lc, block, k8 == 0);
-        transposed(g, t);
-        stage_blocks<FMT, TR, WR, true>(t, cols[0], col_scales[0], lc, lr, band, m == 0);
-        transposed(u, t);
-        stage_blocks<FMT, TR, WR, true>(t, cols[1], col_scales[1], lc, lr, band, m == 0);
+        if (!EARLY && tile + 1 < end) fetch(y1, x1);
+        const bool row_writer = (k8 & 3) == 0, col_writer = m == 0;
+        stage_rows<FMT, TC, WS>(g, rows[0], row_scales[0], lr, lc, block, row_writer);
+        stage_rows<FMT, TC, WS>(u, rows[1], row_scales[1], lr, lc, block, row_writer);
+        stage_columns<FMT, TR, WR>(g, cols[0], col_scales[0], lc, lr, band, col_writer);
+        stage_columns<FMT, TR, WR>(u, cols[1], col_scales[1], lc, lr, band, col_writer);
         if (a.qh) {
-            transposed(h, t);
-            if (a.h_fmt == E4M3) stage_blocks<E4M3, TR, WR, true>(t, cols[2], col_scales[2], lc, lr, band, m == 0);
-            else stage_blocks<E5M2, TR, WR, true>(t, cols[2], col_scales[2], lc, lr, band, m == 0);
+            if (a.h_fmt == E4M3) stage_columns<E4M3, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
+            else stage_columns<E5M2, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
         }
         // The next tile's inputs have landed, most of a tile's work after they
         // were asked for: waited for here, ahead of this tile's stores, since
@@ -522,8 +514,8 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
             if (a.qh) store_scale_bytes<WR>(a.sh + at, (uint32_t)line * sr, &col_scales[2][line * WR], nr / 32);
         }
         if (--left == 0) {
-            const int64_t at = 2 * r0 * sc + (int64_t)first * WC;
-            const int n = (int)min((int64_t)(tx - first + 1) * WC, (int64_t)sc - (int64_t)first * WC);
+            const int64_t at = 2 * r0 * sc + (int64_t)first * 2 * WC;
+            const int n = (int)min((int64_t)(tx - first + 1) * 2 * WC, (int64_t)sc - (int64_t)first * 2 * WC);
             move_row_scales<WB, TR, NT, true>(tid, row_scales[0], a.s_row + at, 2 * sc, nr, n);
             move_row_scales<WB, TR, NT, true>(tid, row_scales[1], a.s_row + at + sc, 2 * sc, nr, n);
         }
@@ -537,12 +529,12 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
 template <int SRC, int ACT, int FROM, int FMT, int WR, int WC>
 hipError_t run_dual(const GluBwdJob& j, hipStream_t s)
 {
-    const DualTiles n{(uint32_t)((j.cols + 32 * WC - 1) / (32 * WC)), (uint32_t)((j.rows + 32 * WR - 1) / (32 * WR))};
+    const DualTiles n{(uint32_t)((j.cols + 64 * WC - 1) / (64 * WC)), (uint32_t)((j.rows + 32 * WR - 1) / (32 * WR))};
     int dev = 0, cus = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
     if (e != hipSuccess) return e;
-    const int64_t all = (int64_t)n.nx * n.ny, most = (int64_t)cus * (16 / (WR * WC)), grid = all < most ? all : most;
+    const int64_t all = (int64_t)n.nx * n.ny, most = (int64_t)cus * (8 / (WR * WC)), grid = all < most ? all : most;
     k_glu_bwd_dual<SRC, ACT, FROM, FMT, WR, WC><<<dim3((unsigned)grid), dim3(64 * WR * WC), 0, s>>>(j, n);
     return hipGetLastError();
 }
@@ -584,7 +576,7 @@ hipError_t launch_glu_bwd_dual(const GluBwdJob& j, hipStream_t s)
     return by_act(j.act, [&](auto A) {
         return by_source(j, [&](auto from) {
             auto fmt = [&](auto F) {
-                return j.src == SRC_F32 ? run_dual<SRC_F32, A, from, F, 4, 4>(j, s) : run_dual<SRC_BF16, A, from, F, 4, 4>(j, s);
+                return j.src == SRC_F32 ? run_dual<SRC_F32, A, from, F, 4, 2>(j, s) : run_dual<SRC_BF16, A, from, F, 4, 2>(j, s);
             };
             return j.fmt == E4M3 ? fmt(std::integral_constant<int, E4M3>()) : fmt(std::integral_constant<int, E5M2>());
         });
