@@ -414,75 +414,122 @@ def checkpoint(fmt, q: torch.Tensor, s: torch.Tensor) -> Checkpoint:
     return Checkpoint(_fmt(fmt), q, s)
 
 
-def _fits(t: torch.Tensor, shape, dtype, name: str, dense: bool = False) -> torch.Tensor:
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
+def _misfit(t: torch.Tensor, shape, dtype, at: int, name: str, layout: str):
+    """Why t is not what a call needs."""
+    if t.get_device() != at:
+        return ValueError(f"{name} must be on the device of the call's first tensor")
+    if t.dtype is not dtype:
+        return TypeError(f"{name} must be {dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if not (t.is_contiguous() if dense else t.shape[-1] <= 1 or t.stride(-1) == 1):
-        raise ValueError(f"{name} must be contiguous" if dense else f"{name} must have unit column stride")
-    return t
+        return ValueError(f"{name} must have shape {tuple(shape)}")
+    return ValueError(f"{name} must {layout}")
 
 
-def _at(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+# The checks below run on every call, so each looks at a tensor once and
+# returns what the call passes on.
+
+def _matrix(t: torch.Tensor, shape, dtype, at: int, name: str):
+    """(address, row stride in elements) of a matrix of this shape, type and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == at:
+        ld, unit = t.stride()
+        rows, cols = shape
+        if unit == 1 or cols <= 1:
+            return t.data_ptr(), ld if rows > 1 or ld > cols else cols    # one row: any stride will do
+    raise _misfit(t, shape, dtype, at, name, "have unit column stride")
 
 
-def _ld(t: Optional[torch.Tensor]) -> int:
-    """Row stride in elements (that of a single row is its length)."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _maybe_matrix(t: Optional[torch.Tensor], shape, dtype, at: int, name: str):
+    return (None, 0) if t is None else _matrix(t, shape, dtype, at, name)
 
 
-def _out(t, shape, dtype, device, name: str, dense: bool = True) -> torch.Tensor:
-    """The caller's output, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _fits(t, shape, dtype, name, dense)
+def _dense(t: torch.Tensor, shape, dtype, at: int, name: str) -> int:
+    """Address of a contiguous tensor of this shape, type and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == at and t.is_contiguous():
+        return t.data_ptr()
+    raise _misfit(t, shape, dtype, at, name, "be contiguous")
 
 
-def _copy_out(fmt, q, s, shape, device, name: str):
-    """(format, codes, scales) of a row copy to be written; (0, None, None) without a format."""
-    if fmt is None:
-        if q is not None or s is not None:
-            raise ValueError(f"{name} needs a format")
-        return 0, None, None
-    rows, cols = shape
-    return (_fmt(fmt), _out(q, shape, torch.uint8, device, f"{name} codes"),
-            _out(s, (rows, cols // 32), torch.uint8, device, f"{name} scales"))
-
-
-def _copy_in(c: Optional[Checkpoint], shape, name: str):
-    if c is None:
-        return 0, None, None
-    rows, cols = shape
-    return (c.fmt, _fits(c.q, shape, torch.uint8, f"{name} codes", True),
-            _fits(c.s, (rows, cols // 32), torch.uint8, f"{name} scales", True))
-
-
-def _matrix(x: torch.Tensor, name: str) -> int:
+def _source(x: torch.Tensor, name: str) -> int:
     """Source dtype code of a 2-D operand."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    if x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
-    if x.dtype == torch.bfloat16:
+    if x.dtype is torch.bfloat16:
         return MX_SRC_BF16
-    if x.dtype == torch.float32:
+    if x.dtype is torch.float32:
         return MX_SRC_F32
     raise TypeError(f"{name} must be float32 or bfloat16")
 
 
-def _params(weight, bias, cols: int) -> int:
-    """Common dtype code of the parameters."""
-    given = [p for p in (weight, bias) if p is not None]
-    if not given:
-        return 0
-    dtype = given[0].dtype
-    if dtype not in (torch.float32, torch.bfloat16):
+def _out_dtype(dtype, default):
+    """(torch dtype, MX_OUT_* code) of a matrix output."""
+    dtype = default if dtype is None else dtype
+    if dtype is torch.bfloat16:
+        return dtype, MX_OUT_BF16
+    if dtype is torch.float32:
+        return dtype, MX_OUT_F32
+    raise TypeError("out_dtype must be float32 or bfloat16")
+
+
+def _copy_out(fmt, q, s, shape, first, names):
+    """(format code, codes, scales, their addresses) of a row copy to be
+    written, new where the caller gave none; nothing without a format.
+    first: the call's first tensor."""
+    if fmt is None:
+        if q is not None or s is not None:
+            raise ValueError(f"{names[0]} need a format")
+        return 0, None, None, None, None
+    rows, cols = shape
+    blocks = (rows, cols // 32)
+    at = first.get_device()
+    if q is None:
+        q = first.new_empty(shape, dtype=torch.uint8)
+    if s is None:
+        s = first.new_empty(blocks, dtype=torch.uint8)
+    return _fmt(fmt), q, s, _dense(q, shape, torch.uint8, at, names[0]), _dense(s, blocks, torch.uint8, at, names[1])
+
+
+def _copy_in(c: Optional[Checkpoint], shape, at: int, names):
+    """(format code, addresses of codes and scales) of a checkpoint that is read."""
+    if c is None:
+        return 0, None, None
+    rows, cols = shape
+    return (c.fmt, _dense(c.q, shape, torch.uint8, at, names[0]),
+            _dense(c.s, (rows, cols // 32), torch.uint8, at, names[1]))
+
+
+_Y, _X = ("the codes of y", "the scales of y"), ("the checkpoint's codes", "the checkpoint's scales")
+_H = ("the codes of h", "the scales of h")
+_GATE = ("the codes of gate's checkpoint", "the scales of gate's checkpoint")
+_UP = ("the codes of up's checkpoint", "the scales of up's checkpoint")
+_ROW = ("the codes of the row copy", "the scales of the row copy")
+_COL = ("the codes of the column copy", "the scales of the column copy")
+
+
+def _params(weight, bias, cols: int, at: int):
+    """(addresses, common dtype code) of the parameters."""
+    given = weight if weight is not None else bias
+    if given is None:
+        return None, None, 0
+    dtype = given.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise TypeError("weight and bias must be float32 or bfloat16")
-    for p in given:
-        _fits(p, (cols,), dtype, "weight and bias", True)
-    return MX_SRC_F32 if dtype == torch.float32 else MX_SRC_BF16
+    return (None if weight is None else _dense(weight, (cols,), dtype, at, "weight"),
+            None if bias is None else _dense(bias, (cols,), dtype, at, "bias"),
+            MX_SRC_F32 if dtype is torch.float32 else MX_SRC_BF16)
+
+
+# the handle of a device's current stream; torch.cuda.current_stream() builds
+# an object around it (2.7 us against 0.1 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, at: int) -> int:
+    """The given stream, or the current one."""
+    if at < 0 or at != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current GPU")
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(at) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def mx_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -493,29 +540,39 @@ def mx_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias
     """RMS norm or layer norm of x (+ residual), with y as a tensor, as an MX
     row copy (y_fmt) or both, and the 8-bit checkpoint (ckpt_fmt) of what was
     normalised.  stats: also mean (layer norm) and rstd for the backward."""
-    src = _matrix(x, "x")
-    shape, dev, k = x.shape, x.device, NORMS[kind]
-    if residual is not None:
-        _fits(residual, shape, x.dtype, "residual")
-        sum_out = _out(sum_out, shape, x.dtype, dev, "sum_out", False)
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("out_dtype must be float32 or bfloat16")
-    y = _out(y, shape, out_dtype, dev, "y", False) if write_y else None
-    yf, qy, sy = _copy_out(y_fmt, qy, sy, shape, dev, "y")
-    cf, qx, sx = _copy_out(ckpt_fmt, qx, sx, shape, dev, "checkpoint")
+    src = _source(x, "x")
+    shape, dtype, at, k = x.shape, x.dtype, x.get_device(), NORMS[kind]
+    rows, cols = shape
+    px, ld_x = _matrix(x, shape, dtype, at, "x")
+    pres, ld_res = _maybe_matrix(residual, shape, dtype, at, "residual")
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+    elif sum_out is None:
+        sum_out = x.new_empty(shape, dtype=dtype)
+    psum, ld_sum = _maybe_matrix(sum_out, shape, dtype, at, "sum_out")
+    out_dtype, out = _out_dtype(out_dtype, dtype)
+    if not write_y:
+        y = None
+    elif y is None:
+        y = x.new_empty(shape, dtype=out_dtype)
+    py, ld_y = _maybe_matrix(y, shape, out_dtype, at, "y")
+    yf, qy, sy, pqy, psy = _copy_out(y_fmt, qy, sy, shape, x, _Y)
+    cf, qx, sx, pqx, psx = _copy_out(ckpt_fmt, qx, sx, shape, x, _X)
+    pw, pb, pd = _params(weight, bias, cols, at)
+    pmean = prstd = None
     if stats:
-        rstd = _out(rstd, shape[:1], torch.float32, dev, "rstd")
-        mean = _out(mean, shape[:1], torch.float32, dev, "mean") if k == MX_NORM_LAYER else None
+        rstd = x.new_empty(rows, dtype=torch.float32) if rstd is None else rstd
+        prstd = _dense(rstd, (rows,), torch.float32, at, "rstd")
     else:
-        mean = rstd = None
-    _check(load().mx_norm_forward(
-        _at(x), _ld(x), _at(residual), _ld(residual), src, shape[0], shape[1], k, _at(weight), _at(bias),
-        _params(weight, bias, shape[1]), eps, _at(sum_out), _ld(sum_out), _at(y), _ld(y),
-        MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, yf, _at(qy), _at(sy), cf, _at(qx), _at(sx),
-        _at(mean), _at(rstd), _stream(stream)))
+        rstd = None
+    if stats and k == MX_NORM_LAYER:
+        mean = x.new_empty(rows, dtype=torch.float32) if mean is None else mean
+        pmean = _dense(mean, (rows,), torch.float32, at, "mean")
+    else:
+        mean = None
+    _check(load().mx_norm_forward(px, ld_x, pres, ld_res, src, rows, cols, k, pw, pb, pd, eps, psum, ld_sum, py,
+                                  ld_y, out, yf, pqy, psy, cf, pqx, psx, pmean, prstd, _stream_on(stream, at)))
     return NormForward(y, sum_out, qy, sy, qx, sx, mean, rstd)
 
 
@@ -527,30 +584,37 @@ def mx_norm_backward(dy: torch.Tensor, rstd: torch.Tensor, x: Optional[torch.Ten
     """Gradients of mx_norm_forward from what it normalised (x) or from its
     checkpoint; dsum is a gradient of the same tensor from elsewhere, added
     to dx.  dweight and dbias are float32."""
-    src = _matrix(dy, "dy")
-    shape, dev, k = dy.shape, dy.device, NORMS[kind]
-    if x is not None:
-        _fits(x, shape, dy.dtype, "x")
-    cf, qx, sx = _copy_in(ckpt, shape, "checkpoint")
-    _fits(rstd, shape[:1], torch.float32, "rstd", True)
-    if k == MX_NORM_LAYER and mean is not None:
-        _fits(mean, shape[:1], torch.float32, "mean", True)
-    if dsum is not None:
-        _fits(dsum, shape, dy.dtype, "dsum")
-    dx = _out(dx, shape, dy.dtype, dev, "dx", False)
-    dweight = _out(dweight, shape[1:], torch.float32, dev, "dweight") if want_dweight else None
-    dbias = _out(dbias, shape[1:], torch.float32, dev, "dbias") if want_dbias else None
-    L, nbytes = load(), 0
+    src = _source(dy, "dy")
+    shape, dtype, at, k = dy.shape, dy.dtype, dy.get_device(), NORMS[kind]
+    rows, cols = shape
+    pdy, ld_dy = _matrix(dy, shape, dtype, at, "dy")
+    px, ld_x = _maybe_matrix(x, shape, dtype, at, "x")
+    cf, pqx, psx = _copy_in(ckpt, shape, at, _X)
+    prstd = _dense(rstd, (rows,), torch.float32, at, "rstd")
+    pmean = _dense(mean, (rows,), torch.float32, at, "mean") if k == MX_NORM_LAYER and mean is not None else None
+    pds, ld_ds = _maybe_matrix(dsum, shape, dtype, at, "dsum")
+    dx = dy.new_empty(shape, dtype=dtype) if dx is None else dx
+    pdx, ld_dx = _matrix(dx, shape, dtype, at, "dx")
+    pw, _, pd = _params(weight, None, cols, at)
+    pdw = pdb = pwork = None
+    nbytes = 0
+    L = load()
+    if want_dweight:
+        dweight = dy.new_empty(cols, dtype=torch.float32) if dweight is None else dweight
+        pdw = _dense(dweight, (cols,), torch.float32, at, "dweight")
+    else:
+        dweight = None
+    if want_dbias:
+        dbias = dy.new_empty(cols, dtype=torch.float32) if dbias is None else dbias
+        pdb = _dense(dbias, (cols,), torch.float32, at, "dbias")
+    else:
+        dbias = None
     if want_dweight or want_dbias:
         if work is None:
-            nbytes = int(L.mx_norm_backward_workspace_bytes(shape[0], shape[1]))
-            work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        else:
-            nbytes = work.numel() * work.element_size()
-    _check(L.mx_norm_backward(
-        _at(dy), _ld(dy), src, shape[0], shape[1], _at(x), _ld(x), cf, _at(qx), _at(sx), _at(mean), _at(rstd), k,
-        _at(weight), _params(weight, None, shape[1]), _at(dsum), _ld(dsum), _at(dx), _ld(dx), _at(dweight),
-        _at(dbias), _at(work), nbytes, _stream(stream)))
+            work = dy.new_empty(L.mx_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8)
+        nbytes, pwork = work.numel() * work.element_size(), work.data_ptr()
+    _check(L.mx_norm_backward(pdy, ld_dy, src, rows, cols, px, ld_x, cf, pqx, psx, pmean, prstd, k, pw, pd, pds,
+                              ld_ds, pdx, ld_dx, pdw, pdb, pwork, nbytes, _stream_on(stream, at)))
     return NormBackward(dx, dweight, dbias)
 
 
@@ -559,37 +623,35 @@ def mx_glu_forward(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", writ
                    qg=None, sg=None, qu=None, su=None, stream=None) -> GluForward:
     """h = act(gate) * up as a tensor, as an MX row copy (h_fmt) or both, and
     the 8-bit checkpoints (ckpt_fmt) of gate and up."""
-    src = _matrix(gate, "gate")
-    shape, dev = gate.shape, gate.device
-    _fits(up, shape, gate.dtype, "up")
-    out_dtype = gate.dtype if out_dtype is None else out_dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("out_dtype must be float32 or bfloat16")
-    h = _out(h, shape, out_dtype, dev, "h", False) if write_h else None
-    hf, qh, sh = _copy_out(h_fmt, qh, sh, shape, dev, "h")
-    cf, qg, sg = _copy_out(ckpt_fmt, qg, sg, shape, dev, "gate checkpoint")
-    _, qu, su = _copy_out(ckpt_fmt, qu, su, shape, dev, "up checkpoint")
-    _check(load().mx_glu_forward(
-        _at(gate), _ld(gate), _at(up), _ld(up), src, shape[0], shape[1], ACTS[act], _at(h), _ld(h),
-        MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, hf, _at(qh), _at(sh), cf, _at(qg), _at(sg),
-        _at(qu), _at(su), _stream(stream)))
+    src = _source(gate, "gate")
+    shape, dtype, at = gate.shape, gate.dtype, gate.get_device()
+    rows, cols = shape
+    pg, ld_g = _matrix(gate, shape, dtype, at, "gate")
+    pu, ld_u = _matrix(up, shape, dtype, at, "up")
+    out_dtype, out = _out_dtype(out_dtype, dtype)
+    if not write_h:
+        h = None
+    elif h is None:
+        h = gate.new_empty(shape, dtype=out_dtype)
+    ph, ld_h = _maybe_matrix(h, shape, out_dtype, at, "h")
+    hf, qh, sh, pqh, psh = _copy_out(h_fmt, qh, sh, shape, gate, _H)
+    cf, qg, sg, pqg, psg = _copy_out(ckpt_fmt, qg, sg, shape, gate, _GATE)
+    _, qu, su, pqu, psu = _copy_out(ckpt_fmt, qu, su, shape, gate, _UP)
+    _check(load().mx_glu_forward(pg, ld_g, pu, ld_u, src, rows, cols, ACTS[act], ph, ld_h, out, hf, pqh, psh, cf,
+                                 pqg, psg, pqu, psu, _stream_on(stream, at)))
     return GluForward(h, qh, sh, qg, sg, qu, su)
 
 
 def _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act):
     """The shared leading arguments of the backward calls."""
-    src = _matrix(dh, "dh")
-    shape = dh.shape
-    if gate is not None:
-        _fits(gate, shape, dh.dtype, "gate")
-    if up is not None:
-        _fits(up, shape, dh.dtype, "up")
-    gf, qg, sg = _copy_in(gate_ckpt, shape, "gate checkpoint")
-    uf, qu, su = _copy_in(up_ckpt, shape, "up checkpoint")
+    src = _source(dh, "dh")
+    shape, dtype, at = dh.shape, dh.dtype, dh.get_device()
+    gf, pqg, psg = _copy_in(gate_ckpt, shape, at, _GATE)
+    uf, pqu, psu = _copy_in(up_ckpt, shape, at, _UP)
     if gate_ckpt is not None and up_ckpt is not None and gf != uf:
         raise ValueError("the checkpoints of gate and up must have one format")
-    return (_at(dh), _ld(dh), src, shape[0], shape[1], _at(gate), _ld(gate), _at(up), _ld(up), gf, _at(qg),
-            _at(sg), _at(qu), _at(su), ACTS[act])
+    return (*_matrix(dh, shape, dtype, at, "dh"), src, *shape, *_maybe_matrix(gate, shape, dtype, at, "gate"),
+            *_maybe_matrix(up, shape, dtype, at, "up"), gf, pqg, psg, pqu, psu, ACTS[act])
 
 
 def mx_glu_backward(dh: torch.Tensor, gate: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None,
@@ -599,12 +661,16 @@ def mx_glu_backward(dh: torch.Tensor, gate: Optional[torch.Tensor] = None, up: O
     """Gradients of mx_glu_forward from gate and up, or from their
     checkpoints; recompute_h: also h = act(gate) * up."""
     head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
-    shape, dev = dh.shape, dh.device
-    dgate = _out(dgate, shape, dh.dtype, dev, "dgate", False)
-    dup = _out(dup, shape, dh.dtype, dev, "dup", False)
-    h = _out(h, shape, dh.dtype, dev, "h", False) if recompute_h else None
-    _check(load().mx_glu_backward(*head, _at(dgate), _ld(dgate), _at(dup), _ld(dup), _at(h), _ld(h),
-                                  _stream(stream)))
+    shape, dtype, at = dh.shape, dh.dtype, dh.get_device()
+    dgate = dh.new_empty(shape, dtype=dtype) if dgate is None else dgate
+    dup = dh.new_empty(shape, dtype=dtype) if dup is None else dup
+    if not recompute_h:
+        h = None
+    elif h is None:
+        h = dh.new_empty(shape, dtype=dtype)
+    _check(load().mx_glu_backward(*head, *_matrix(dgate, shape, dtype, at, "dgate"),
+                                  *_matrix(dup, shape, dtype, at, "dup"), *_maybe_matrix(h, shape, dtype, at, "h"),
+                                  _stream_on(stream, at)))
     return GluBackward(dgate, dup, h)
 
 
@@ -616,10 +682,10 @@ def mx_glu_backward_dual_layout(dh: torch.Tensor, gate: Optional[torch.Tensor] =
     """mx_glu_backward straight into the backward GEMMs' operands: the row and
     column copies of [dgate | dup] and (h_fmt) the column copy of h."""
     head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
-    (rows, cols), dev = dh.shape, dh.device
-    f, q_row, s_row = _copy_out(fmt, q_row, s_row, (rows, 2 * cols), dev, "row copy")
-    _, q_col, s_col = _copy_out(fmt, q_col, s_col, (2 * cols, rows), dev, "column copy")
-    hf, qh_col, sh_col = _copy_out(h_fmt, qh_col, sh_col, (cols, rows), dev, "column copy of h")
-    _check(load().mx_glu_backward_dual_layout(*head, f, _at(q_row), _at(s_row), _at(q_col), _at(s_col), hf,
-                                              _at(qh_col), _at(sh_col), _stream(stream)))
+    rows, cols = dh.shape
+    f, q_row, s_row, pqr, psr = _copy_out(fmt, q_row, s_row, (rows, 2 * cols), dh, _ROW)
+    _, q_col, s_col, pqc, psc = _copy_out(fmt, q_col, s_col, (2 * cols, rows), dh, _COL)
+    hf, qh_col, sh_col, pqh, psh = _copy_out(h_fmt, qh_col, sh_col, (cols, rows), dh, _H)
+    _check(load().mx_glu_backward_dual_layout(*head, f, pqr, psr, pqc, psc, hf, pqh, psh,
+                                              _stream_on(stream, dh.get_device())))
     return GluBackwardDual(q_row, s_row, q_col, s_col, qh_col, sh_col)

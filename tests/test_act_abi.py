@@ -178,6 +178,11 @@ R4 = torch.zeros(4)
     (lambda: mx.mx_glu_backward(X, gate=X, up=X, dgate=X.t()), ValueError),
     (lambda: mx.mx_glu_backward_dual_layout(X, X, X, q_row=CODES), ValueError),
     (lambda: mx.mx_glu_backward_dual_layout(X, X, X, qh_col=CODES), ValueError),
+    (lambda: mx.mx_norm_forward(X), ValueError),                      # host tensors
+    (lambda: mx.mx_norm_backward(X, R4, x=X), ValueError),
+    (lambda: mx.mx_glu_forward(X, X), ValueError),
+    (lambda: mx.mx_glu_backward(X, gate=X, up=X), ValueError),
+    (lambda: mx.mx_norm_forward(X, weight=torch.empty(64, device="meta")), ValueError),
 ])
 def test_binding_refuses(call, error):
     with pytest.raises(error):
