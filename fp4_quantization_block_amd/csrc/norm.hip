@@ -33,65 +33,106 @@ namespace mx {
 
 namespace {
 
-// A row spread over T lanes: element i of lane t's chunk j
-template <bool VEC, int T>
-__device__ __forceinline__ int64_t col_of(int64_t j, int t, int i)
-{
-    return VEC ? (j * T + t) * 8 + i : (j * 8 + i) * T + t;
-}
+// How a row is spread over T lanes (chunk j of lane t):
+//   WHOLE    eight consecutive elements; the row is a multiple of eight
+//   OVERLAP  the same for any row of at least eight: the last chunk is the
+//            row's last eight elements, so that some of them are held twice.
+//            They come out the same twice, and are left out of one lane's
+//            part of a sum.
+//   STRIDED  elements t, t + T, ... t + 7 T of a run of 8 T: any row, and
+//            no element twice (an output may be written over an input)
+enum : int { WHOLE, OVERLAP, STRIDED };
 
-// chunk j of a row as fp32.  Places past the row read the row's first
-// elements (VEC) or element (else): the caller leaves them out.
-template <int SRC, bool VEC, int T>
-__device__ __forceinline__ void load_row(const void* row, int64_t j, int t, int64_t cols, float (&v)[8])
+template <int MODE, int T>
+struct Cols {
+    int64_t c0, c;          // where chunk j would begin, and where it is read
+    bool in;                // whether any of it is in the row (else it reads the row's beginning)
+    int64_t cols;
+    __device__ __forceinline__ Cols(int64_t j, int t, int64_t n) : cols(n)
+    {
+        c0 = MODE == STRIDED ? j * 8 * T + t : (j * T + t) * 8;
+        in = c0 < n;
+        c = !in ? 0 : MODE == OVERLAP && c0 + 8 > n ? n - 8 : c0;
+    }
+    __device__ __forceinline__ int64_t at(int i) const          // column of element i, clamped into the row
+    {
+        if constexpr (MODE == STRIDED) return c0 + i * T < cols ? c0 + i * T : 0;
+        else return c + i;
+    }
+    __device__ __forceinline__ bool counts(int i) const          // whether element i is this lane's in a sum
+    {
+        if constexpr (MODE == STRIDED) return c0 + i * T < cols;
+        else if constexpr (MODE == OVERLAP) return in && c + i >= c0;
+        else return in;
+    }
+};
+
+// a chunk as it is in memory
+template <int SRC, int MODE> struct RowRaw { uint32_t w[MODE == STRIDED ? 8 : 2 * ElemT<SRC>::bytes]; };
+
+template <int SRC, int MODE, int T>
+__device__ __forceinline__ RowRaw<SRC, MODE> load_raw(const void* row, const Cols<MODE, T>& p)
 {
-    if constexpr (VEC) {
-        const int64_t c = col_of<VEC, T>(j, t, 0);
-        const Chunk<SRC> w = load_chunk<SRC>(row, c < cols ? c : 0);
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = chunk_value<SRC>(w, i);
-    } else {
+    RowRaw<SRC, MODE> r;
+    if constexpr (MODE == STRIDED) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const int64_t c = col_of<VEC, T>(j, t, i);
-            v[i] = load_elem<SRC>(row, c < cols ? c : 0);
+            if constexpr (SRC == SRC_BF16) r.w[i] = ((const uint16_t*)row)[p.at(i)];
+            else r.w[i] = ((const uint32_t*)row)[p.at(i)];
         }
+    } else {
+        r = __builtin_bit_cast(decltype(r), load_chunk<SRC>(row, p.c));
+    }
+    return r;
+}
+
+template <int SRC, int MODE>
+__device__ __forceinline__ void raw_values(const RowRaw<SRC, MODE>& r, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        if constexpr (SRC == SRC_F32) v[i] = __uint_as_float(r.w[i]);
+        else if constexpr (MODE == STRIDED) v[i] = bf16_lo(r.w[i]);
+        else v[i] = (i & 1) ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
     }
 }
 
-template <int SRC, bool VEC, int T>
-__device__ __forceinline__ void store_row(void* row, int64_t j, int t, int64_t cols, const float (&v)[8])
+template <int SRC, int MODE, int T>
+__device__ __forceinline__ void load_row(const void* row, const Cols<MODE, T>& p, float (&v)[8])
 {
-    if constexpr (VEC) {
-        const int64_t c = col_of<VEC, T>(j, t, 0);
-        if (c < cols) store_chunk<SRC>(row, c, make_chunk<SRC>(v));
-    } else {
+    raw_values(load_raw<SRC>(row, p), v);
+}
+
+template <int SRC, int MODE, int T>
+__device__ __forceinline__ void store_row(void* row, const Cols<MODE, T>& p, const float (&v)[8])
+{
+    if constexpr (MODE == STRIDED) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int64_t c = col_of<VEC, T>(j, t, i);
-            if (c < cols) store_elem<SRC>(row, c, v[i]);
-        }
+        for (int i = 0; i < 8; i++)
+            if (p.counts(i)) store_elem<SRC>(row, p.at(i), v[i]);
+    } else {
+        if (p.in) store_chunk<SRC>(row, p.c, make_chunk<SRC>(v));
     }
 }
 
-template <bool VEC, int T>
-__device__ __forceinline__ void load_param(const void* p, int f32, int64_t j, int t, int64_t cols, float (&v)[8])
+template <int MODE, int T>
+__device__ __forceinline__ void load_param(const void* q, int f32, const Cols<MODE, T>& p, float (&v)[8])
 {
-    if (f32) load_row<SRC_F32, VEC, T>(p, j, t, cols, v);
-    else load_row<SRC_BF16, VEC, T>(p, j, t, cols, v);
+    if (f32) load_row<SRC_F32>(q, p, v);
+    else load_row<SRC_BF16>(q, p, v);
 }
 
-// the sum of f(i) over the chunk's elements that are in the row
-template <bool VEC, int T, class F>
-__device__ __forceinline__ float chunk_sum(int64_t j, int t, int64_t cols, F&& f)
+// the sum of f(i) over the elements of the chunk that count
+template <int MODE, int T, class F>
+__device__ __forceinline__ float chunk_sum(const Cols<MODE, T>& p, F&& f)
 {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const float x = f(i);
-        s += VEC || col_of<VEC, T>(j, t, i) < cols ? x : 0.0f;
+        s += MODE == WHOLE || p.counts(i) ? x : 0.0f;
     }
-    return !VEC || col_of<VEC, T>(j, t, 0) < cols ? s : 0.0f;
+    return MODE != WHOLE || p.in ? s : 0.0f;
 }
 
 template <int SRC>
@@ -101,8 +142,8 @@ __device__ __forceinline__ const void* row_of(const void* p, int64_t row, int64_
 }
 
 // y of one chunk, and its outputs
-template <int SRC, bool VEC, int T>
-__device__ __forceinline__ void finish_chunk(const NormFwdJob& a, int64_t row, int64_t j, int t, const float (&s)[8],
+template <int SRC, int MODE, int T>
+__device__ __forceinline__ void finish_chunk(const NormFwdJob& a, int64_t row, const Cols<MODE, T>& p, const float (&s)[8],
                                              float mean, float rstd)
 {
     if (!a.y && !a.qy) return;
@@ -111,47 +152,43 @@ __device__ __forceinline__ void finish_chunk(const NormFwdJob& a, int64_t row, i
     for (int i = 0; i < 8; i++) y[i] = (s[i] - mean) * rstd;
     if (a.weight) {
         float w[8];
-        load_param<VEC, T>(a.weight, a.param_f32, j, t, a.cols, w);
+        load_param(a.weight, a.param_f32, p, w);
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] *= w[i];
     }
     if (a.bias) {
         float b[8];
-        load_param<VEC, T>(a.bias, a.param_f32, j, t, a.cols, b);
+        load_param(a.bias, a.param_f32, p, b);
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] += b[i];
     }
     if (a.y) {
-        if (a.out_f32) store_row<SRC_F32, VEC, T>((float*)a.y + row * a.ld_y, j, t, a.cols, y);
-        else store_row<SRC_BF16, VEC, T>((uint16_t*)a.y + row * a.ld_y, j, t, a.cols, y);
+        if (a.out_f32) store_row<SRC_F32>((float*)a.y + row * a.ld_y, p, y);
+        else store_row<SRC_BF16>((uint16_t*)a.y + row * a.ld_y, p, y);
     }
-    if constexpr (VEC) {
-        const int64_t c = col_of<VEC, T>(j, t, 0);
-        if (a.qy) encode_row_chunk(a.y_fmt, y, c < a.cols, row * a.cols + c, a.qy, a.sy);
-    }
+    if constexpr (MODE == WHOLE)
+        if (a.qy) encode_row_chunk(a.y_fmt, y, p.in, row * a.cols + p.c0, a.qy, a.sy);
 }
 
 // s = x (+ residual) of one chunk, with the sum and the checkpoint written
-template <int SRC, bool VEC, int T>
-__device__ __forceinline__ void residual_and_checkpoint(const NormFwdJob& a, int64_t row, int64_t j, int t,
+template <int SRC, int MODE, int T>
+__device__ __forceinline__ void residual_and_checkpoint(const NormFwdJob& a, int64_t row, const Cols<MODE, T>& p,
                                                         float (&s)[8])
 {
     if (a.residual) {
         float r[8];
-        load_row<SRC, VEC, T>(row_of<SRC>(a.residual, row, a.ld_res), j, t, a.cols, r);
+        load_row<SRC>(row_of<SRC>(a.residual, row, a.ld_res), p, r);
 #pragma unroll
         for (int i = 0; i < 8; i++) s[i] = rounded<SRC>(s[i] + r[i]);
-        store_row<SRC, VEC, T>((void*)row_of<SRC>(a.sum, row, a.ld_sum), j, t, a.cols, s);
+        store_row<SRC>((void*)row_of<SRC>(a.sum, row, a.ld_sum), p, s);
     }
-    if constexpr (VEC) {
-        const int64_t c = col_of<VEC, T>(j, t, 0);
-        if (a.qx) encode_row_chunk(a.ckpt_fmt, s, c < a.cols, row * a.cols + c, a.qx, a.sx);
-    }
+    if constexpr (MODE == WHOLE)
+        if (a.qx) encode_row_chunk(a.ckpt_fmt, s, p.in, row * a.cols + p.c0, a.qx, a.sx);
 }
 
 __device__ __forceinline__ float inv_sqrt(float v) { return 1.0f / __builtin_sqrtf(v); }
 
-template <int SRC, bool VEC, int T, int N>
+template <int SRC, int MODE, int T, int N>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_fwd(NormFwdJob a)
 {
     constexpr int RPB = T < 256 ? 256 / T : 1;
@@ -159,48 +196,52 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_fwd(NormFwdJob a)
     const int t = (int)threadIdx.x % T;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / T;
     if (row >= a.rows) return;               // whole waves, and only where no barrier follows (T = 64)
+    typedef Cols<MODE, T> P;
     float s[N][8];
 #pragma unroll
-    for (int j = 0; j < N; j++) load_row<SRC, VEC, T>(row_of<SRC>(a.x, row, a.ld_x), j, t, a.cols, s[j]);
+    for (int j = 0; j < N; j++) load_row<SRC>(row_of<SRC>(a.x, row, a.ld_x), P(j, t, a.cols), s[j]);
 #pragma unroll
-    for (int j = 0; j < N; j++) residual_and_checkpoint<SRC, VEC, T>(a, row, j, t, s[j]);
+    for (int j = 0; j < N; j++) residual_and_checkpoint<SRC>(a, row, P(j, t, a.cols), s[j]);
     const float n = (float)a.cols;
     float mean = 0.0f;
     if (a.layer) {
         float p = 0.0f;
 #pragma unroll
-        for (int j = 0; j < N; j++) p += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return s[j][i]; });
+        for (int j = 0; j < N; j++) p += chunk_sum(P(j, t, a.cols), [&](int i) { return s[j][i]; });
         mean = group_sum<T>(p, red[0]) / n;
     }
     float p = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; j++)
-        p += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { const float c = s[j][i] - mean; return c * c; });
+        p += chunk_sum(P(j, t, a.cols), [&](int i) { const float c = s[j][i] - mean; return c * c; });
     const float rstd = inv_sqrt(group_sum<T>(p, red[1]) / n + a.eps);
     if (t == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
 #pragma unroll
-    for (int j = 0; j < N; j++) finish_chunk<SRC, VEC, T>(a, row, j, t, s[j], mean, rstd);
+    for (int j = 0; j < N; j++) finish_chunk<SRC>(a, row, P(j, t, a.cols), s[j], mean, rstd);
 }
 
-template <int SRC, bool VEC>
+template <int SRC, int MODE>
 __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormFwdJob a)
 {
     constexpr int T = 1024;
+    typedef Cols<MODE, T> P;
     __shared__ float red[2][T / 64];
     const int t = (int)threadIdx.x;
     const int64_t row = blockIdx.x, steps = (a.cols + T * 8 - 1) / (T * 8);
-    // after the first pass s is in the sum, written by the same thread
+    // after the first pass s is in the sum, written by the same thread (and
+    // by a second one, in OVERLAP, with the same values)
     const void* xr = row_of<SRC>(a.x, row, a.ld_x);
     const void* sr = a.residual ? row_of<SRC>(a.sum, row, a.ld_sum) : xr;
     float p = 0.0f;
     for (int64_t j = 0; j < steps; j++) {
         float s[8];
-        load_row<SRC, VEC, T>(xr, j, t, a.cols, s);
-        residual_and_checkpoint<SRC, VEC, T>(a, row, j, t, s);
-        p += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return a.layer ? s[i] : s[i] * s[i]; });
+        const P at(j, t, a.cols);
+        load_row<SRC>(xr, at, s);
+        residual_and_checkpoint<SRC>(a, row, at, s);
+        p += chunk_sum(at, [&](int i) { return a.layer ? s[i] : s[i] * s[i]; });
     }
     const float n = (float)a.cols;
     p = group_sum<T>(p, red[0]) / n;
@@ -210,8 +251,9 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormFwdJob a)
         p = 0.0f;
         for (int64_t j = 0; j < steps; j++) {
             float s[8];
-            load_row<SRC, VEC, T>(sr, j, t, a.cols, s);
-            p += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { const float c = s[i] - mean; return c * c; });
+            const P at(j, t, a.cols);
+            load_row<SRC>(sr, at, s);
+            p += chunk_sum(at, [&](int i) { const float c = s[i] - mean; return c * c; });
         }
         var = group_sum<T>(p, red[1]) / n;
     }
@@ -222,8 +264,9 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormFwdJob a)
     }
     for (int64_t j = 0; j < steps; j++) {
         float s[8];
-        load_row<SRC, VEC, T>(sr, j, t, a.cols, s);
-        finish_chunk<SRC, VEC, T>(a, row, j, t, s, mean, rstd);
+        const P at(j, t, a.cols);
+        load_row<SRC>(sr, at, s);
+        finish_chunk<SRC>(a, row, at, s, mean, rstd);
     }
 }
 
@@ -231,143 +274,237 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormFwdJob a)
 // backward
 // ---------------------------------------------------------------------------
 
-// chunk j of the normalised input (s - m) r, from the tensor or the checkpoint
-template <int SRC, int FROM, bool VEC, int T>
-__device__ __forceinline__ void load_unit(const NormBwdJob& a, int64_t row, int64_t j, int t, float mean, float rstd,
-                                          float (&h)[8])
+// the inputs of one chunk of a row, as they are in memory
+template <int SRC, int FROM, int MODE>
+struct BwdRaw {
+    RowRaw<SRC, MODE> dy, x, dsum;
+    uint2 q;
+    uint8_t s;
+};
+
+template <int SRC, int FROM, int MODE, int T>
+__device__ __forceinline__ void load_bwd(const NormBwdJob& a, int64_t row, const Cols<MODE, T>& p, bool dsum,
+                                         BwdRaw<SRC, FROM, MODE>& r)
 {
+    r.dy = load_raw<SRC>(row_of<SRC>(a.dy, row, a.ld_dy), p);
     if constexpr (FROM != FROM_TENSOR) {
-        const int64_t c = col_of<VEC, T>(j, t, 0), e = row * a.cols + (c < a.cols ? c : 0);
-        decode8<FROM>(*(const uint2*)(a.qx + e), a.sx[e >> 5], h);
+        const int64_t e = row * a.cols + p.c;
+        r.q = *(const uint2*)(a.qx + e);
+        r.s = a.sx[e >> 5];
     } else {
-        load_row<SRC, VEC, T>(row_of<SRC>(a.x, row, a.ld_x), j, t, a.cols, h);
+        r.x = load_raw<SRC>(row_of<SRC>(a.x, row, a.ld_x), p);
     }
+    if (dsum) r.dsum = load_raw<SRC>(row_of<SRC>(a.dsum, row, a.ld_dsum), p);
+}
+
+// h = (s - m) r of one chunk
+template <int SRC, int FROM, int MODE>
+__device__ __forceinline__ void unit_values(const BwdRaw<SRC, FROM, MODE>& r, float mean, float rstd, float (&h)[8])
+{
+    if constexpr (FROM != FROM_TENSOR) decode8<FROM>(r.q, r.s, h);
+    else raw_values<SRC, MODE>(r.x, h);
 #pragma unroll
     for (int i = 0; i < 8; i++) h[i] = (h[i] - mean) * rstd;
 }
 
 // dx of one chunk from g, h and the two means
-template <int SRC, bool VEC, int T>
-__device__ __forceinline__ void store_dx(const NormBwdJob& a, int64_t row, int64_t j, int t, const float (&g)[8],
-                                         const float (&h)[8], float rstd, float mg, float mgh)
+template <int SRC, int FROM, int MODE, int T>
+__device__ __forceinline__ void store_dx(const NormBwdJob& a, int64_t row, const Cols<MODE, T>& p,
+                                         const BwdRaw<SRC, FROM, MODE>& r, const float (&g)[8], const float (&h)[8],
+                                         float rstd, float mg, float mgh)
 {
     float d[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) d[i] = rstd * (g[i] - mg - h[i] * mgh);
     if (a.dsum) {
-        float r[8];
-        load_row<SRC, VEC, T>(row_of<SRC>(a.dsum, row, a.ld_dsum), j, t, a.cols, r);
+        float e[8];
+        raw_values<SRC, MODE>(r.dsum, e);
 #pragma unroll
-        for (int i = 0; i < 8; i++) d[i] += r[i];
+        for (int i = 0; i < 8; i++) d[i] += e[i];
     }
-    store_row<SRC, VEC, T>((void*)row_of<SRC>(a.dx, row, a.ld_dx), j, t, a.cols, d);
+    store_row<SRC>((void*)row_of<SRC>(a.dx, row, a.ld_dx), p, d);
 }
 
-template <int SRC, int FROM, bool VEC, int T, int N>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_bwd(NormBwdJob a)
+// Workgroups of RPB groups of T threads, a row per group at a time.  The next
+// row's inputs are loaded before the current row is worked on, and the weight
+// stays in registers, except where 1024 threads leave 128 registers each.
+template <int T> constexpr int bwd_block() { return T < 512 ? 512 : T; }
+
+template <int SRC, int FROM, int MODE, int T, int N>
+__global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
 {
-    constexpr int RPB = T < 256 ? 256 / T : 1;
-    __shared__ float red[2][2][T < 256 ? 1 : T / 64];
-    const int t = (int)threadIdx.x % T;
-    const int64_t part = (int64_t)blockIdx.x * RPB + threadIdx.x / T, parts = (int64_t)gridDim.x * RPB;
+    constexpr int RPB = bwd_block<T>() / T, W = T / 64;
+    typedef Cols<MODE, T> P;
+    __shared__ float red[2][2][RPB][W];
+    __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? N * T * 8 : 1];
+    const int t = (int)threadIdx.x % T, sub = (int)threadIdx.x / T;
+    constexpr bool AHEAD = T < 1024;
     float w[N][8], dw[N][8], db[N][8];
+    auto weight = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[j][i] = 1.0f;
+        if (a.weight) load_param(a.weight, a.param_f32, P(j, t, a.cols), w[j]);
+    };
 #pragma unroll
     for (int j = 0; j < N; j++) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) w[j][i] = 1.0f, dw[j][i] = 0.0f, db[j][i] = 0.0f;
-        if (a.weight) load_param<VEC, T>(a.weight, a.param_f32, j, t, a.cols, w[j]);
+        for (int i = 0; i < 8; i++) dw[j][i] = 0.0f, db[j][i] = 0.0f;
+        if (AHEAD) weight(j);
     }
     const float n = (float)a.cols;
-    // the two sums alternate between two halves of `red`: a wave writes one
-    // half again only after the barrier of the row between, which every wave
-    // reaches after reading it
-    int half = 0;
-    for (int64_t row = part; row < a.rows; row += parts, half ^= 1) {
-        const float mean = a.layer ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+    BwdRaw<SRC, FROM, MODE> raw[N];
+    float mean = 0.0f, rstd = 0.0f;
+    auto fetch = [&](int64_t row) {
+        rstd = a.rstd[row];
+        mean = a.layer ? a.mean[row] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; j++) load_bwd(a, row, P(j, t, a.cols), a.dsum != nullptr, raw[j]);
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + sub;
+    if (AHEAD && row < a.rows) fetch(row);
+    // The sums alternate between two halves of `red`: a wave writes one half
+    // again only after the barrier of the step between, which every wave
+    // reaches after reading it.  A group whose rows have ended keeps meeting
+    // the others' barriers.
+    for (int half = 0; row - sub < a.rows; row += step, half ^= 1) {
+        const bool live = row < a.rows;
+        if (!AHEAD && live) fetch(row);
+        const float m = mean, r = rstd;
+        BwdRaw<SRC, FROM, MODE> now[N];
+#pragma unroll
+        for (int j = 0; j < N; j++) now[j] = raw[j];
+        if (AHEAD && row + step < a.rows) fetch(row + step);
         float g[N][8], h[N][8], pg = 0.0f, pgh = 0.0f;
+        if (live) {
 #pragma unroll
-        for (int j = 0; j < N; j++) load_row<SRC, VEC, T>(row_of<SRC>(a.dy, row, a.ld_dy), j, t, a.cols, g[j]);
+            for (int j = 0; j < N; j++) {
+                const P p(j, t, a.cols);
+                if (!AHEAD) weight(j);
+                raw_values<SRC, MODE>(now[j].dy, g[j]);
+                unit_values(now[j], m, r, h[j]);
 #pragma unroll
-        for (int j = 0; j < N; j++) load_unit<SRC, FROM, VEC, T>(a, row, j, t, mean, rstd, h[j]);
-#pragma unroll
-        for (int j = 0; j < N; j++) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                dw[j][i] += g[j][i] * h[j][i];
-                db[j][i] += g[j][i];
-                g[j][i] *= w[j][i];
+                for (int i = 0; i < 8; i++) {
+                    dw[j][i] += g[j][i] * h[j][i];
+                    db[j][i] += g[j][i];
+                    g[j][i] *= w[j][i];
+                }
+                pgh += chunk_sum(p, [&](int i) { return g[j][i] * h[j][i]; });
+                pg += chunk_sum(p, [&](int i) { return g[j][i]; });
             }
-            pgh += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return g[j][i] * h[j][i]; });
-            pg += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return g[j][i]; });
+            pgh = wave_sum(pgh);
+            if (a.layer) pg = wave_sum(pg);
         }
-        const float mgh = group_sum<T>(pgh, red[half][0]) / n;
-        const float mg = a.layer ? group_sum<T>(pg, red[half][1]) / n : 0.0f;
+        if constexpr (W > 1) {
+            if ((threadIdx.x & 63) == 0) {
+                red[half][0][sub][t >> 6] = pgh;
+                red[half][1][sub][t >> 6] = pg;
+            }
+            __syncthreads();
+            pgh = red[half][0][sub][0];
+            pg = red[half][1][sub][0];
 #pragma unroll
-        for (int j = 0; j < N; j++) store_dx<SRC, VEC, T>(a, row, j, t, g[j], h[j], rstd, mg, mgh);
-    }
+            for (int i = 1; i < W; i++) {
+                pgh += red[half][0][sub][i];
+                pg += red[half][1][sub][i];
+            }
+        }
+        if (live) {
+            const float mgh = pgh / n, mg = a.layer ? pg / n : 0.0f;
 #pragma unroll
-    for (int j = 0; j < N; j++) {
-        if (a.dweight) store_row<SRC_F32, VEC, T>(a.work + part * a.cols, j, t, a.cols, dw[j]);
-        if (a.dbias) store_row<SRC_F32, VEC, T>(a.work + ((a.dweight ? parts : 0) + part) * a.cols, j, t, a.cols, db[j]);
+            for (int j = 0; j < N; j++) store_dx(a, row, P(j, t, a.cols), now[j], g[j], h[j], r, mg, mgh);
+        }
     }
+    // the groups' sums added in their order, and this workgroup's partial row
+    auto finish = [&](float (&v)[N][8], float* out) {
+        if constexpr (RPB > 1) {
+            __syncthreads();
+            if (sub > 0) {
+#pragma unroll
+                for (int j = 0; j < N; j++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) part[sub - 1][(j * 8 + i) * T + t] = v[j][i];
+            }
+            __syncthreads();
+            if (sub > 0) return;
+#pragma unroll
+            for (int k = 0; k < RPB - 1; k++)
+#pragma unroll
+                for (int j = 0; j < N; j++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v[j][i] += part[k][(j * 8 + i) * T + t];
+        }
+#pragma unroll
+        for (int j = 0; j < N; j++) store_row<SRC_F32>(out, P(j, t, a.cols), v[j]);
+    };
+    if (a.dweight) finish(dw, a.work + blockIdx.x * a.cols);
+    if (a.dbias) finish(db, a.work + ((a.dweight ? gridDim.x : 0) + blockIdx.x) * a.cols);
 }
 
-template <int SRC, int FROM, bool VEC>
+template <int SRC, int FROM, int MODE>
 __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormBwdJob a)
 {
     constexpr int T = 1024;
+    typedef Cols<MODE, T> P;
     __shared__ float red[2][T / 64];
     const int t = (int)threadIdx.x;
     const int64_t row = blockIdx.x, steps = (a.cols + T * 8 - 1) / (T * 8);
     const float mean = a.layer ? a.mean[row] : 0.0f, rstd = a.rstd[row], n = (float)a.cols;
-    const void* dyr = row_of<SRC>(a.dy, row, a.ld_dy);
     float pg = 0.0f, pgh = 0.0f;
-    auto gradient = [&](int64_t j, float (&g)[8]) {
-        load_row<SRC, VEC, T>(dyr, j, t, a.cols, g);
+    auto values = [&](const P& p, const BwdRaw<SRC, FROM, MODE>& r, float (&g)[8], float (&h)[8]) {
+        raw_values<SRC, MODE>(r.dy, g);
         if (a.weight) {
             float w[8];
-            load_param<VEC, T>(a.weight, a.param_f32, j, t, a.cols, w);
+            load_param(a.weight, a.param_f32, p, w);
 #pragma unroll
             for (int i = 0; i < 8; i++) g[i] *= w[i];
         }
+        unit_values(r, mean, rstd, h);
     };
     for (int64_t j = 0; j < steps; j++) {
         float g[8], h[8];
-        gradient(j, g);
-        load_unit<SRC, FROM, VEC, T>(a, row, j, t, mean, rstd, h);
-        pgh += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return g[i] * h[i]; });
-        pg += chunk_sum<VEC, T>(j, t, a.cols, [&](int i) { return g[i]; });
+        const P p(j, t, a.cols);
+        BwdRaw<SRC, FROM, MODE> r;
+        load_bwd(a, row, p, false, r);
+        values(p, r, g, h);
+        pgh += chunk_sum(p, [&](int i) { return g[i] * h[i]; });
+        pg += chunk_sum(p, [&](int i) { return g[i]; });
     }
     const float mgh = group_sum<T>(pgh, red[0]) / n;
     const float mg = a.layer ? group_sum<T>(pg, red[1]) / n : 0.0f;
     for (int64_t j = 0; j < steps; j++) {
         float g[8], h[8];
-        gradient(j, g);
-        load_unit<SRC, FROM, VEC, T>(a, row, j, t, mean, rstd, h);
-        store_dx<SRC, VEC, T>(a, row, j, t, g, h, rstd, mg, mgh);
+        const P p(j, t, a.cols);
+        BwdRaw<SRC, FROM, MODE> r;
+        load_bwd(a, row, p, a.dsum != nullptr, r);
+        values(p, r, g, h);
+        store_dx(a, row, p, r, g, h, rstd, mg, mgh);
     }
 }
 
 // Partial sums of dw and db over the rows of one part, a strip of 512
 // columns per wave: grid (strips / 4, parts)
-template <int SRC, int FROM, bool VEC>
+template <int SRC, int FROM, int MODE>
 __global__ __launch_bounds__(256) void k_norm_cols(NormBwdJob a, int64_t rows_per_part)
 {
     constexpr int T = 64;
     const int t = (int)threadIdx.x & 63;
     const int64_t j = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), part = blockIdx.y, parts = gridDim.y;
     if (j * T * 8 >= a.cols) return;
+    const Cols<MODE, T> p(j, t, a.cols);
     float dw[8] = {}, db[8] = {};
     const int64_t end = min((part + 1) * rows_per_part, a.rows);
     for (int64_t row = part * rows_per_part; row < end; row++) {
         float dy[8], h[8];
-        load_row<SRC, VEC, T>(row_of<SRC>(a.dy, row, a.ld_dy), j, t, a.cols, dy);
-        load_unit<SRC, FROM, VEC, T>(a, row, j, t, a.layer ? a.mean[row] : 0.0f, a.rstd[row], h);
+        BwdRaw<SRC, FROM, MODE> r;
+        load_bwd(a, row, p, false, r);
+        raw_values<SRC, MODE>(r.dy, dy);
+        unit_values(r, a.layer ? a.mean[row] : 0.0f, a.rstd[row], h);
 #pragma unroll
         for (int i = 0; i < 8; i++) dw[i] += dy[i] * h[i], db[i] += dy[i];
     }
-    if (a.dweight) store_row<SRC_F32, VEC, T>(a.work + part * a.cols, j, t, a.cols, dw);
-    if (a.dbias) store_row<SRC_F32, VEC, T>(a.work + ((a.dweight ? parts : 0) + part) * a.cols, j, t, a.cols, db);
+    if (a.dweight) store_row<SRC_F32>(a.work + part * a.cols, p, dw);
+    if (a.dbias) store_row<SRC_F32>(a.work + ((a.dweight ? parts : 0) + part) * a.cols, p, db);
 }
 
 // dw (blockIdx.y 0) and db (1, or 0 without dw): 32 columns per workgroup, 32
@@ -380,8 +517,16 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(const float* work, int64_t
     const int64_t c = (int64_t)blockIdx.x * 32 + x;
     const float* p = work + (int64_t)blockIdx.y * parts * cols;
     float s = 0.0f;
-    if (c < cols)
-        for (int64_t r = y; r < parts; r += 32) s += p[r * cols + c];
+    if (c < cols) {
+        // four partial rows in flight a thread
+        float v[4] = {};
+        int64_t r = y;
+        for (; r + 96 < parts; r += 128)
+#pragma unroll
+            for (int k = 0; k < 4; k++) v[k] += p[(r + 32 * k) * cols + c];
+        for (; r < parts; r += 32) v[0] += p[r * cols + c];
+        s = (v[0] + v[1]) + (v[2] + v[3]);
+    }
     sum[y][x] = s;
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
@@ -404,51 +549,48 @@ hipError_t by_width(int64_t cols, F&& f)
 
 constexpr int64_t WIDE = 16384;        // rows beyond this do not stay in registers
 
-template <int SRC, bool VEC>
+template <int SRC, int MODE>
 hipError_t launch_fwd(const NormFwdJob& j, hipStream_t s)
 {
     if (j.cols > WIDE) {
-        k_norm_fwd_wide<SRC, VEC><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
+        k_norm_fwd_wide<SRC, MODE><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
         return hipGetLastError();
     }
     return by_width(j.cols, [&](auto T, auto N) {
         constexpr int B = T < 256 ? 256 : (int)T, RPB = B / T;
-        k_norm_fwd<SRC, VEC, T, N><<<dim3((unsigned)((j.rows + RPB - 1) / RPB)), dim3(B), 0, s>>>(j);
+        k_norm_fwd<SRC, MODE, T, N><<<dim3((unsigned)((j.rows + RPB - 1) / RPB)), dim3(B), 0, s>>>(j);
         return hipGetLastError();
     });
 }
 
-// workgroups of the backward kernel, and the rows each of its workgroups takes at a time
-int64_t bwd_groups(int64_t rows, int64_t cols)
-{
-    const int64_t rpb = cols <= 512 ? 4 : 1, want = (rows + rpb - 1) / rpb;
-    return want < 512 ? want : 512;
-}
+// Workgroups (partial rows) of the backward: two for each CU, if there are
+// rows for them
+constexpr int64_t MOST_PARTS = 512;
 
 int64_t wide_parts(int64_t rows) { return rows < 64 ? rows : 64; }
 
-template <int SRC, int FROM, bool VEC>
+template <int SRC, int FROM, int MODE>
 hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
 {
     int64_t parts = 0;
     if (j.cols > WIDE) {
-        k_norm_bwd_wide<SRC, FROM, VEC><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
+        k_norm_bwd_wide<SRC, FROM, MODE><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         if (j.dweight || j.dbias) {
             parts = wide_parts(j.rows);
             const int64_t per = (j.rows + parts - 1) / parts;
             parts = (j.rows + per - 1) / per;
-            k_norm_cols<SRC, FROM, VEC><<<dim3((unsigned)((j.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s>>>(j, per);
+            k_norm_cols<SRC, FROM, MODE><<<dim3((unsigned)((j.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s>>>(j, per);
         }
     } else {
-        const int64_t groups = bwd_groups(j.rows, j.cols);
         const hipError_t e = by_width(j.cols, [&](auto T, auto N) {
-            constexpr int B = T < 256 ? 256 : (int)T;
-            k_norm_bwd<SRC, FROM, VEC, T, N><<<dim3((unsigned)groups), dim3(B), 0, s>>>(j);
+            constexpr int RPB = bwd_block<T>() / T;
+            parts = (j.rows + RPB - 1) / RPB;
+            parts = parts < MOST_PARTS ? parts : MOST_PARTS;
+            k_norm_bwd<SRC, FROM, MODE, T, N><<<dim3((unsigned)parts), dim3(bwd_block<T>()), 0, s>>>(j);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;
-        parts = groups * (j.cols <= 512 ? 4 : 1);
     }
     if (j.dweight || j.dbias) {
         const bool both = j.dweight && j.dbias;
@@ -458,26 +600,36 @@ hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
     return hipGetLastError();
 }
 
+// f(how the rows are spread): `in_place` where an output is written over an input
+template <class F>
+hipError_t by_mode(int64_t cols, bool in_place, F&& f)
+{
+    if (cols % 8 == 0) return f(std::integral_constant<int, WHOLE>());
+    if (cols > 8 && !in_place) return f(std::integral_constant<int, OVERLAP>());
+    return f(std::integral_constant<int, STRIDED>());
+}
+
 }  // namespace
 
 int64_t norm_bwd_partials(int64_t rows, int64_t cols)
 {
     if (cols > WIDE) return wide_parts(rows);
-    return bwd_groups(rows, cols) * (cols <= 512 ? 4 : 1);
+    return rows < MOST_PARTS ? rows : MOST_PARTS;
 }
 
 hipError_t launch_norm_fwd(const NormFwdJob& j, hipStream_t s)
 {
-    const bool vec = j.cols % 8 == 0;
-    if (j.src == SRC_F32) return vec ? launch_fwd<SRC_F32, true>(j, s) : launch_fwd<SRC_F32, false>(j, s);
-    return vec ? launch_fwd<SRC_BF16, true>(j, s) : launch_fwd<SRC_BF16, false>(j, s);
+    const bool in_place = j.residual && (j.sum == j.x || j.sum == j.residual);
+    return by_mode(j.cols, in_place, [&](auto mode) {
+        return j.src == SRC_F32 ? launch_fwd<SRC_F32, mode>(j, s) : launch_fwd<SRC_BF16, mode>(j, s);
+    });
 }
 
 hipError_t launch_norm_bwd(const NormBwdJob& j, hipStream_t s)
 {
     auto run = [&](auto src) {
-        if (j.qx) return j.ckpt_fmt == E4M3 ? launch_bwd<src, FROM_E4M3, true>(j, s) : launch_bwd<src, FROM_E5M2, true>(j, s);
-        return j.cols % 8 == 0 ? launch_bwd<src, FROM_TENSOR, true>(j, s) : launch_bwd<src, FROM_TENSOR, false>(j, s);
+        if (j.qx) return j.ckpt_fmt == E4M3 ? launch_bwd<src, FROM_E4M3, WHOLE>(j, s) : launch_bwd<src, FROM_E5M2, WHOLE>(j, s);
+        return by_mode(j.cols, j.dx == j.dy || j.dx == j.dsum || j.dx == j.x, [&](auto mode) { return launch_bwd<src, FROM_TENSOR, mode>(j, s); });
     };
     return j.src == SRC_F32 ? run(std::integral_constant<int, SRC_F32>()) : run(std::integral_constant<int, SRC_BF16>());
 }
