@@ -3,12 +3,12 @@
 // blocks encoded and decoded by the four lanes that hold them, wave and
 // workgroup sums in a fixed order, and the gate functions with their slopes.
 //
-// Chunks.  VEC kernels (row lengths that are a multiple of 8) give a lane
-// eight consecutive elements, 16 bytes of bf16 or 32 of fp32; rows may start
-// at any element, since the loads and stores are declared with the element's
-// alignment and gfx950 takes 16-byte accesses at any of them.  The other
-// kernels give lane t the elements t, t + T, ... t + 7T, so that a wave's
-// 2- or 4-byte accesses are consecutive whatever the row length.
+// Chunks.  A lane takes eight consecutive elements at a time, 16 bytes of bf16
+// or 32 of fp32; rows may start at any element, since the loads and stores are
+// declared with the element's alignment and gfx950 takes 16-byte accesses at
+// any of them.  Rows whose length is no multiple of eight end in a chunk that
+// overlaps the one before; the few cases that cannot have an element twice
+// (an output over an input, rows under eight) take elements one by one.
 #pragma once
 #include "mx_device.h"
 

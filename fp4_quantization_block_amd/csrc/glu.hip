@@ -41,27 +41,38 @@ __device__ __forceinline__ uint32_t quotient(const FastDiv& f, uint32_t n)
     return (t + ((n - t) >> f.s1)) >> f.s2;
 }
 
-// Places of a thread: VEC: eight consecutive elements of chunk `id`; else the
-// elements id * 2048 + i * 256 + thread.  `units` counts chunks or elements.
-template <bool VEC>
+// Places of a thread:
+//   WHOLE    the eight consecutive elements of chunk `id`; rows are multiples
+//            of eight
+//   OVERLAP  the same for any row of at least eight: a row's last chunk is
+//            its last eight elements, some of which the chunk before has too,
+//            with the same results
+//   STRIDED  elements id * 2048 + i * 256 + thread: any row, no element twice
+//            (an output may be written over an input)
+// `units` counts chunks (WHOLE, OVERLAP) or elements.
+enum : int { WHOLE, OVERLAP, STRIDED };
+
+template <int MODE>
 struct Place {
-    uint32_t row[VEC ? 1 : 8], col[VEC ? 1 : 8];
-    bool ok[VEC ? 1 : 8];
-    __device__ __forceinline__ Place(const FastDiv& per_row, uint32_t units)
+    static constexpr int NP = MODE == STRIDED ? 8 : 1;
+    uint32_t row[NP], col[NP];
+    bool ok[NP];
+    __device__ __forceinline__ Place(const FastDiv& per_row, uint32_t units, uint32_t cols)
     {
 #pragma unroll
-        for (int i = 0; i < (VEC ? 1 : 8); i++) {
-            uint32_t u = VEC ? blockIdx.x * 256u + threadIdx.x : blockIdx.x * 2048u + 256u * i + threadIdx.x;
+        for (int i = 0; i < NP; i++) {
+            uint32_t u = MODE == STRIDED ? blockIdx.x * 2048u + 256u * i + threadIdx.x : blockIdx.x * 256u + threadIdx.x;
             ok[i] = u < units;
             u = ok[i] ? u : 0u;
             row[i] = quotient(per_row, u);
-            col[i] = (u - row[i] * per_row.d) * (VEC ? 8u : 1u);
+            col[i] = (u - row[i] * per_row.d) * (MODE == STRIDED ? 1u : 8u);
+            if (MODE == OVERLAP) col[i] = min(col[i], cols - 8u);
         }
     }
     template <int SRC>
     __device__ __forceinline__ void load(const void* p, int64_t ld, float (&v)[8]) const
     {
-        if constexpr (VEC) {
+        if constexpr (MODE != STRIDED) {
             const Chunk<SRC> c = load_chunk<SRC>(p, row[0] * ld + col[0]);
 #pragma unroll
             for (int i = 0; i < 8; i++) v[i] = chunk_value<SRC>(c, i);
@@ -73,7 +84,7 @@ struct Place {
     template <int SRC>
     __device__ __forceinline__ void store(void* p, int64_t ld, const float (&v)[8]) const
     {
-        if constexpr (VEC) {
+        if constexpr (MODE != STRIDED) {
             if (ok[0]) store_chunk<SRC>(p, row[0] * ld + col[0], make_chunk<SRC>(v));
         } else {
 #pragma unroll
@@ -81,14 +92,14 @@ struct Place {
                 if (ok[i]) store_elem<SRC>(p, row[i] * ld + col[i], v[i]);
         }
     }
-    // place in a dense row copy (VEC)
+    // place in a dense row copy (WHOLE)
     __device__ __forceinline__ int64_t dense(int64_t cols) const { return row[0] * cols + col[0]; }
 };
 
-template <int SRC, int ACT, bool VEC>
+template <int SRC, int ACT, int MODE>
 __global__ __launch_bounds__(256) void k_glu_fwd(GluFwdJob a, FastDiv per_row, uint32_t units)
 {
-    const Place<VEC> at(per_row, units);
+    const Place<MODE> at(per_row, units, (uint32_t)a.cols);
     float g[8], u[8], h[8];
     at.template load<SRC>(a.gate, a.ld_gate, g);
     at.template load<SRC>(a.up, a.ld_up, u);
@@ -102,7 +113,7 @@ __global__ __launch_bounds__(256) void k_glu_fwd(GluFwdJob a, FastDiv per_row, u
         if (a.out_f32) at.template store<SRC_F32>(a.h, a.ld_h, h);
         else at.template store<SRC_BF16>(a.h, a.ld_h, h);
     }
-    if constexpr (VEC) {
+    if constexpr (MODE == WHOLE) {
         const int64_t e = at.dense(a.cols);
         if (a.qh) encode_row_chunk(a.h_fmt, h, at.ok[0], e, a.qh, a.sh);
         if (a.qg) {
@@ -112,10 +123,10 @@ __global__ __launch_bounds__(256) void k_glu_fwd(GluFwdJob a, FastDiv per_row, u
     }
 }
 
-template <int SRC, int ACT, int FROM, bool VEC>
+template <int SRC, int ACT, int FROM, int MODE>
 __global__ __launch_bounds__(256) void k_glu_bwd(GluBwdJob a, FastDiv per_row, uint32_t units)
 {
-    const Place<VEC> at(per_row, units);
+    const Place<MODE> at(per_row, units, (uint32_t)a.cols);
     float d[8], g[8], u[8], h[8];
     at.template load<SRC>(a.dh, a.ld_dh, d);
     if constexpr (FROM != FROM_TENSOR) {
@@ -143,19 +154,27 @@ __global__ __launch_bounds__(256) void k_glu_bwd(GluBwdJob a, FastDiv per_row, u
 
 // Launches of at most 2^31 elements: the rows of a larger tensor are taken in
 // slices, since the kernels count places in 32 bits.
-template <bool VEC, class F>
+template <int MODE, class F>
 hipError_t sliced(int64_t rows, int64_t cols, F&& f)
 {
-    const int64_t per_row = VEC ? cols / 8 : cols;
-    const int64_t most = ((int64_t)1 << 31) / per_row < rows ? ((int64_t)1 << 31) / per_row : rows;
+    const int64_t per_row = MODE == STRIDED ? cols : (cols + 7) / 8, most = ((int64_t)1 << 31) / per_row;
     const FastDiv d = fast_div((uint32_t)per_row);
     for (int64_t r = 0; r < rows; r += most) {
         const int64_t n = rows - r < most ? rows - r : most, units = n * per_row;
-        const int64_t per_group = VEC ? 256 : 2048;
+        const int64_t per_group = MODE == STRIDED ? 2048 : 256;
         f(r, n, d, (uint32_t)units, dim3((unsigned)((units + per_group - 1) / per_group)));
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+// f(how the rows are taken): `in_place` where an output is written over an input
+template <class F>
+hipError_t by_mode(int64_t cols, bool in_place, F&& f)
+{
+    if (cols % 8 == 0) return f(std::integral_constant<int, WHOLE>());
+    if (cols > 8 && !in_place) return f(std::integral_constant<int, OVERLAP>());
+    return f(std::integral_constant<int, STRIDED>());
 }
 
 template <class T>
@@ -164,10 +183,10 @@ void advance(T*& p, int64_t bytes)
     if (p) p = (T*)((uint8_t*)p + bytes);
 }
 
-template <int SRC, int ACT, bool VEC>
+template <int SRC, int ACT, int MODE>
 hipError_t run_fwd(const GluFwdJob& job, hipStream_t s)
 {
-    return sliced<VEC>(job.rows, job.cols, [&](int64_t r, int64_t n, FastDiv d, uint32_t units, dim3 grid) {
+    return sliced<MODE>(job.rows, job.cols, [&](int64_t r, int64_t n, FastDiv d, uint32_t units, dim3 grid) {
         GluFwdJob j = job;
         constexpr int64_t B = ElemT<SRC>::bytes;
         j.rows = n;
@@ -176,14 +195,14 @@ hipError_t run_fwd(const GluFwdJob& job, hipStream_t s)
         advance(j.h, r * j.ld_h * (j.out_f32 ? 4 : 2));
         for (uint8_t** q : {&j.qh, &j.qg, &j.qu}) advance(*q, r * j.cols);
         for (uint8_t** q : {&j.sh, &j.sg, &j.su}) advance(*q, r * (j.cols / 32));
-        k_glu_fwd<SRC, ACT, VEC><<<grid, dim3(256), 0, s>>>(j, d, units);
+        k_glu_fwd<SRC, ACT, MODE><<<grid, dim3(256), 0, s>>>(j, d, units);
     });
 }
 
-template <int SRC, int ACT, int FROM, bool VEC>
+template <int SRC, int ACT, int FROM, int MODE>
 hipError_t run_bwd(const GluBwdJob& job, hipStream_t s)
 {
-    return sliced<VEC>(job.rows, job.cols, [&](int64_t r, int64_t n, FastDiv d, uint32_t units, dim3 grid) {
+    return sliced<MODE>(job.rows, job.cols, [&](int64_t r, int64_t n, FastDiv d, uint32_t units, dim3 grid) {
         GluBwdJob j = job;
         constexpr int64_t B = ElemT<SRC>::bytes;
         j.rows = n;
@@ -195,7 +214,7 @@ hipError_t run_bwd(const GluBwdJob& job, hipStream_t s)
         advance(j.h, r * j.ld_h * B);
         for (const uint8_t** q : {&j.qg, &j.qu}) advance(*q, r * j.cols);
         for (const uint8_t** q : {&j.sg, &j.su}) advance(*q, r * (j.cols / 32));
-        k_glu_bwd<SRC, ACT, FROM, VEC><<<grid, dim3(256), 0, s>>>(j, d, units);
+        k_glu_bwd<SRC, ACT, FROM, MODE><<<grid, dim3(256), 0, s>>>(j, d, units);
     });
 }
 
@@ -552,21 +571,25 @@ hipError_t by_source(const GluBwdJob& j, F&& f)
 
 hipError_t launch_glu_fwd(const GluFwdJob& j, hipStream_t s)
 {
-    const bool vec = j.cols % 8 == 0;
     return by_act(j.act, [&](auto A) {
-        if (j.src == SRC_F32) return vec ? run_fwd<SRC_F32, A, true>(j, s) : run_fwd<SRC_F32, A, false>(j, s);
-        return vec ? run_fwd<SRC_BF16, A, true>(j, s) : run_fwd<SRC_BF16, A, false>(j, s);
+        return by_mode(j.cols, false, [&](auto mode) {
+            return j.src == SRC_F32 ? run_fwd<SRC_F32, A, mode>(j, s) : run_fwd<SRC_BF16, A, mode>(j, s);
+        });
     });
 }
 
 hipError_t launch_glu_bwd(const GluBwdJob& j, hipStream_t s)
 {
+    bool in_place = false;
+    for (const void* out : {(const void*)j.dgate, (const void*)j.dup, (const void*)j.h})
+        in_place |= out && (out == j.dh || out == j.gate || out == j.up);
     return by_act(j.act, [&](auto A) {
         return by_source(j, [&](auto from) {
-            if constexpr (from == FROM_TENSOR) {
-                if (j.cols % 8 != 0) return j.src == SRC_F32 ? run_bwd<SRC_F32, A, from, false>(j, s) : run_bwd<SRC_BF16, A, from, false>(j, s);
-            }
-            return j.src == SRC_F32 ? run_bwd<SRC_F32, A, from, true>(j, s) : run_bwd<SRC_BF16, A, from, true>(j, s);
+            auto run = [&](auto mode) {
+                return j.src == SRC_F32 ? run_bwd<SRC_F32, A, from, mode>(j, s) : run_bwd<SRC_BF16, A, from, mode>(j, s);
+            };
+            if constexpr (from == FROM_TENSOR) return by_mode(j.cols, in_place, run);
+            else return run(std::integral_constant<int, WHOLE>());
         });
     });
 }

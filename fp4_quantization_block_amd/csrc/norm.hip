@@ -189,10 +189,10 @@ __device__ __forceinline__ void residual_and_checkpoint(const NormFwdJob& a, int
 __device__ __forceinline__ float inv_sqrt(float v) { return 1.0f / __builtin_sqrtf(v); }
 
 template <int SRC, int MODE, int T, int N>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_fwd(NormFwdJob a)
+__global__ __launch_bounds__(T < 128 ? 256 : T) void k_norm_fwd(NormFwdJob a)
 {
-    constexpr int RPB = T < 256 ? 256 / T : 1;
-    __shared__ float red[2][T < 256 ? 1 : T / 64];
+    constexpr int RPB = T < 128 ? 256 / T : 1;
+    __shared__ float red[2][T / 64];
     const int t = (int)threadIdx.x % T;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / T;
     if (row >= a.rows) return;               // whole waves, and only where no barrier follows (T = 64)
@@ -327,8 +327,9 @@ __device__ __forceinline__ void store_dx(const NormBwdJob& a, int64_t row, const
 
 // Workgroups of RPB groups of T threads, a row per group at a time.  The next
 // row's inputs are loaded before the current row is worked on, and the weight
-// stays in registers, except where 1024 threads leave 128 registers each.
-template <int T> constexpr int bwd_block() { return T < 512 ? 512 : T; }
+// stays in registers, except where 1024 threads (128 registers each) hold two
+// chunks.
+template <int T> constexpr int bwd_block() { return T <= 256 ? 512 : T; }
 
 template <int SRC, int FROM, int MODE, int T, int N>
 __global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
@@ -338,7 +339,7 @@ __global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
     __shared__ float red[2][2][RPB][W];
     __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? N * T * 8 : 1];
     const int t = (int)threadIdx.x % T, sub = (int)threadIdx.x / T;
-    constexpr bool AHEAD = T < 1024;
+    constexpr bool AHEAD = N == 1;
     float w[N][8], dw[N][8], db[N][8];
     auto weight = [&](int j) {
 #pragma unroll
@@ -536,15 +537,28 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(const float* work, int64_t
     if (y == 0 && c < cols) (blockIdx.y ? out1 : out0)[c] = sum[0][x];
 }
 
-// Threads and chunks per row: the fewest threads that hold it in registers.
-template <class F>
+// Threads per row, one chunk each where 1024 threads hold the row so.  Against
+// 256 threads with 2 to 4 chunks each (64 and 512 threads in the backward),
+// bf16 with a checkpoint: the forward 32768 x 1024 50.5 us against 52.8, 8192 x
+// 4096 50.4 against 52.9, 8192 x 8192 105.7 against 114.4; the backward 44.1
+// against 65.9, 44.8 against 46.9, 94.4 against 95.0.
+// 640 threads are for the forward alone (8192 x 5120: 71.5 us against 72.5 with
+// 768; the backward 63.4 against 60.2).
+template <bool BACKWARD, class F>
 hipError_t by_width(int64_t cols, F&& f)
 {
-    if (cols <= 512) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
-    if (cols <= 2048) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-    if (cols <= 4096) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-    if (cols <= 8192) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
-    return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 2> two;
+    if (cols <= 64 * 8) return f(std::integral_constant<int, 64>(), one);
+    if (cols <= 128 * 8) return f(std::integral_constant<int, 128>(), one);
+    if (cols <= 256 * 8) return f(std::integral_constant<int, 256>(), one);
+    if (cols <= 384 * 8) return f(std::integral_constant<int, 384>(), one);
+    if (cols <= 512 * 8) return f(std::integral_constant<int, 512>(), one);
+    if constexpr (!BACKWARD)
+        if (cols <= 640 * 8) return f(std::integral_constant<int, 640>(), one);
+    if (cols <= 768 * 8) return f(std::integral_constant<int, 768>(), one);
+    if (cols <= 1024 * 8) return f(std::integral_constant<int, 1024>(), one);
+    return f(std::integral_constant<int, 1024>(), two);
 }
 
 constexpr int64_t WIDE = 16384;        // rows beyond this do not stay in registers
@@ -556,16 +570,18 @@ hipError_t launch_fwd(const NormFwdJob& j, hipStream_t s)
         k_norm_fwd_wide<SRC, MODE><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
         return hipGetLastError();
     }
-    return by_width(j.cols, [&](auto T, auto N) {
-        constexpr int B = T < 256 ? 256 : (int)T, RPB = B / T;
+    return by_width<false>(j.cols, [&](auto T, auto N) {
+        constexpr int B = T < 128 ? 256 : (int)T, RPB = B / T;
         k_norm_fwd<SRC, MODE, T, N><<<dim3((unsigned)((j.rows + RPB - 1) / RPB)), dim3(B), 0, s>>>(j);
         return hipGetLastError();
     });
 }
 
-// Workgroups (partial rows) of the backward: two for each CU, if there are
-// rows for them
-constexpr int64_t MOST_PARTS = 512;
+// Workgroups, and so partial rows, of the backward at most: one for each CU,
+// two for rows that few threads hold.  (32768 x 1024 43.9 us with 512, 45.9
+// with 256; 8192 x 4096 layer norm 54.3 and 48.7; 2047 x 4097 fp32 37.7 and
+// 30.9: there the partial sums' traffic counts.)
+int64_t most_parts(int64_t cols) { return cols <= 1024 ? 512 : 256; }
 
 int64_t wide_parts(int64_t rows) { return rows < 64 ? rows : 64; }
 
@@ -583,10 +599,10 @@ hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
             k_norm_cols<SRC, FROM, MODE><<<dim3((unsigned)((j.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s>>>(j, per);
         }
     } else {
-        const hipError_t e = by_width(j.cols, [&](auto T, auto N) {
+        const hipError_t e = by_width<true>(j.cols, [&](auto T, auto N) {
             constexpr int RPB = bwd_block<T>() / T;
             parts = (j.rows + RPB - 1) / RPB;
-            parts = parts < MOST_PARTS ? parts : MOST_PARTS;
+            parts = parts < most_parts(j.cols) ? parts : most_parts(j.cols);
             k_norm_bwd<SRC, FROM, MODE, T, N><<<dim3((unsigned)parts), dim3(bwd_block<T>()), 0, s>>>(j);
             return hipGetLastError();
         });
@@ -614,7 +630,7 @@ hipError_t by_mode(int64_t cols, bool in_place, F&& f)
 int64_t norm_bwd_partials(int64_t rows, int64_t cols)
 {
     if (cols > WIDE) return wide_parts(rows);
-    return rows < MOST_PARTS ? rows : MOST_PARTS;
+    return rows < most_parts(cols) ? rows : most_parts(cols);
 }
 
 hipError_t launch_norm_fwd(const NormFwdJob& j, hipStream_t s)
