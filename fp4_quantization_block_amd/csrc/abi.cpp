@@ -645,6 +645,12 @@ mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src
     mx_status s = check_glu_inputs(dh, ld_dh, src_dtype, rows, cols, gate, ld_gate, up, ld_up, ckpt_fmt, qg, sg, qu, su, act);
     if (s != MX_OK) return s;
     if (rows % 32 != 0 || cols % 32 != 0) return fail(MX_ERR_INVALID_ARG, "dual layout needs rows % 32 == 0 and cols % 32 == 0");
+    // the kernel addresses the rows of a tile, of inputs and copies, with
+    // 32-bit offsets, and numbers its tiles with 32-bit integers
+    constexpr int64_t most = (int64_t)1 << 23;
+    if (rows > most || cols > most) return fail(MX_ERR_INVALID_ARG, "rows and cols must be <= 2^23");
+    if (ld_dh > most || (gate && (ld_gate > most || ld_up > most)))
+        return fail(MX_ERR_INVALID_ARG, "row strides must be <= 2^23");
     if ((rows + 127) / 128 * ((cols + 31) / 32) >= (int64_t)1 << 31)
         return fail(MX_ERR_INVALID_ARG, "rows x cols must be fewer than 2^31 tiles of 128 x 32");
     if (!q_row || !s_row || !q_col || !s_col) return fail(MX_ERR_INVALID_ARG, "an output pointer is NULL");

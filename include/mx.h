@@ -503,8 +503,9 @@ mx_status mx_glu_backward(const void* dh, int64_t ld_dh, int32_t src_dtype, int6
  *        NULL.
  * Each block encodes the fp32 values that mx_glu_backward rounds, as
  * mx_quantize_dual_layout does with MX_SCALE_E8M0 and MX_RNE.
- * fmt, h_fmt: MX_E4M3 or MX_E5M2.  Needs rows % 32 == 0 and cols % 32 == 0.
- * Inputs as mx_glu_backward.
+ * fmt, h_fmt: MX_E4M3 or MX_E5M2.  Needs rows % 32 == 0 and cols % 32 == 0;
+ * rows, cols and the row strides at most 2^23 (what mx_gemm takes as K), and
+ * fewer than 2^31 tiles of 128 x 32.  Inputs as mx_glu_backward.
  */
 mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src_dtype, int64_t rows, int64_t cols,
                                       const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,

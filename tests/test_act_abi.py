@@ -132,6 +132,12 @@ def test_glu_backward_refuses_outputs(lib, args, status):
     ({}, (1, P + 8, P, P, P, 0, None, None), ALI), ({}, (1, P, P, P + 8, P, 0, None, None), ALI),
     ({}, (1, P, P, P, P, 0, P, None), INV), ({}, (1, P, P, P, P, 2, P, P), UNS), ({}, (1, P, P, P, P, 0, P + 8, P), ALI),
     (dict(rows=(1 << 30), cols=1 << 30, ld_dh=1 << 30, ld_g=1 << 30, ld_u=1 << 30), (1, P, P, P, P, 0, None, None), INV),
+    (dict(rows=(1 << 23) + 32), (1, P, P, P, P, 0, None, None), INV),           # 32-bit offsets in a tile
+    (dict(cols=(1 << 23) + 32, ld_dh=1 << 24, ld_g=1 << 24, ld_u=1 << 24), (1, P, P, P, P, 0, None, None), INV),
+    (dict(ld_dh=(1 << 23) + 1), (1, P, P, P, P, 0, None, None), INV),
+    (dict(ld_g=(1 << 23) + 1), (1, P, P, P, P, 0, None, None), INV),
+    (dict(ld_u=(1 << 23) + 1), (1, P, P, P, P, 0, None, None), INV),
+    (dict(rows=1 << 23, cols=1 << 23, ld_dh=1 << 23, ld_g=1 << 23, ld_u=1 << 23), (1, P, P, P, P, 0, None, None), INV),
 ])
 def test_glu_backward_dual_refuses(lib, kw, args, status):
     assert lib.mx_glu_backward_dual_layout(*_head(**kw), *args, None) == status

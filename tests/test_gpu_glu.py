@@ -176,7 +176,7 @@ def _check_dual(d, b, fmt, h_fmt, what):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("fmt,h_fmt", [("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", None)])
-@pytest.mark.parametrize("rows,cols", [(32, 32), (64, 96), (128, 64), (160, 160), (288, 1056), (96, 4096), (1056, 128)])
+@pytest.mark.parametrize("rows,cols", [(32, 32), (64, 96), (128, 64), (160, 160), (288, 1056), (96, 4096), (1056, 128), (2080, 2144), (4128, 1056)])
 def test_dual_layout(rows, cols, fmt, h_fmt, act):
     """The codes encode the fp32 gradients that mx_glu_backward gives for
     fp32 inputs, in both layouts."""
@@ -188,7 +188,7 @@ def test_dual_layout(rows, cols, fmt, h_fmt, act):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
-@pytest.mark.parametrize("rows,cols", [(32, 32), (160, 2080), (256, 512)])
+@pytest.mark.parametrize("rows,cols", [(32, 32), (160, 2080), (256, 512), (2144, 2080), (96, 40960), (160, 40992)])
 def test_dual_layout_from_checkpoints(rows, cols, fmt):
     """From checkpoints, with bf16 dh: the fp32 gradients come from the same
     values through fp32 inputs."""
@@ -202,10 +202,10 @@ def test_dual_layout_from_checkpoints(rows, cols, fmt):
     _check_dual(d16, b16, "e5m2", "e4m3", f"{rows}x{cols} bf16")
 
 
-def test_dual_layout_special_blocks():
+@pytest.mark.parametrize("rows,cols", [(96, 96), (4096, 1024)])
+def test_dual_layout_special_blocks(rows, cols):
     """Zero, subnormal, huge, Inf and NaN places: blocks in both directions as
-    the quantizer encodes them."""
-    rows, cols = 96, 96
+    the quantizer encodes them, in both kernels' tiles."""
     g, u, dh = _inputs(rows, cols, torch.float32)
     dh[:32] = 0.0
     dh[40, 5] = float("inf")
