@@ -182,22 +182,30 @@ struct BlockScale {
 
 // Four codes of a finite block.  The scaled converters return RNE(x / 2^e),
 // the scale's exponent field read as E8M0, and do not saturate: the values are
-// clamped to +-Fmax 2^e first.  (Equal to scaling, clamping and converting
-// for every block exponent over 28 binades below it, and 1.5 instructions an
-// element instead of 2.5.)
-template <int FMT>
+// clamped to +-Fmax 2^e first, or the kernel has asked the converters to
+// (SATURATED: saturate_converters).  (Both were found equal to scaling,
+// clamping and converting for every block exponent over 28 binades below it,
+// at 1.5 and 0.5 instructions an element instead of 2.5.)
+template <int FMT, bool SATURATED = false>
 __device__ __forceinline__ uint32_t encode4(const BlockScale<FMT>& b, float v0, float v1, float v2, float v3)
 {
-    short2v d = __builtin_nondeterministic_value(short2v{});    // both halves are written
-    const float c0 = b.clamped(v0), c1 = b.clamped(v1), c2 = b.clamped(v2), c3 = b.clamped(v3);
+    short2v d = {0, 0};
+    if constexpr (!SATURATED) v0 = b.clamped(v0), v1 = b.clamped(v1), v2 = b.clamped(v2), v3 = b.clamped(v3);
     if constexpr (FMT == E4M3) {
-        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(d, c0, c1, b.scale, false);
-        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(d, c2, c3, b.scale, true);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(d, v0, v1, b.scale, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(d, v2, v3, b.scale, true);
     } else {
-        d = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(d, c0, c1, b.scale, false);
-        d = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(d, c2, c3, b.scale, true);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(d, v0, v1, b.scale, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(d, v2, v3, b.scale, true);
     }
     return __builtin_bit_cast(uint32_t, d);
+}
+
+// Sets the wave's MODE.FP16_OVFL, with which conversions to FP8 saturate.
+// (It clamps fp16 results too: for kernels that have none.)
+__device__ __forceinline__ void saturate_converters()
+{
+    __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);     // register 1 (MODE), bit 23, one bit
 }
 
 constexpr uint32_t NONFINITE = 0x7F800000u;      // keys from here on: a block with a NaN or an Inf

@@ -245,21 +245,33 @@ hipError_t by_act(int act, F&& f)
 // to 16 tiles at a time through LDS.
 // ---------------------------------------------------------------------------
 
-// the largest key of the four lanes 8 apart that hold a row block: l ^ 8 (in
-// the 16-lane row) and l ^ 16
-__device__ __forceinline__ uint32_t row_block_max(uint32_t k)
+// Block maxima from the lanes' own, for several blocks a step at a time (a
+// cross-lane step has to wait for the one before on the same register).
+
+// over the four lanes 8 apart that hold a row block: l ^ 8 (in the 16-lane
+// row) and l ^ 16
+template <int B>
+__device__ __forceinline__ void row_block_max(uint32_t (&k)[B])
 {
-    k = max(k, dpp<0x128>(k));                 // rotate by 8 in a row of 16
-    auto p = __builtin_amdgcn_permlane16_swap(k, k, false, false);
-    return max((uint32_t)p[0], (uint32_t)p[1]);
+#pragma unroll
+    for (int j = 0; j < B; j++) k[j] = max(k[j], dpp<0x128>(k[j]));        // rotate by 8 in a row of 16
+#pragma unroll
+    for (int j = 0; j < B; j++) {
+        auto p = __builtin_amdgcn_permlane16_swap(k[j], k[j], false, false);
+        k[j] = max((uint32_t)p[0], (uint32_t)p[1]);
+    }
 }
 
-// the largest key of eight neighbouring lanes
-__device__ __forceinline__ uint32_t oct_max(uint32_t k)
+// over eight neighbouring lanes
+template <int B>
+__device__ __forceinline__ void oct_max(uint32_t (&k)[B])
 {
-    k = max(k, dpp<DPP_XOR1>(k));
-    k = max(k, dpp<DPP_XOR2>(k));
-    return max(k, dpp<DPP_HALF_MIRROR>(k));
+#pragma unroll
+    for (int j = 0; j < B; j++) k[j] = max(k[j], dpp<DPP_XOR1>(k[j]));
+#pragma unroll
+    for (int j = 0; j < B; j++) k[j] = max(k[j], dpp<DPP_XOR2>(k[j]));
+#pragma unroll
+    for (int j = 0; j < B; j++) k[j] = max(k[j], dpp<DPP_HALF_MIRROR>(k[j]));
 }
 
 // Waits for this wave's LDS traffic only (its global loads and stores stay in
@@ -330,17 +342,49 @@ __device__ __forceinline__ void dual_load(const GluBwdJob& a, int64_t row, int64
 // different groups of eight banks.
 template <int LB> constexpr int line_bytes() { return LB + 8; }
 
+// Codes and scale bytes of B blocks, N values of each in this lane; a block
+// with a NaN or an Inf, in any lane, is put right in a step of its own
+template <int FMT, int B, int N>
+__device__ __forceinline__ void encode_blocks(const float (&v)[B][N], const uint32_t (&key)[B], uint32_t (&code)[B][N / 4],
+                                              uint32_t (&byte)[B])
+{
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < B; j++) {
+        const BlockScale<FMT> b(key[j]);
+#pragma unroll
+        for (int i = 0; i < N / 4; i++)
+            code[j][i] = encode4<FMT, true>(b, v[j][4 * i], v[j][4 * i + 1], v[j][4 * i + 2], v[j][4 * i + 3]);
+        byte[j] = b.byte;
+        most = max(most, key[j]);
+    }
+    if (__builtin_expect(most >= NONFINITE, 0)) {
+#pragma unroll
+        for (int j = 0; j < B; j++) {
+            if (key[j] < NONFINITE) continue;
+#pragma unroll
+            for (int i = 0; i < N / 4; i++) code[j][i] = 0x7F7F7F7Fu;
+            byte[j] = 0xFFu;
+        }
+    }
+}
+
 // Row codes of one tensor's 4 x 8 values per lane to `stage`, eight bytes from
 // `at` in lines line0 .. line0 + 3, and the blocks' scale bytes
 template <int FMT, int LB, int SPL>
 __device__ __forceinline__ void stage_rows(const float (&v)[4][8], uint8_t* stage, uint8_t* scales, int line0, int at,
                                            int block, bool writes)
 {
+    uint32_t key[4], code[4][2], byte[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const Codes8 c = encode8<FMT>(v[i], row_block_max(chunk_key(v[i])));
-        *(uint2*)(stage + (line0 + i) * line_bytes<LB>() + at) = make_uint2(c.lo, c.hi);
-        if (writes) scales[(line0 + i) * SPL + block] = (uint8_t)c.scale;
+    for (int i = 0; i < 4; i++) key[i] = chunk_key(v[i]);
+    row_block_max(key);
+    encode_blocks<FMT>(v, key, code, byte);
+#pragma unroll
+    for (int i = 0; i < 4; i++) *(uint2*)(stage + (line0 + i) * line_bytes<LB>() + at) = make_uint2(code[i][0], code[i][1]);
+    if (writes) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) scales[(line0 + i) * SPL + block] = (uint8_t)byte[i];
     }
 }
 
@@ -349,15 +393,21 @@ template <int FMT, int LB, int SPL>
 __device__ __forceinline__ void stage_columns(const float (&v)[4][8], uint8_t* stage, uint8_t* scales, int line0, int at,
                                               int block, bool writes)
 {
+    float w[8][4];
+    uint32_t key[8], code[8][1], byte[8];
 #pragma unroll
     for (int c = 0; c < 8; c++) {
-        const float w[4] = {v[0][c], v[1][c], v[2][c], v[3][c]};
-        const uint32_t key = oct_max(chunk_key(w));
-        const BlockScale<FMT> b(key);
-        uint32_t code = encode4<FMT>(b, w[0], w[1], w[2], w[3]), byte = b.byte;
-        if (key >= NONFINITE) code = 0x7F7F7F7Fu, byte = 0xFFu;
-        *(uint32_t*)(stage + (line0 + c) * line_bytes<LB>() + at) = code;
-        if (writes) scales[(line0 + c) * SPL + block] = (uint8_t)byte;
+#pragma unroll
+        for (int r = 0; r < 4; r++) w[c][r] = v[r][c];
+        key[c] = chunk_key(w[c]);
+    }
+    oct_max(key);
+    encode_blocks<FMT>(w, key, code, byte);
+#pragma unroll
+    for (int c = 0; c < 8; c++) *(uint32_t*)(stage + (line0 + c) * line_bytes<LB>() + at) = code[c][0];
+    if (writes) {
+#pragma unroll
+        for (int c = 0; c < 8; c++) scales[(line0 + c) * SPL + block] = (uint8_t)byte[c];
     }
 }
 
@@ -440,6 +490,7 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
     constexpr bool EARLY = !(TENSOR && SRC == SRC_F32);    // two tiles' inputs fit the registers
     __shared__ __align__(16) uint8_t cols[3][TC * line_bytes<TR>()], rows[2][TR * line_bytes<TC>()];
     __shared__ __align__(16) uint8_t col_scales[3][TC * WR], row_scales[2][TR * WS], in_scales[2][TENSOR ? 16 : TR * WS];
+    saturate_converters();
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, band = wave % WR, part = wave / WR;
     const int m = lane & 7, k8 = lane >> 3, lr = band * 32 + m * 4, lc = part * 64 + k8 * 8;
     const uint32_t sr = (uint32_t)(a.rows / 32), sc = (uint32_t)(a.cols / 32);
@@ -502,16 +553,21 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
                 u[i][c] = dh * act;
             }
         }
-        if (!EARLY && tile + 1 < end) fetch(y1, x1);
         const bool row_writer = (k8 & 3) == 0, col_writer = m == 0;
+        auto stage_h = [&] {
+            if (!a.qh) return;
+            if (a.h_fmt == E4M3) stage_columns<E4M3, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
+            else stage_columns<E5M2, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
+        };
+        if constexpr (!EARLY) {                // h's registers are free before the next tile's inputs come
+            stage_h();
+            if (tile + 1 < end) fetch(y1, x1);
+        }
         stage_rows<FMT, TC, WS>(g, rows[0], row_scales[0], lr, lc, block, row_writer);
         stage_rows<FMT, TC, WS>(u, rows[1], row_scales[1], lr, lc, block, row_writer);
         stage_columns<FMT, TR, WR>(g, cols[0], col_scales[0], lc, lr, band, col_writer);
         stage_columns<FMT, TR, WR>(u, cols[1], col_scales[1], lc, lr, band, col_writer);
-        if (a.qh) {
-            if (a.h_fmt == E4M3) stage_columns<E4M3, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
-            else stage_columns<E5M2, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
-        }
+        if constexpr (EARLY) stage_h();
         // The next tile's inputs have landed, most of a tile's work after they
         // were asked for: waited for here, ahead of this tile's stores, since
         // loads and stores complete in one count and a wait for the loads
