@@ -549,7 +549,7 @@ def mx_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias
         if sum_out is not None:
             raise ValueError("sum_out needs a residual")
     elif sum_out is None:
-        sum_out = x.new_empty(shape, dtype=dtype)
+        sum_out = torch.empty_like(x)
     psum, ld_sum = _maybe_matrix(sum_out, shape, dtype, at, "sum_out")
     out_dtype, out = _out_dtype(out_dtype, dtype)
     if not write_y:
@@ -593,7 +593,7 @@ def mx_norm_backward(dy: torch.Tensor, rstd: torch.Tensor, x: Optional[torch.Ten
     prstd = _dense(rstd, (rows,), torch.float32, at, "rstd")
     pmean = _dense(mean, (rows,), torch.float32, at, "mean") if k == MX_NORM_LAYER and mean is not None else None
     pds, ld_ds = _maybe_matrix(dsum, shape, dtype, at, "dsum")
-    dx = dy.new_empty(shape, dtype=dtype) if dx is None else dx
+    dx = torch.empty_like(dy) if dx is None else dx
     pdx, ld_dx = _matrix(dx, shape, dtype, at, "dx")
     pw, _, pd = _params(weight, None, cols, at)
     pdw = pdb = pwork = None
@@ -662,8 +662,8 @@ def mx_glu_backward(dh: torch.Tensor, gate: Optional[torch.Tensor] = None, up: O
     checkpoints; recompute_h: also h = act(gate) * up."""
     head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
     shape, dtype, at = dh.shape, dh.dtype, dh.get_device()
-    dgate = dh.new_empty(shape, dtype=dtype) if dgate is None else dgate
-    dup = dh.new_empty(shape, dtype=dtype) if dup is None else dup
+    dgate = torch.empty_like(dh) if dgate is None else dgate
+    dup = torch.empty_like(dh) if dup is None else dup
     if not recompute_h:
         h = None
     elif h is None:
