@@ -15,17 +15,32 @@
 //   [COAT] write-up of "COAT: Compressing Optimizer States and Activation for
 //          memory efficient FP8 Training"
 //
-// Kernels
+// What is rounded: the sum to the source type, since it is the residual stream
+// that the next block reads, and what is normalised is what was stored; y, dx
+// and the codes once each, from fp32.  Statistics and the parameters'
+// gradients stay fp32.
+//
+// All of it is bound by memory: a few operations an element, so that the one
+// aim is to read and write each byte once.
+//
+// Kernels (times at 8192 x 4096 bf16 on one MI355X, where a 1 GiB copy runs at
+// 5.1 TB/s)
 //   k_norm_fwd       T threads hold a row in registers (N chunks of eight
-//                    elements each): read once, written once.
+//                    elements each): read once, written once.  RMS norm with
+//                    residual, sum, y and checkpoint, 303 MB: 52 us, 5.8 TB/s
+//                    (counters: 134 MB read, 169 MB written).
 //   k_norm_fwd_wide  rows beyond 16384: a workgroup walks the row, and reads
 //                    it again for each of the statistics and the output.
-//   k_norm_bwd       T threads hold a row; a workgroup walks rows and keeps
-//                    its share of the dw and db sums in registers, written
-//                    as one row of partial sums each at the end.
+//   k_norm_bwd       T threads hold a row; a workgroup walks rows, the next
+//                    one's inputs loaded ahead, and keeps its share of the dw
+//                    and db sums in registers, written as one row of partial
+//                    sums each at the end.  From the checkpoint, with dsum,
+//                    236 MB: 40.5 us.
 //   k_norm_bwd_wide / k_norm_cols   the same in two kernels for rows beyond
 //                    16384: dx by rows, then partial sums by column strips.
-//   k_norm_colsum    adds the partial rows up, in a fixed order.
+//   k_norm_colsum    adds the partial rows up, in a fixed order: 4.7 us for
+//                    256 rows of 4096, most of it the launch and one pass of
+//                    latency (both backward kernels 5.2 TB/s).
 #include "act_device.h"
 #include "mx_internal.h"
 
