@@ -458,13 +458,13 @@ __global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
 }
 
 template <int SRC, int FROM, int MODE>
-__global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormBwdJob a)
+__global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormBwdJob a, int64_t row0)
 {
     constexpr int T = 1024;
     typedef Cols<MODE, T> P;
     __shared__ float red[2][T / 64];
     const int t = (int)threadIdx.x;
-    const int64_t row = blockIdx.x, steps = (a.cols + T * 8 - 1) / (T * 8);
+    const int64_t row = row0 + blockIdx.x, steps = (a.cols + T * 8 - 1) / (T * 8);
     const float mean = a.layer ? a.mean[row] : 0.0f, rstd = a.rstd[row], n = (float)a.cols;
     float pg = 0.0f, pgh = 0.0f;
     auto values = [&](const P& p, const BwdRaw<SRC, FROM, MODE>& r, float (&g)[8], float (&h)[8]) {
@@ -578,17 +578,53 @@ hipError_t by_width(int64_t cols, F&& f)
 
 constexpr int64_t WIDE = 16384;        // rows beyond this do not stay in registers
 
-template <int SRC, int MODE>
-hipError_t launch_fwd(const NormFwdJob& j, hipStream_t s)
+// A launch counts its threads in 32 bits: f(first row, rows) for slices of
+// rows that need at most 2^31, at T threads a row.
+template <class F>
+hipError_t sliced(int64_t rows, int64_t T, F&& f)
 {
-    if (j.cols > WIDE) {
-        k_norm_fwd_wide<SRC, MODE><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
-        return hipGetLastError();
+    const int64_t most = ((int64_t)1 << 31) / T;
+    for (int64_t r = 0; r < rows; r += most) {
+        f(r, rows - r < most ? rows - r : most);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    return by_width<false>(j.cols, [&](auto T, auto N) {
+    return hipSuccess;
+}
+
+template <class T>
+void advance(T*& p, int64_t bytes)
+{
+    if (p) p = (T*)((uint8_t*)p + bytes);
+}
+
+template <int SRC>
+NormFwdJob rows_of(NormFwdJob j, int64_t r, int64_t n)
+{
+    constexpr int64_t B = ElemT<SRC>::bytes;
+    j.rows = n;
+    advance(j.x, r * j.ld_x * B);
+    advance(j.residual, r * j.ld_res * B);
+    advance(j.sum, r * j.ld_sum * B);
+    advance(j.y, r * j.ld_y * (j.out_f32 ? 4 : 2));
+    for (uint8_t** q : {&j.qy, &j.qx}) advance(*q, r * j.cols);
+    for (uint8_t** q : {&j.sy, &j.sx}) advance(*q, r * (j.cols / 32));
+    for (float** v : {&j.mean, &j.rstd}) advance(*v, r * 4);
+    return j;
+}
+
+template <int SRC, int MODE>
+hipError_t launch_fwd(const NormFwdJob& job, hipStream_t s)
+{
+    if (job.cols > WIDE) {
+        return sliced(job.rows, 1024, [&](int64_t r, int64_t n) {
+            k_norm_fwd_wide<SRC, MODE><<<dim3((unsigned)n), dim3(1024), 0, s>>>(rows_of<SRC>(job, r, n));
+        });
+    }
+    return by_width<false>(job.cols, [&](auto T, auto N) {
         constexpr int B = T < 128 ? 256 : (int)T, RPB = B / T;
-        k_norm_fwd<SRC, MODE, T, N><<<dim3((unsigned)((j.rows + RPB - 1) / RPB)), dim3(B), 0, s>>>(j);
-        return hipGetLastError();
+        return sliced(job.rows, T, [&](int64_t r, int64_t n) {
+            k_norm_fwd<SRC, MODE, T, N><<<dim3((unsigned)((n + RPB - 1) / RPB)), dim3(B), 0, s>>>(rows_of<SRC>(job, r, n));
+        });
     });
 }
 
@@ -605,8 +641,10 @@ hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
 {
     int64_t parts = 0;
     if (j.cols > WIDE) {
-        k_norm_bwd_wide<SRC, FROM, MODE><<<dim3((unsigned)j.rows), dim3(1024), 0, s>>>(j);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        const hipError_t e = sliced(j.rows, 1024, [&](int64_t r, int64_t n) {
+            k_norm_bwd_wide<SRC, FROM, MODE><<<dim3((unsigned)n), dim3(1024), 0, s>>>(j, r);
+        });
+        if (e != hipSuccess) return e;
         if (j.dweight || j.dbias) {
             parts = wide_parts(j.rows);
             const int64_t per = (j.rows + parts - 1) / parts;

@@ -377,3 +377,37 @@ def test_offsets_beyond_32_bits():
     ct = mx.checkpoint("e4m3", tail.qx, tail.sx)
     bt = mx.mx_norm_backward(x[-3:], tail.rstd, ckpt=ct, weight=w, kind="rms", want_dweight=False)
     assert torch.equal(b.dx[-3:], bt.dx)
+
+
+def test_more_rows_than_one_launch_counts():
+    """2^26 rows and some: 64 threads a row are more than 2^32, which no one
+    launch counts.  Every row against the same rows in another place."""
+    rows, cols = (1 << 26) + 37, 8
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x.normal_(generator=torch.Generator(device=DEV).manual_seed(1))
+    w = dev(rand(3, cols), torch.bfloat16)
+    f = mx.mx_norm_forward(x, w, eps=EPS, kind="layer")
+    for first in (0, (1 << 25) - 50, (1 << 26) - 60, rows - 100):
+        part = slice(first, first + 100)
+        alone = mx.mx_norm_forward(x[part], w, eps=EPS, kind="layer")
+        assert torch.equal(f.y[part], alone.y) and torch.equal(f.rstd[part], alone.rstd)
+        assert torch.equal(f.mean[part], alone.mean)
+    b = mx.mx_norm_backward(x, f.rstd, x=x, mean=f.mean, weight=w, kind="layer", want_dweight=False)
+    part = slice(rows - 100, rows)
+    alone = mx.mx_norm_backward(x[part], f.rstd[part], x=x[part], mean=f.mean[part], weight=w, kind="layer",
+                                want_dweight=False)
+    assert torch.equal(b.dx[part], alone.dx)
+
+
+def test_wide_rows_in_slices_of_a_launch():
+    """More than 2^21 rows beyond 16384 columns need two launches of the wide
+    kernels (bf16, 69 GB in, as much out)."""
+    rows, cols = (1 << 21) + 3, 16392
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[-5:] = dev(rand(1, 5, cols), torch.bfloat16)
+    x[:5] = dev(rand(2, 5, cols), torch.bfloat16)
+    f = mx.mx_norm_forward(x, eps=EPS, kind="rms")
+    for part in (slice(0, 5), slice(rows - 5, rows)):
+        alone = mx.mx_norm_forward(x[part], eps=EPS, kind="rms")
+        assert torch.equal(f.y[part], alone.y) and torch.equal(f.rstd[part], alone.rstd)
+    del f
