@@ -336,21 +336,33 @@ __device__ __forceinline__ Chunk<SRC> lane_chunk(const void* base, uint32_t offs
 struct DualAt { uint32_t d, g, u, q; };
 
 template <int SRC, bool TENSOR>
-__device__ __forceinline__ void dual_load(const GluBwdJob& a, int64_t row, int64_t col, const DualAt& at,
-                                          DualRaw<SRC, TENSOR>& r)
+__device__ __forceinline__ void dual_load_dh(const GluBwdJob& a, int64_t row, int64_t col, const DualAt& at,
+                                             DualRaw<SRC, TENSOR>& r)
 {
-    constexpr int B = ElemT<SRC>::bytes;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        r.d[i] = lane_chunk<SRC>((const uint8_t*)a.dh + ((row + i) * a.ld_dh + col) * ElemT<SRC>::bytes, at.d);
+}
+
+template <int SRC, bool TENSOR>
+__device__ __forceinline__ void dual_load_gate(const GluBwdJob& a, int64_t row, int64_t col, const DualAt& at,
+                                               DualRaw<SRC, TENSOR>& r)
+{
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        r.d[i] = lane_chunk<SRC>((const uint8_t*)a.dh + ((row + i) * a.ld_dh + col) * B, at.d);
-        if constexpr (!TENSOR) {
-            const int64_t e = (row + i) * a.cols + col;
-            r.g[i] = __builtin_bit_cast(uint2, dwords2(lane_at<dwords2>(a.qg + e, at.q)->v));
-            r.u[i] = __builtin_bit_cast(uint2, dwords2(lane_at<dwords2>(a.qu + e, at.q)->v));
-        } else {
-            r.g[i] = lane_chunk<SRC>((const uint8_t*)a.gate + ((row + i) * a.ld_gate + col) * B, at.g);
-            r.u[i] = lane_chunk<SRC>((const uint8_t*)a.up + ((row + i) * a.ld_up + col) * B, at.u);
-        }
+        if constexpr (TENSOR) r.g[i] = lane_chunk<SRC>((const uint8_t*)a.gate + ((row + i) * a.ld_gate + col) * ElemT<SRC>::bytes, at.g);
+        else r.g[i] = __builtin_bit_cast(uint2, dwords2(lane_at<dwords2>(a.qg + (row + i) * a.cols + col, at.q)->v));
+    }
+}
+
+template <int SRC, bool TENSOR>
+__device__ __forceinline__ void dual_load_up(const GluBwdJob& a, int64_t row, int64_t col, const DualAt& at,
+                                             DualRaw<SRC, TENSOR>& r)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if constexpr (TENSOR) r.u[i] = lane_chunk<SRC>((const uint8_t*)a.up + ((row + i) * a.ld_up + col) * ElemT<SRC>::bytes, at.u);
+        else r.u[i] = __builtin_bit_cast(uint2, dwords2(lane_at<dwords2>(a.qu + (row + i) * a.cols + col, at.q)->v));
     }
 }
 
@@ -522,12 +534,28 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
     DualRaw<SRC, TENSOR> raw;
     // a lane past the tensor's end reads the tile's first places instead (its
     // whole blocks lie outside: rows and cols are multiples of 32)
-    auto fetch = [&](uint32_t y, uint32_t x) {
+    // `more` false: the run has ended.  The registers are cleared then, rather
+    // than left: what they hold need not be kept through the iteration.
+    enum { DH = 1, GATE = 2, UP = 4 };
+    auto fetch = [&](bool more, uint32_t y, uint32_t x, int which) {
+        if (!more) {
+            const DualRaw<SRC, TENSOR> none{};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (which & DH) raw.d[i] = none.d[i];
+                if (which & GATE) raw.g[i] = none.g[i];
+                if (which & UP) raw.u[i] = none.u[i];
+            }
+            return;
+        }
         const int64_t r = (int64_t)y * TR, c = (int64_t)x * TC;
         const bool in = r + lr < a.rows && c + lc < a.cols;
-        dual_load(a, r, c, in ? place : DualAt{}, raw);
+        const DualAt at = in ? place : DualAt{};
+        if (which & DH) dual_load_dh(a, r, c, at, raw);
+        if (which & GATE) dual_load_gate(a, r, c, at, raw);
+        if (which & UP) dual_load_up(a, r, c, at, raw);
     };
-    if (tile < end) fetch(ty, tx);
+    fetch(tile < end, ty, tx, DH | GATE | UP);
     __builtin_amdgcn_s_waitcnt(WAIT_VMEM);     // as inside the loop: no load is in flight where it begins again
     uint32_t first = tx, left = 0;             // the window's first tile column, its tiles still to do
     while (tile < end) {
@@ -549,7 +577,8 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
         const DualRaw<SRC, TENSOR> now = raw;
         uint32_t y1 = ty, x1 = tx + 1;
         if (x1 == tiles.nx) x1 = 0, y1++;
-        if (EARLY && tile + 1 < end) fetch(y1, x1);
+        const bool more = tile + 1 < end;
+        if constexpr (EARLY) fetch(more, y1, x1, DH | GATE | UP);
         float g[4][8], u[4][8], h[4][8];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -568,6 +597,7 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
                 h[i][c] = act * u[i][c];
                 g[i][c] = dh * u[i][c] * slope;
                 u[i][c] = dh * act;
+                if constexpr (!EARLY) __builtin_amdgcn_sched_barrier(0);   // one at a time: few temporaries
             }
         }
         const bool row_writer = (k8 & 3) == 0, col_writer = m == 0;
@@ -576,13 +606,17 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
             if (a.h_fmt == E4M3) stage_columns<E4M3, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
             else stage_columns<E5M2, TR, WR>(h, cols[2], col_scales[2], lc, lr, band, col_writer);
         };
-        if constexpr (!EARLY) {                // h's registers are free before the next tile's inputs come
+        // fp32 tensors: each of the next tile's inputs is asked for when a
+        // staged tensor has given its registers back
+        if constexpr (!EARLY) {
             stage_h();
-            if (tile + 1 < end) fetch(y1, x1);
+            fetch(more, y1, x1, DH);
         }
         stage_rows<FMT, TC, WS>(g, rows[0], row_scales[0], lr, lc, block, row_writer);
-        stage_rows<FMT, TC, WS>(u, rows[1], row_scales[1], lr, lc, block, row_writer);
+        if constexpr (EARLY) stage_rows<FMT, TC, WS>(u, rows[1], row_scales[1], lr, lc, block, row_writer);
         stage_columns<FMT, TR, WR>(g, cols[0], col_scales[0], lc, lr, band, col_writer);
+        if constexpr (!EARLY) fetch(more, y1, x1, GATE | UP);
+        if constexpr (!EARLY) stage_rows<FMT, TC, WS>(u, rows[1], row_scales[1], lr, lc, block, row_writer);
         stage_columns<FMT, TR, WR>(u, cols[1], col_scales[1], lc, lr, band, col_writer);
         if constexpr (EARLY) stage_h();
         // The next tile's inputs have landed, most of a tile's work after they

@@ -207,10 +207,10 @@ template <int SRC, int MODE, int T, int N>
 __global__ __launch_bounds__(T < 128 ? 256 : T) void k_norm_fwd(NormFwdJob a)
 {
     constexpr int RPB = T < 128 ? 256 / T : 1;
-    __shared__ float red[2][T / 64];
+    __shared__ float red[2][T < 64 ? 1 : T / 64];
     const int t = (int)threadIdx.x % T;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / T;
-    if (row >= a.rows) return;               // whole waves, and only where no barrier follows (T = 64)
+    if (row >= a.rows) return;               // whole rows' lanes, and only where no barrier follows (T <= 64)
     typedef Cols<MODE, T> P;
     float s[N][8];
 #pragma unroll
@@ -349,7 +349,7 @@ template <int T> constexpr int bwd_block() { return T <= 256 ? 512 : T; }
 template <int SRC, int FROM, int MODE, int T, int N>
 __global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
 {
-    constexpr int RPB = bwd_block<T>() / T, W = T / 64;
+    constexpr int RPB = bwd_block<T>() / T, W = T < 64 ? 1 : T / 64;
     typedef Cols<MODE, T> P;
     __shared__ float red[2][2][RPB][W];
     __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? N * T * 8 : 1];
@@ -408,8 +408,8 @@ __global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
                 pgh += chunk_sum(p, [&](int i) { return g[j][i] * h[j][i]; });
                 pg += chunk_sum(p, [&](int i) { return g[j][i]; });
             }
-            pgh = wave_sum(pgh);
-            if (a.layer) pg = wave_sum(pg);
+            pgh = lanes_sum<T>(pgh);
+            if (a.layer) pg = lanes_sum<T>(pg);
         }
         if constexpr (W > 1) {
             if ((threadIdx.x & 63) == 0) {
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
             }
             __syncthreads();
             if (sub > 0) return;
-#pragma unroll
+#pragma unroll 4
             for (int k = 0; k < RPB - 1; k++)
 #pragma unroll
                 for (int j = 0; j < N; j++)
@@ -556,7 +556,8 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(const float* work, int64_t
 // 256 threads with 2 to 4 chunks each (64 and 512 threads in the backward),
 // bf16 with a checkpoint: the forward 32768 x 1024 50.5 us against 52.8, 8192 x
 // 4096 50.4 against 52.9, 8192 x 8192 105.7 against 114.4; the backward 44.1
-// against 65.9, 44.8 against 46.9, 94.4 against 95.0.
+// against 65.9, 44.8 against 46.9, 94.4 against 95.0.  Rows of up to 256 share
+// a wave (the norms of single heads).
 // 640 threads are for the forward alone (8192 x 5120: 71.5 us against 72.5 with
 // 768; the backward 63.4 against 60.2).
 template <bool BACKWARD, class F>
@@ -564,6 +565,9 @@ hipError_t by_width(int64_t cols, F&& f)
 {
     constexpr std::integral_constant<int, 1> one;
     constexpr std::integral_constant<int, 2> two;
+    if (cols <= 8 * 8) return f(std::integral_constant<int, 8>(), one);
+    if (cols <= 16 * 8) return f(std::integral_constant<int, 16>(), one);
+    if (cols <= 32 * 8) return f(std::integral_constant<int, 32>(), one);
     if (cols <= 64 * 8) return f(std::integral_constant<int, 64>(), one);
     if (cols <= 128 * 8) return f(std::integral_constant<int, 128>(), one);
     if (cols <= 256 * 8) return f(std::integral_constant<int, 256>(), one);
