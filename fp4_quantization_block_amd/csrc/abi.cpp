@@ -537,6 +537,8 @@ mx_status mx_norm_backward(const void* dy, int64_t ld_dy, int32_t src_dtype, int
         if (work_bytes < mx_norm_backward_workspace_bytes(rows, cols))
             return fail(MX_ERR_INVALID_ARG, "work is smaller than mx_norm_backward_workspace_bytes()");
     }
+    if (cols > mx::NORM_WIDE && (dx == dy || (x && dx == x)))
+        return fail(MX_ERR_UNSUPPORTED, "dx over dy or x needs cols <= 16384 (wider rows are read again)");
     mx::NormBwdJob j{};
     j.dy = dy; j.ld_dy = ld_dy; j.src = src_dtype; j.rows = rows; j.cols = cols;
     j.x = x; j.ld_x = ld_x; j.ckpt_fmt = ckpt_fmt; j.qx = (const uint8_t*)qx; j.sx = sx;

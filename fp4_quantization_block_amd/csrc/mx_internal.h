@@ -124,6 +124,9 @@ struct NormBwdJob {
     float* work;            // partial rows of dweight, then of dbias
 };
 
+// rows beyond this do not stay in registers, and are read more than once
+constexpr int64_t NORM_WIDE = 16384;
+
 // partial rows that launch_norm_bwd writes, at most, for each of dweight and dbias
 int64_t norm_bwd_partials(int64_t rows, int64_t cols);
 hipError_t launch_norm_bwd(const NormBwdJob& j, hipStream_t stream);

@@ -580,8 +580,6 @@ hipError_t by_width(int64_t cols, F&& f)
     return f(std::integral_constant<int, 1024>(), two);
 }
 
-constexpr int64_t WIDE = 16384;        // rows beyond this do not stay in registers
-
 // A launch counts its threads in 32 bits: f(first row, rows) for slices of
 // rows that need at most 2^31, at T threads a row.
 template <class F>
@@ -619,7 +617,7 @@ NormFwdJob rows_of(NormFwdJob j, int64_t r, int64_t n)
 template <int SRC, int MODE>
 hipError_t launch_fwd(const NormFwdJob& job, hipStream_t s)
 {
-    if (job.cols > WIDE) {
+    if (job.cols > NORM_WIDE) {
         return sliced(job.rows, 1024, [&](int64_t r, int64_t n) {
             k_norm_fwd_wide<SRC, MODE><<<dim3((unsigned)n), dim3(1024), 0, s>>>(rows_of<SRC>(job, r, n));
         });
@@ -644,7 +642,7 @@ template <int SRC, int FROM, int MODE>
 hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
 {
     int64_t parts = 0;
-    if (j.cols > WIDE) {
+    if (j.cols > NORM_WIDE) {
         const hipError_t e = sliced(j.rows, 1024, [&](int64_t r, int64_t n) {
             k_norm_bwd_wide<SRC, FROM, MODE><<<dim3((unsigned)n), dim3(1024), 0, s>>>(j, r);
         });
@@ -686,7 +684,7 @@ hipError_t by_mode(int64_t cols, bool in_place, F&& f)
 
 int64_t norm_bwd_partials(int64_t rows, int64_t cols)
 {
-    if (cols > WIDE) return wide_parts(rows);
+    if (cols > NORM_WIDE) return wide_parts(rows);
     return rows < most_parts(cols) ? rows : most_parts(cols);
 }
 

@@ -612,6 +612,8 @@ def mx_norm_backward(dy: torch.Tensor, rstd: torch.Tensor, x: Optional[torch.Ten
     if want_dweight or want_dbias:
         if work is None:
             work = dy.new_empty(L.mx_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8)
+        elif work.get_device() != at or not work.is_contiguous():
+            raise ValueError("work must be contiguous and on the device of dy")
         nbytes, pwork = work.numel() * work.element_size(), work.data_ptr()
     _check(L.mx_norm_backward(pdy, ld_dy, src, rows, cols, px, ld_x, cf, pqx, psx, pmean, prstd, k, pw, pd, pds,
                               ld_ds, pdx, ld_dx, pdw, pdb, pwork, nbytes, _stream_on(stream, at)))

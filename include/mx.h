@@ -442,7 +442,8 @@ mx_status mx_norm_forward(const void* x, int64_t ld_x, const void* residual, int
  *        for MX_NORM_RMS.
  * weight, param_dtype: as in the forward call.
  * dsum:  a gradient of s from elsewhere (the residual path), or NULL.  dx may
- *        be dsum or dy themselves (same pointer and stride) for cols <= 16384.
+ *        be dsum itself, or, for cols <= 16384 (else MX_ERR_UNSUPPORTED), dy or
+ *        x (same pointer and stride).
  * dweight, dbias: cols fp32 each, or NULL.
  * work:  at least mx_norm_backward_workspace_bytes(rows, cols) bytes, 4-byte
  *        aligned, for the partial sums of dweight and dbias (may be NULL if

@@ -59,6 +59,8 @@ def _norm_bwd(lib, dy=P, ld_dy=64, src=1, rows=4, cols=64, x=P, ld_x=64, cf=0, q
     (dict(rstd=P + 1), ALI), (dict(kind=0, mean=P + 2), ALI), (dict(pd=9), INV), (dict(w=P + 1, pd=1), ALI),
     (dict(dsum=P, ld_dsum=2), INV), (dict(dsum=P + 1), ALI), (dict(dw=P + 2), ALI), (dict(db=P + 2), ALI),
     (dict(work=None), INV), (dict(work=P + 2), ALI), (dict(nbytes=100), INV), (dict(dw=None, db=P, work=None), INV),
+    (dict(cols=16385, ld_dy=16385, ld_x=16385, ld_dx=16385, x=2 * P), UNS),
+    (dict(cols=16385, ld_dy=16385, ld_x=16385, ld_dx=16385, dy=2 * P), UNS),
 ])
 def test_norm_backward_refuses(lib, kw, status):
     assert _norm_bwd(lib, **kw) == status
@@ -193,3 +195,10 @@ R4 = torch.zeros(4)
 def test_binding_refuses(call, error):
     with pytest.raises(error):
         call()
+
+
+@pytest.mark.parametrize("work", [torch.empty(1 << 16, device="meta", dtype=torch.uint8)[::2],
+                                  torch.empty((64, 64), dtype=torch.float32).t()])
+def test_binding_refuses_a_strided_workspace(work):
+    with pytest.raises(ValueError, match="work must be contiguous"):
+        mx.mx_norm_backward(X, R4, x=X, work=work)

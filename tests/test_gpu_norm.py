@@ -14,8 +14,9 @@ pytestmark = pytest.mark.gpu
 EPS = 1e-5
 
 # row lengths at which the kernels, or the last chunk, change
-COLS = [1, 2, 7, 8, 31, 32, 33, 64, 509, 512, 513, 520, 1000, 2048, 2049, 2056, 4096, 4097, 5000, 8192, 8193, 16384,
-        16385, 20000, 24577]
+COLS = [1, 2, 7, 8, 16, 31, 32, 33, 64, 65, 100, 128, 129, 200, 256, 257, 384, 509, 512, 513, 520, 1000, 1024,
+        1025, 2048, 2049, 2056, 3080, 4096, 4097, 5000, 5121, 6144, 6145, 8192, 8193, 16384, 16385, 20000,
+        24577]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -200,7 +201,7 @@ def test_backward(cols, dtype, kind):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 3, 5, 255, 511, 513, 1300, 2600])
-@pytest.mark.parametrize("cols", [24, 100, 640, 641])
+@pytest.mark.parametrize("cols", [24, 100, 136, 200, 640, 641])
 def test_backward_rows(rows, cols):
     """Row counts around the number of workgroups and of rows they share."""
     x, dy, w, mean, rstd = _backward_case(rows, cols, torch.float32, "layer")
@@ -251,9 +252,10 @@ def test_backward_every_code_and_scale():
 
 
 @pytest.mark.parametrize("what", ["no weight", "bf16 weight f32 x", "no dweight", "dbias only", "dsum in place",
-                                  "dy in place"])
-def test_backward_options(what):
-    rows, cols = 21, 777
+                                  "dy in place", "x in place"])
+@pytest.mark.parametrize("cols", [5, 99, 777, 6145, 12001, 12000])
+def test_backward_options(what, cols):
+    rows = 21
     x, dy, w, mean, rstd = _backward_case(rows, cols, torch.float32, "layer")
     dsum, kw = None, dict(want_dbias=True)
     dy0 = dy.clone()
@@ -269,10 +271,13 @@ def test_backward_options(what):
         dsum = dev(rand(9, rows, cols), torch.float32)
         kw = dict(dsum=dsum, dx=dsum)
         dsum = dsum.clone()
-    else:
+    elif what == "dy in place":
         kw = dict(dx=dy)
+    else:
+        kw = dict(dx=x)
+    x0 = x.cpu().double()
     out = mx.mx_norm_backward(dy, rstd, x=x, mean=mean, weight=w, kind="layer", **kw)
-    _check_backward(out, dy0, x.cpu().double(), mean, rstd, w, dsum, "layer", what)
+    _check_backward(out, dy0, x0, mean, rstd, w, dsum, "layer", f"{what} {cols}")
 
 
 @pytest.mark.parametrize("offset,pad", [(1, 3), (3, 0), (0, 8)])
