@@ -15,11 +15,11 @@
 //   k_glu_fwd, k_glu_bwd   one chunk of eight elements per thread, in order
 //                    over rows and columns: each byte read and written once,
 //                    and bound by that.  The forward with h as E4M3 codes and
-//                    both checkpoints, 833 MB: 143.5 us, 5.8 TB/s.  The
+//                    both checkpoints, 833 MB: 145 us, 5.7 TB/s.  The
 //                    backward from the checkpoints, 947 MB: 163 us, 5.8 TB/s.
 //   k_glu_bwd_dual   tiles whose gradients never leave registers before they
 //                    are codes, in both layouts.  From the checkpoints, with
-//                    h, 1083 MB: 242 us, 4.5 TB/s (counters: 493 MB read, 625
+//                    h, 1083 MB: 239 us, 4.5 TB/s (counters: 493 MB read, 622
 //                    MB written).  The same by k_glu_bwd and the dual-layout
 //                    quantizer moves 2.1 GB.
 #include "act_device.h"
@@ -254,7 +254,7 @@ hipError_t by_act(int act, F&& f)
 // What it waits for, timed with parts of it left out (8192 x 14336, 263 us
 // then): no loads and no stores 179 us, no loads 193, no stores 223.  So the
 // arithmetic (five encodings of 1 1/2 steps an element, the gate, the block
-// maxima; vector units busy 46% of the time at two waves a SIMD) and the
+// maxima; vector units busy 47% of the time at two waves a SIMD) and the
 // memory traffic overlap in part; one workgroup a CU, held by 256 registers a
 // lane and 129 KiB of LDS, meets at two barriers a tile.  Measured slower: 16
 // waves with 4 x 4 values a lane (275 us: half-line loads), 64-row tiles two

@@ -27,7 +27,7 @@
 // 5.1 TB/s)
 //   k_norm_fwd       T threads hold a row in registers (N chunks of eight
 //                    elements each): read once, written once.  RMS norm with
-//                    residual, sum, y and checkpoint, 303 MB: 52 us, 5.8 TB/s
+//                    residual, sum, y and checkpoint, 303 MB: 53 us, 5.7 TB/s
 //                    (counters: 134 MB read, 169 MB written).
 //   k_norm_fwd_wide  rows beyond 16384: a workgroup walks the row, and reads
 //                    it again for each of the statistics and the output.
