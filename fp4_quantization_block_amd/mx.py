@@ -449,15 +449,46 @@ def _dense(t: torch.Tensor, shape, dtype, at: int, name: str) -> int:
     raise _misfit(t, shape, dtype, at, name, "be contiguous")
 
 
-def _source(x: torch.Tensor, name: str) -> int:
-    """Source dtype code of a 2-D operand."""
-    if x.dim() != 2:
+def _first(x: torch.Tensor, name: str):
+    """(source code, shape, type, device, address, row stride) of a call's first operand."""
+    shape, dtype, at = x.shape, x.dtype, x.get_device()
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
-    if x.dtype is torch.bfloat16:
-        return MX_SRC_BF16
-    if x.dtype is torch.float32:
-        return MX_SRC_F32
-    raise TypeError(f"{name} must be float32 or bfloat16")
+    if dtype is torch.bfloat16:
+        src = MX_SRC_BF16
+    elif dtype is torch.float32:
+        src = MX_SRC_F32
+    else:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return (src, shape, dtype, at, *_matrix(x, shape, dtype, at, name))
+
+
+# What a call writes: the caller's tensor, looked at as above, or a new one,
+# which needs no looking at.  (A new one costs 1.2 us by empty_like and 1.4 by
+# new_empty_strided; new_empty, which first works out the strides, 1.6-1.8.)
+
+def _out_matrix(t: Optional[torch.Tensor], first: torch.Tensor, shape, dtype, at: int, name: str):
+    """(tensor, address, row stride) of a matrix output of the first operand's shape."""
+    if t is None:
+        t = torch.empty_like(first, dtype=dtype)
+        return t, t.data_ptr(), shape[1]
+    return (t, *_matrix(t, shape, dtype, at, name))
+
+
+def _out_vector(t: Optional[torch.Tensor], first: torch.Tensor, n: int, at: int, name: str):
+    """(tensor, address) of a float32 vector output."""
+    if t is None:
+        t = first.new_empty_strided((n,), (1,), dtype=torch.float32)
+        return t, t.data_ptr()
+    return t, _dense(t, (n,), torch.float32, at, name)
+
+
+def _out_bytes(t: Optional[torch.Tensor], first: torch.Tensor, shape, at: int, name: str):
+    """(tensor, address) of codes or scales."""
+    if t is None:
+        t = first.new_empty_strided(shape, (shape[1], 1), dtype=torch.uint8)
+        return t, t.data_ptr()
+    return t, _dense(t, shape, torch.uint8, at, name)
 
 
 def _out_dtype(dtype, default):
@@ -470,7 +501,7 @@ def _out_dtype(dtype, default):
     raise TypeError("out_dtype must be float32 or bfloat16")
 
 
-def _copy_out(fmt, q, s, shape, first, names):
+def _copy_out(fmt, q, s, shape, first, at, names):
     """(format code, codes, scales, their addresses) of a row copy to be
     written, new where the caller gave none; nothing without a format.
     first: the call's first tensor."""
@@ -478,14 +509,9 @@ def _copy_out(fmt, q, s, shape, first, names):
         if q is not None or s is not None:
             raise ValueError(f"{names[0]} need a format")
         return 0, None, None, None, None
-    rows, cols = shape
-    blocks = (rows, cols // 32)
-    at = first.get_device()
-    if q is None:
-        q = first.new_empty(shape, dtype=torch.uint8)
-    if s is None:
-        s = first.new_empty(blocks, dtype=torch.uint8)
-    return _fmt(fmt), q, s, _dense(q, shape, torch.uint8, at, names[0]), _dense(s, blocks, torch.uint8, at, names[1])
+    q, pq = _out_bytes(q, first, shape, at, names[0])
+    s, ps = _out_bytes(s, first, (shape[0], shape[1] // 32), at, names[1])
+    return _fmt(fmt), q, s, pq, ps
 
 
 def _copy_in(c: Optional[Checkpoint], shape, at: int, names):
@@ -521,11 +547,13 @@ def _params(weight, bias, cols: int, at: int):
 # the handle of a device's current stream; torch.cuda.current_stream() builds
 # an object around it (2.7 us against 0.1 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch.cuda.current_device() without its look at whether torch has started the GPU
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_on(stream, at: int) -> int:
     """The given stream, or the current one."""
-    if at < 0 or at != torch.cuda.current_device():
+    if at < 0 or at != _device():
         raise ValueError("the tensors must be on the current GPU")
     if stream is not None:
         return stream.cuda_stream
@@ -540,35 +568,31 @@ def mx_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias
     """RMS norm or layer norm of x (+ residual), with y as a tensor, as an MX
     row copy (y_fmt) or both, and the 8-bit checkpoint (ckpt_fmt) of what was
     normalised.  stats: also mean (layer norm) and rstd for the backward."""
-    src = _source(x, "x")
-    shape, dtype, at, k = x.shape, x.dtype, x.get_device(), NORMS[kind]
+    src, shape, dtype, at, px, ld_x = _first(x, "x")
     rows, cols = shape
-    px, ld_x = _matrix(x, shape, dtype, at, "x")
-    pres, ld_res = _maybe_matrix(residual, shape, dtype, at, "residual")
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out needs a residual")
-    elif sum_out is None:
-        sum_out = torch.empty_like(x)
-    psum, ld_sum = _maybe_matrix(sum_out, shape, dtype, at, "sum_out")
+    k = NORMS[kind]
+    pres = psum = py = None
+    ld_res = ld_sum = ld_y = 0
+    if residual is not None:
+        pres, ld_res = _matrix(residual, shape, dtype, at, "residual")
+        sum_out, psum, ld_sum = _out_matrix(sum_out, x, shape, dtype, at, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
     out_dtype, out = _out_dtype(out_dtype, dtype)
-    if not write_y:
+    if write_y:
+        y, py, ld_y = _out_matrix(y, x, shape, out_dtype, at, "y")
+    else:
         y = None
-    elif y is None:
-        y = x.new_empty(shape, dtype=out_dtype)
-    py, ld_y = _maybe_matrix(y, shape, out_dtype, at, "y")
-    yf, qy, sy, pqy, psy = _copy_out(y_fmt, qy, sy, shape, x, _Y)
-    cf, qx, sx, pqx, psx = _copy_out(ckpt_fmt, qx, sx, shape, x, _X)
+    yf, qy, sy, pqy, psy = _copy_out(y_fmt, qy, sy, shape, x, at, _Y)
+    cf, qx, sx, pqx, psx = _copy_out(ckpt_fmt, qx, sx, shape, x, at, _X)
     pw, pb, pd = _params(weight, bias, cols, at)
     pmean = prstd = None
     if stats:
-        rstd = x.new_empty(rows, dtype=torch.float32) if rstd is None else rstd
-        prstd = _dense(rstd, (rows,), torch.float32, at, "rstd")
+        rstd, prstd = _out_vector(rstd, x, rows, at, "rstd")
     else:
         rstd = None
     if stats and k == MX_NORM_LAYER:
-        mean = x.new_empty(rows, dtype=torch.float32) if mean is None else mean
-        pmean = _dense(mean, (rows,), torch.float32, at, "mean")
+        mean, pmean = _out_vector(mean, x, rows, at, "mean")
     else:
         mean = None
     _check(load().mx_norm_forward(px, ld_x, pres, ld_res, src, rows, cols, k, pw, pb, pd, eps, psum, ld_sum, py,
@@ -584,37 +608,36 @@ def mx_norm_backward(dy: torch.Tensor, rstd: torch.Tensor, x: Optional[torch.Ten
     """Gradients of mx_norm_forward from what it normalised (x) or from its
     checkpoint; dsum is a gradient of the same tensor from elsewhere, added
     to dx.  dweight and dbias are float32."""
-    src = _source(dy, "dy")
-    shape, dtype, at, k = dy.shape, dy.dtype, dy.get_device(), NORMS[kind]
+    src, shape, dtype, at, pdy, ld_dy = _first(dy, "dy")
     rows, cols = shape
-    pdy, ld_dy = _matrix(dy, shape, dtype, at, "dy")
+    k = NORMS[kind]
     px, ld_x = _maybe_matrix(x, shape, dtype, at, "x")
     cf, pqx, psx = _copy_in(ckpt, shape, at, _X)
     prstd = _dense(rstd, (rows,), torch.float32, at, "rstd")
     pmean = _dense(mean, (rows,), torch.float32, at, "mean") if k == MX_NORM_LAYER and mean is not None else None
     pds, ld_ds = _maybe_matrix(dsum, shape, dtype, at, "dsum")
-    dx = torch.empty_like(dy) if dx is None else dx
-    pdx, ld_dx = _matrix(dx, shape, dtype, at, "dx")
+    dx, pdx, ld_dx = _out_matrix(dx, dy, shape, dtype, at, "dx")
     pw, _, pd = _params(weight, None, cols, at)
     pdw = pdb = pwork = None
     nbytes = 0
     L = load()
     if want_dweight:
-        dweight = dy.new_empty(cols, dtype=torch.float32) if dweight is None else dweight
-        pdw = _dense(dweight, (cols,), torch.float32, at, "dweight")
+        dweight, pdw = _out_vector(dweight, dy, cols, at, "dweight")
     else:
         dweight = None
     if want_dbias:
-        dbias = dy.new_empty(cols, dtype=torch.float32) if dbias is None else dbias
-        pdb = _dense(dbias, (cols,), torch.float32, at, "dbias")
+        dbias, pdb = _out_vector(dbias, dy, cols, at, "dbias")
     else:
         dbias = None
     if want_dweight or want_dbias:
         if work is None:
-            work = dy.new_empty(L.mx_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8)
+            nbytes = L.mx_norm_backward_workspace_bytes(rows, cols)
+            work = dy.new_empty_strided((nbytes,), (1,), dtype=torch.uint8)
         elif work.get_device() != at or not work.is_contiguous():
             raise ValueError("work must be contiguous and on the device of dy")
-        nbytes, pwork = work.numel() * work.element_size(), work.data_ptr()
+        else:
+            nbytes = work.numel() * work.element_size()
+        pwork = work.data_ptr()
     _check(L.mx_norm_backward(pdy, ld_dy, src, rows, cols, px, ld_x, cf, pqx, psx, pmean, prstd, k, pw, pd, pds,
                               ld_ds, pdx, ld_dx, pdw, pdb, pwork, nbytes, _stream_on(stream, at)))
     return NormBackward(dx, dweight, dbias)
@@ -625,35 +648,31 @@ def mx_glu_forward(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", writ
                    qg=None, sg=None, qu=None, su=None, stream=None) -> GluForward:
     """h = act(gate) * up as a tensor, as an MX row copy (h_fmt) or both, and
     the 8-bit checkpoints (ckpt_fmt) of gate and up."""
-    src = _source(gate, "gate")
-    shape, dtype, at = gate.shape, gate.dtype, gate.get_device()
+    src, shape, dtype, at, pg, ld_g = _first(gate, "gate")
     rows, cols = shape
-    pg, ld_g = _matrix(gate, shape, dtype, at, "gate")
     pu, ld_u = _matrix(up, shape, dtype, at, "up")
     out_dtype, out = _out_dtype(out_dtype, dtype)
-    if not write_h:
-        h = None
-    elif h is None:
-        h = gate.new_empty(shape, dtype=out_dtype)
-    ph, ld_h = _maybe_matrix(h, shape, out_dtype, at, "h")
-    hf, qh, sh, pqh, psh = _copy_out(h_fmt, qh, sh, shape, gate, _H)
-    cf, qg, sg, pqg, psg = _copy_out(ckpt_fmt, qg, sg, shape, gate, _GATE)
-    _, qu, su, pqu, psu = _copy_out(ckpt_fmt, qu, su, shape, gate, _UP)
+    if write_h:
+        h, ph, ld_h = _out_matrix(h, gate, shape, out_dtype, at, "h")
+    else:
+        h, ph, ld_h = None, None, 0
+    hf, qh, sh, pqh, psh = _copy_out(h_fmt, qh, sh, shape, gate, at, _H)
+    cf, qg, sg, pqg, psg = _copy_out(ckpt_fmt, qg, sg, shape, gate, at, _GATE)
+    _, qu, su, pqu, psu = _copy_out(ckpt_fmt, qu, su, shape, gate, at, _UP)
     _check(load().mx_glu_forward(pg, ld_g, pu, ld_u, src, rows, cols, ACTS[act], ph, ld_h, out, hf, pqh, psh, cf,
                                  pqg, psg, pqu, psu, _stream_on(stream, at)))
     return GluForward(h, qh, sh, qg, sg, qu, su)
 
 
 def _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act):
-    """The shared leading arguments of the backward calls."""
-    src = _source(dh, "dh")
-    shape, dtype, at = dh.shape, dh.dtype, dh.get_device()
+    """Shape, type and device of the backward calls' operands, and their shared leading arguments."""
+    src, shape, dtype, at, pd, ld_d = _first(dh, "dh")
     gf, pqg, psg = _copy_in(gate_ckpt, shape, at, _GATE)
     uf, pqu, psu = _copy_in(up_ckpt, shape, at, _UP)
     if gate_ckpt is not None and up_ckpt is not None and gf != uf:
         raise ValueError("the checkpoints of gate and up must have one format")
-    return (*_matrix(dh, shape, dtype, at, "dh"), src, *shape, *_maybe_matrix(gate, shape, dtype, at, "gate"),
-            *_maybe_matrix(up, shape, dtype, at, "up"), gf, pqg, psg, pqu, psu, ACTS[act])
+    return shape, dtype, at, (pd, ld_d, src, *shape, *_maybe_matrix(gate, shape, dtype, at, "gate"),
+                              *_maybe_matrix(up, shape, dtype, at, "up"), gf, pqg, psg, pqu, psu, ACTS[act])
 
 
 def mx_glu_backward(dh: torch.Tensor, gate: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None,
@@ -662,17 +681,14 @@ def mx_glu_backward(dh: torch.Tensor, gate: Optional[torch.Tensor] = None, up: O
                     stream=None) -> GluBackward:
     """Gradients of mx_glu_forward from gate and up, or from their
     checkpoints; recompute_h: also h = act(gate) * up."""
-    head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
-    shape, dtype, at = dh.shape, dh.dtype, dh.get_device()
-    dgate = torch.empty_like(dh) if dgate is None else dgate
-    dup = torch.empty_like(dh) if dup is None else dup
-    if not recompute_h:
-        h = None
-    elif h is None:
-        h = dh.new_empty(shape, dtype=dtype)
-    _check(load().mx_glu_backward(*head, *_matrix(dgate, shape, dtype, at, "dgate"),
-                                  *_matrix(dup, shape, dtype, at, "dup"), *_maybe_matrix(h, shape, dtype, at, "h"),
-                                  _stream_on(stream, at)))
+    shape, dtype, at, head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
+    dgate, pdg, ld_dg = _out_matrix(dgate, dh, shape, dtype, at, "dgate")
+    dup, pdu, ld_du = _out_matrix(dup, dh, shape, dtype, at, "dup")
+    if recompute_h:
+        h, ph, ld_h = _out_matrix(h, dh, shape, dtype, at, "h")
+    else:
+        h, ph, ld_h = None, None, 0
+    _check(load().mx_glu_backward(*head, pdg, ld_dg, pdu, ld_du, ph, ld_h, _stream_on(stream, at)))
     return GluBackward(dgate, dup, h)
 
 
@@ -683,11 +699,10 @@ def mx_glu_backward_dual_layout(dh: torch.Tensor, gate: Optional[torch.Tensor] =
                                 qh_col=None, sh_col=None, stream=None) -> GluBackwardDual:
     """mx_glu_backward straight into the backward GEMMs' operands: the row and
     column copies of [dgate | dup] and (h_fmt) the column copy of h."""
-    head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
-    rows, cols = dh.shape
-    f, q_row, s_row, pqr, psr = _copy_out(fmt, q_row, s_row, (rows, 2 * cols), dh, _ROW)
-    _, q_col, s_col, pqc, psc = _copy_out(fmt, q_col, s_col, (2 * cols, rows), dh, _COL)
-    hf, qh_col, sh_col, pqh, psh = _copy_out(h_fmt, qh_col, sh_col, (cols, rows), dh, _H)
-    _check(load().mx_glu_backward_dual_layout(*head, f, pqr, psr, pqc, psc, hf, pqh, psh,
-                                              _stream_on(stream, dh.get_device())))
+    shape, _, at, head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
+    rows, cols = shape
+    f, q_row, s_row, pqr, psr = _copy_out(fmt, q_row, s_row, (rows, 2 * cols), dh, at, _ROW)
+    _, q_col, s_col, pqc, psc = _copy_out(fmt, q_col, s_col, (2 * cols, rows), dh, at, _COL)
+    hf, qh_col, sh_col, pqh, psh = _copy_out(h_fmt, qh_col, sh_col, (cols, rows), dh, at, _H)
+    _check(load().mx_glu_backward_dual_layout(*head, f, pqr, psr, pqc, psc, hf, pqh, psh, _stream_on(stream, at)))
     return GluBackwardDual(q_row, s_row, q_col, s_col, qh_col, sh_col)
