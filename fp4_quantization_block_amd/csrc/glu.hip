@@ -367,8 +367,11 @@ __device__ __forceinline__ void dual_load_up(const GluBwdJob& a, int64_t row, in
 }
 
 // Staged lines of LB code bytes are LB + 8 bytes apart: the eight lines that
-// a wave writes dwords of at once are four lines apart, and start in eight
-// different groups of eight banks.
+// a wave writes row codes of at once are four lines apart, and start in eight
+// different groups of eight banks.  Column codes are written eight lines
+// apart, two lines to a group of sixteen banks; another order of the bytes
+// there, one line to each eight banks, changed neither the time (236.7 us at
+// 8192 x 14336 both ways) nor the count of conflicts.
 template <int LB> constexpr int line_bytes() { return LB + 8; }
 
 // Codes and scale bytes of B blocks, N values of each in this lane; a block
