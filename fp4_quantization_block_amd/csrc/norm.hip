@@ -343,13 +343,19 @@ __device__ __forceinline__ void store_dx(const NormBwdJob& a, int64_t row, const
 // Workgroups of RPB groups of T threads, a row per group at a time.  The next
 // row's inputs are loaded before the current row is worked on, and the weight
 // stays in registers, except where 1024 threads (128 registers each) hold two
-// chunks.
-template <int T> constexpr int bwd_block() { return T <= 256 ? 512 : T; }
+// chunks.  Two groups of 384 threads for bf16, four of 192: one row ahead of
+// one group is too little in flight for a CU (8192 x 2304 bf16 with a
+// checkpoint 33.6 us against 44.7, 16384 x 2656 59.9 and 71.3, 500 x 2656 9.0
+// and 8.5).  fp32 rows have the bytes with one group of 384 (16384 x 3000
+// 146.7 us, with two 151.7), as have those of 512 threads (8192 x 4096 46.2
+// and 47.7).
+template <int SRC, int T>
+constexpr int bwd_block() { return T == 192 ? 768 : T <= 256 ? 512 : T == 384 && SRC == SRC_BF16 ? 768 : T; }
 
 template <int SRC, int FROM, int MODE, int T, int N>
-__global__ __launch_bounds__(bwd_block<T>()) void k_norm_bwd(NormBwdJob a)
+__global__ __launch_bounds__((bwd_block<SRC, T>())) void k_norm_bwd(NormBwdJob a)
 {
-    constexpr int RPB = bwd_block<T>() / T, W = T < 64 ? 1 : T / 64;
+    constexpr int RPB = bwd_block<SRC, T>() / T, W = T < 64 ? 1 : T / 64;
     typedef Cols<MODE, T> P;
     __shared__ float red[2][2][RPB][W];
     __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? N * T * 8 : 1];
@@ -559,7 +565,9 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(const float* work, int64_t
 // against 65.9, 44.8 against 46.9, 94.4 against 95.0.  Rows of up to 256 share
 // a wave (the norms of single heads).
 // 640 threads are for the forward alone (8192 x 5120: 71.5 us against 72.5 with
-// 768; the backward 63.4 against 60.2).
+// 768; the backward 63.4 against 60.2), 192 for the backward, four rows at a
+// time (16384 x 1536 bf16 37.9 us against 49.8 with 256 threads two at a time
+// and 39.2 four at a time, which is slower for 8192 x 2048, 27.9 against 27.2).
 template <bool BACKWARD, class F>
 hipError_t by_width(int64_t cols, F&& f)
 {
@@ -570,6 +578,8 @@ hipError_t by_width(int64_t cols, F&& f)
     if (cols <= 32 * 8) return f(std::integral_constant<int, 32>(), one);
     if (cols <= 64 * 8) return f(std::integral_constant<int, 64>(), one);
     if (cols <= 128 * 8) return f(std::integral_constant<int, 128>(), one);
+    if constexpr (BACKWARD)
+        if (cols <= 192 * 8) return f(std::integral_constant<int, 192>(), one);
     if (cols <= 256 * 8) return f(std::integral_constant<int, 256>(), one);
     if (cols <= 384 * 8) return f(std::integral_constant<int, 384>(), one);
     if (cols <= 512 * 8) return f(std::integral_constant<int, 512>(), one);
@@ -655,10 +665,10 @@ hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
         }
     } else {
         const hipError_t e = by_width<true>(j.cols, [&](auto T, auto N) {
-            constexpr int RPB = bwd_block<T>() / T;
+            constexpr int RPB = bwd_block<SRC, T>() / T;
             parts = (j.rows + RPB - 1) / RPB;
             parts = parts < most_parts(j.cols) ? parts : most_parts(j.cols);
-            k_norm_bwd<SRC, FROM, MODE, T, N><<<dim3((unsigned)parts), dim3(bwd_block<T>()), 0, s>>>(j);
+            k_norm_bwd<SRC, FROM, MODE, T, N><<<dim3((unsigned)parts), dim3(bwd_block<SRC, T>()), 0, s>>>(j);
             return hipGetLastError();
         });
         if (e != hipSuccess) return e;

@@ -15,7 +15,7 @@ EPS = 1e-5
 
 # row lengths at which the kernels, or the last chunk, change
 COLS = [1, 2, 7, 8, 16, 31, 32, 33, 64, 65, 100, 128, 129, 200, 256, 257, 384, 509, 512, 513, 520, 1000, 1024,
-        1025, 2048, 2049, 2056, 3080, 4096, 4097, 5000, 5121, 6144, 6145, 8192, 8193, 16384, 16385, 20000,
+        1025, 1536, 1537, 2048, 2049, 2056, 3080, 4096, 4097, 5000, 5121, 6144, 6145, 8192, 8193, 16384, 16385, 20000,
         24577]
 
 
@@ -207,6 +207,16 @@ def test_backward_rows(rows, cols):
     x, dy, w, mean, rstd = _backward_case(rows, cols, torch.float32, "layer")
     out = mx.mx_norm_backward(dy, rstd, x=x, mean=mean, weight=w, kind="layer", want_dbias=True)
     _check_backward(out, dy, x.cpu().double(), mean, rstd, w, None, "layer", f"{rows}x{cols}")
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 7, 255, 511, 513, 1023, 1025, 1300, 2600])
+@pytest.mark.parametrize("cols", [1056, 1100, 2304, 2305])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_backward_rows_in_groups(rows, cols, dtype):
+    """Row counts around the number of rows that a workgroup takes at a time."""
+    x, dy, w, mean, rstd = _backward_case(rows, cols, dtype, "layer")
+    out = mx.mx_norm_backward(dy, rstd, x=x, mean=mean, weight=w, kind="layer", want_dbias=True)
+    _check_backward(out, dy, x.cpu().double(), mean, rstd, w, None, "layer", f"{rows}x{cols} {dtype}")
 
 
 @pytest.mark.parametrize("rows", [1, 70, 130])
