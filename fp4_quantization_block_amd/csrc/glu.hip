@@ -663,10 +663,10 @@ hipError_t run_dual(const GluBwdJob& j, DualTiles n, int cus, hipStream_t s)
     return hipGetLastError();
 }
 
-// Tiles of 128 x 128, or, where there are fewer of them than CUs, of 32 x 64
-// (288 x 4096: 10.2 us against 13.8; 32 x 14336: 8.3 and 11.4; from as many
-// tiles as CUs on the large ones: 1024 x 4096 18.3 and 18.5, 2048 x 14336 80
-// and 113).
+// Tiles of 128 x 128, or, where no wave then has more than one of them, of 32
+// x 64 (288 x 4096: 10.2 us against 13.8; 32 x 14336: 8.3 and 11.4; 288 x
+// 14336 15.8 and 22.5; 1024 x 4096 16.1 and 16.7).  With more, the large ones:
+// 1536 x 4096 25.1 us against 28.8, 2048 x 7168 40 and 60.
 template <int SRC, int ACT, int FROM, int FMT>
 hipError_t run_dual(const GluBwdJob& j, hipStream_t s)
 {
@@ -675,9 +675,9 @@ hipError_t run_dual(const GluBwdJob& j, hipStream_t s)
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
     if (e != hipSuccess) return e;
-    const DualTiles large = tiles(128, 128);
-    if ((int64_t)large.nx * large.ny >= cus) return run_dual<SRC, ACT, FROM, FMT, 4, 2>(j, large, cus, s);
-    return run_dual<SRC, ACT, FROM, FMT, 1, 1>(j, tiles(32, 64), cus, s);
+    const DualTiles small = tiles(32, 64);
+    if ((int64_t)small.nx * small.ny <= 8 * (int64_t)cus) return run_dual<SRC, ACT, FROM, FMT, 1, 1>(j, small, cus, s);
+    return run_dual<SRC, ACT, FROM, FMT, 4, 2>(j, tiles(128, 128), cus, s);
 }
 
 // f(where gate and up come from)

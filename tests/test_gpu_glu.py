@@ -188,7 +188,7 @@ def test_dual_layout(rows, cols, fmt, h_fmt, act):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
-@pytest.mark.parametrize("rows,cols", [(32, 32), (160, 2080), (256, 512), (2144, 2080), (96, 40960), (160, 40992)])
+@pytest.mark.parametrize("rows,cols", [(32, 32), (160, 2080), (256, 512), (2144, 2080), (96, 40960), (128, 40960), (160, 40992)])
 def test_dual_layout_from_checkpoints(rows, cols, fmt):
     """From checkpoints, with bf16 dh: the fp32 gradients come from the same
     values through fp32 inputs."""
@@ -202,7 +202,7 @@ def test_dual_layout_from_checkpoints(rows, cols, fmt):
     _check_dual(d16, b16, "e5m2", "e4m3", f"{rows}x{cols} bf16")
 
 
-@pytest.mark.parametrize("rows,cols", [(96, 96), (4096, 1024)])
+@pytest.mark.parametrize("rows,cols", [(96, 96), (4096, 1024), (4096, 1088)])
 def test_dual_layout_special_blocks(rows, cols):
     """Zero, subnormal, huge, Inf and NaN places: blocks in both directions as
     the quantizer encodes them, in both kernels' tiles."""
