@@ -341,9 +341,9 @@ __device__ __forceinline__ void store_dx(const NormBwdJob& a, int64_t row, const
 }
 
 // Workgroups of RPB groups of T threads, a row per group at a time.  The next
-// row's inputs are loaded before the current row is worked on, and the weight
-// stays in registers, except where 1024 threads (128 registers each) hold two
-// chunks.  Two groups of 384 threads for bf16, four of 192: one row ahead of
+// row's inputs are loaded before the current row is worked on, except where
+// 1024 threads (128 registers each) hold two chunks, and the weight stays in
+// registers where a thread has one chunk.  Two groups of 384 threads for bf16, four of 192: one row ahead of
 // one group is too little in flight for a CU (8192 x 2304 bf16 with a
 // checkpoint 33.6 us against 44.7, 16384 x 2656 59.9 and 71.3, 500 x 2656 9.0
 // and 8.5).  fp32 rows have the bytes with one group of 384 (16384 x 3000
@@ -360,7 +360,7 @@ __global__ __launch_bounds__((bwd_block<SRC, T>())) void k_norm_bwd(NormBwdJob a
     __shared__ float red[2][2][RPB][W];
     __shared__ float part[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? N * T * 8 : 1];
     const int t = (int)threadIdx.x % T, sub = (int)threadIdx.x / T;
-    constexpr bool AHEAD = N == 1;
+    constexpr bool AHEAD = N == 1 || T == 512, KEEP = N == 1;
     float w[N][8], dw[N][8], db[N][8];
     auto weight = [&](int j) {
 #pragma unroll
@@ -371,7 +371,7 @@ __global__ __launch_bounds__((bwd_block<SRC, T>())) void k_norm_bwd(NormBwdJob a
     for (int j = 0; j < N; j++) {
 #pragma unroll
         for (int i = 0; i < 8; i++) dw[j][i] = 0.0f, db[j][i] = 0.0f;
-        if (AHEAD) weight(j);
+        if (KEEP) weight(j);
     }
     const float n = (float)a.cols;
     BwdRaw<SRC, FROM, MODE> raw[N];
@@ -402,7 +402,7 @@ __global__ __launch_bounds__((bwd_block<SRC, T>())) void k_norm_bwd(NormBwdJob a
 #pragma unroll
             for (int j = 0; j < N; j++) {
                 const P p(j, t, a.cols);
-                if (!AHEAD) weight(j);
+                if (!KEEP) weight(j);
                 raw_values<SRC, MODE>(now[j].dy, g[j]);
                 unit_values(now[j], m, r, h[j]);
 #pragma unroll
@@ -568,7 +568,12 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(const float* work, int64_t
 // 768; the backward 63.4 against 60.2), 192 for the backward, four rows at a
 // time (16384 x 1536 bf16 37.9 us against 49.8 with 256 threads two at a time
 // and 39.2 four at a time, which is slower for 8192 x 2048, 27.9 against 27.2).
-template <bool BACKWARD, class F>
+// Rows of 8193 to 12288 bf16 elements in the backward: 512 threads with three
+// chunks, which have the registers to load a row ahead (4096 x 8224 with a
+// checkpoint 65.8 us against 75.6 with two chunks of 1024 threads, 4096 x 12288
+// 82.9 and 90.1).  In fp32 three chunks spill (146 us against 124 at 4096 x
+// 8224), as do four chunks, and three in the STRIDED form.
+template <bool BACKWARD, int SRC, int MODE, class F>
 hipError_t by_width(int64_t cols, F&& f)
 {
     constexpr std::integral_constant<int, 1> one;
@@ -587,6 +592,8 @@ hipError_t by_width(int64_t cols, F&& f)
         if (cols <= 640 * 8) return f(std::integral_constant<int, 640>(), one);
     if (cols <= 768 * 8) return f(std::integral_constant<int, 768>(), one);
     if (cols <= 1024 * 8) return f(std::integral_constant<int, 1024>(), one);
+    if constexpr (BACKWARD && SRC == SRC_BF16 && MODE != STRIDED)
+        if (cols <= 3 * 512 * 8) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 3>());
     return f(std::integral_constant<int, 1024>(), two);
 }
 
@@ -632,7 +639,7 @@ hipError_t launch_fwd(const NormFwdJob& job, hipStream_t s)
             k_norm_fwd_wide<SRC, MODE><<<dim3((unsigned)n), dim3(1024), 0, s>>>(rows_of<SRC>(job, r, n));
         });
     }
-    return by_width<false>(job.cols, [&](auto T, auto N) {
+    return by_width<false, SRC, MODE>(job.cols, [&](auto T, auto N) {
         constexpr int B = T < 128 ? 256 : (int)T, RPB = B / T;
         return sliced(job.rows, T, [&](int64_t r, int64_t n) {
             k_norm_fwd<SRC, MODE, T, N><<<dim3((unsigned)((n + RPB - 1) / RPB)), dim3(B), 0, s>>>(rows_of<SRC>(job, r, n));
@@ -664,7 +671,7 @@ hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
             k_norm_cols<SRC, FROM, MODE><<<dim3((unsigned)((j.cols + 2047) / 2048), (unsigned)parts), dim3(256), 0, s>>>(j, per);
         }
     } else {
-        const hipError_t e = by_width<true>(j.cols, [&](auto T, auto N) {
+        const hipError_t e = by_width<true, SRC, MODE>(j.cols, [&](auto T, auto N) {
             constexpr int RPB = bwd_block<SRC, T>() / T;
             parts = (j.rows + RPB - 1) / RPB;
             parts = parts < most_parts(j.cols) ? parts : most_parts(j.cols);

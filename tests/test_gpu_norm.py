@@ -15,7 +15,7 @@ EPS = 1e-5
 
 # row lengths at which the kernels, or the last chunk, change
 COLS = [1, 2, 7, 8, 16, 31, 32, 33, 64, 65, 100, 128, 129, 200, 256, 257, 384, 509, 512, 513, 520, 1000, 1024,
-        1025, 1536, 1537, 2048, 2049, 2056, 3080, 4096, 4097, 5000, 5121, 6144, 6145, 8192, 8193, 16384, 16385, 20000,
+        1025, 1536, 1537, 2048, 2049, 2056, 3080, 4096, 4097, 5000, 5121, 6144, 6145, 8192, 8193, 12288, 12289, 16384, 16385, 20000,
         24577]
 
 
@@ -217,6 +217,14 @@ def test_backward_rows_in_groups(rows, cols, dtype):
     x, dy, w, mean, rstd = _backward_case(rows, cols, dtype, "layer")
     out = mx.mx_norm_backward(dy, rstd, x=x, mean=mean, weight=w, kind="layer", want_dbias=True)
     _check_backward(out, dy, x.cpu().double(), mean, rstd, w, None, "layer", f"{rows}x{cols} {dtype}")
+
+
+@pytest.mark.parametrize("rows", [1, 2, 257, 600])
+@pytest.mark.parametrize("cols", [8200, 10243, 12288])
+def test_backward_rows_of_three_chunks(rows, cols):
+    x, dy, w, mean, rstd = _backward_case(rows, cols, torch.bfloat16, "layer")
+    out = mx.mx_norm_backward(dy, rstd, x=x, mean=mean, weight=w, kind="layer", want_dbias=True)
+    _check_backward(out, dy, x.cpu().double(), mean, rstd, w, None, "layer", f"{rows}x{cols}")
 
 
 @pytest.mark.parametrize("rows", [1, 70, 130])
