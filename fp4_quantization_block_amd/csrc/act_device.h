@@ -300,7 +300,7 @@ enum : int { FROM_TENSOR = -1, FROM_E4M3 = E4M3, FROM_E5M2 = E5M2 };
 //              d = P(x) + x e^(-x^2/2) / sqrt(2 pi)
 //   GELU_TANH  x/2 (1 + tanh z) with z = sqrt(2/pi) (x + 0.044715 x^3).
 //              (1 + tanh z) / 2 = 1 / (1 + e^-2z) = s, so a = x s and
-//              d = s + a (1 - s) z2',  z2' = 2 dz/dx
+//              d = s + a (1 - s) z2',  z2' = 2 dz/dx,  1 - s = e^-2z s
 // Exponentials are the hardware's base-2 one, divisions its reciprocal, each
 // within 1 ulp; the product with log2 e is rounded once, so e^-x is off by a
 // relative |x| 2^-24 more.  e^-x overflows to Inf for x < -88 and s becomes 0.
@@ -341,12 +341,16 @@ __device__ __forceinline__ void gate(float x, float& a, float& d)
         if constexpr (SLOPE) d = __builtin_fmaf(0.39894228f * x, e, p);
     } else {
         // x^2 is held below 2^40, where s is 0 or 1 for long: no overflow to
-        // Inf, which the vanishing 1 - s would turn into NaN
+        // Inf, which the vanishing 1 - s would turn into NaN.  1 - s is taken
+        // as e s: the rounded difference would be off by 2^-24 absolutely,
+        // which a z2' multiplies (the slope off by 33 units of 2^-24 at x = 5,
+        // by 4 at most so).  Where e is Inf, s and a are 0: any finite e does.
         constexpr float Z = 1.59576912f, C = 0.044715f;            // 2 sqrt(2/pi)
         const float x2 = fminf(x * x, 0x1p40f);
-        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * __builtin_fmaf(-LOG2E * Z * C, x2, -LOG2E * Z)));
+        const float e = __builtin_amdgcn_exp2f(x * __builtin_fmaf(-LOG2E * Z * C, x2, -LOG2E * Z));
+        const float s = __builtin_amdgcn_rcpf(1.0f + e);
         a = x * s;
-        if constexpr (SLOPE) d = __builtin_fmaf(a * (1.0f - s), __builtin_fmaf(3.0f * Z * C, x2, Z), s);
+        if constexpr (SLOPE) d = __builtin_fmaf(a * (fminf(e, 0x1p127f) * s), __builtin_fmaf(3.0f * Z * C, x2, Z), s);
     }
 }
 
