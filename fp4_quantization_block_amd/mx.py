@@ -145,6 +145,39 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# the handle of a device's current stream; torch.cuda.current_stream() builds
+# an object around it (2.7 us against 0.1 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch.cuda.current_device() without its look at whether torch has started the GPU
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _other(stream) -> bool:
+    """Whether a stream that a call was given is another than the current one."""
+    if stream is None:
+        return False
+    at = _device()
+    here = _raw_stream(at) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream != here or getattr(stream, "device_index", at) != at
+
+
+def _run_on(stream, call, args):
+    """call(**args) on the given stream, with what it allocates taken for that
+    stream: torch hands memory out again in the order of the stream it was
+    taken for, and a call's kernels are in the order of theirs.  New results
+    are known to the caller's stream as well, where they may be dropped."""
+    before = torch.cuda.current_stream()
+    given = {id(a) for a in args.values()}
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        out = call(**{**args, "stream": None})
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and id(t) not in given:
+            t.record_stream(before)
+    return out
+
+
 def _fmt(f) -> int:
     return FMTS[f] if isinstance(f, str) else int(f)
 
@@ -544,13 +577,6 @@ def _params(weight, bias, cols: int, at: int):
             MX_SRC_F32 if dtype is torch.float32 else MX_SRC_BF16)
 
 
-# the handle of a device's current stream; torch.cuda.current_stream() builds
-# an object around it (2.7 us against 0.1 us a call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-# torch.cuda.current_device() without its look at whether torch has started the GPU
-_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
 def _stream_on(stream, at: int) -> int:
     """The given stream, or the current one."""
     if at < 0 or at != _device():
@@ -608,6 +634,8 @@ def mx_norm_backward(dy: torch.Tensor, rstd: torch.Tensor, x: Optional[torch.Ten
     """Gradients of mx_norm_forward from what it normalised (x) or from its
     checkpoint; dsum is a gradient of the same tensor from elsewhere, added
     to dx.  dweight and dbias are float32."""
+    if _other(stream):
+        return _run_on(stream, mx_norm_backward, locals())
     src, shape, dtype, at, pdy, ld_dy = _first(dy, "dy")
     rows, cols = shape
     k = NORMS[kind]

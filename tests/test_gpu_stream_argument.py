@@ -1,0 +1,44 @@
+"""Calls with stream=, on a stream that is busy, while the caller's own stream
+goes on allocating and writing: results as without it, and nobody's memory
+written by the other."""
+import pytest
+import torch
+
+from act_util import dev, rand
+from fp4_quantization_block_amd import mx
+from gpu_util import DEV, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _beside(call, sizes):
+    """call(stream) behind other work on a side stream; meanwhile memory of
+    these sizes (bytes) is taken and filled on the current one."""
+    side = torch.cuda.Stream()
+    work = torch.ones(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(50):                        # some milliseconds
+            work = work * 0.999 + 0.001
+    out = call(side)
+    own = [torch.full((n,), 90 + k, dtype=torch.uint8, device=DEV) for k, n in enumerate(sizes * 3)]
+    torch.cuda.synchronize()
+    for k, t in enumerate(own):
+        assert bool((t == 90 + k).all()), "memory of the current stream was written by the call"
+    return out
+
+
+@pytest.mark.parametrize("rows,cols", [(3000, 4096), (130, 640), (40, 20000)])
+def test_norm_backward(rows, cols):
+    x, dy = dev(rand(1, rows, cols), torch.bfloat16), dev(rand(2, rows, cols), torch.bfloat16)
+    w, r = dev(rand(3, cols), torch.bfloat16), dev(rand(4, rows).abs(), torch.float32)
+    want = mx.mx_norm_backward(dy, r, x=x, weight=w, want_dbias=True)
+    sizes = [int(mx.load().mx_norm_backward_workspace_bytes(rows, cols)), rows * cols * 2, cols * 4]
+    for _ in range(3):
+        got = _beside(lambda s: mx.mx_norm_backward(dy, r, x=x, weight=w, want_dbias=True, stream=s), sizes)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
