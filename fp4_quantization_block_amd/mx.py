@@ -281,6 +281,8 @@ def mx_predict_tensor_scale(w: torch.Tensor, g: torch.Tensor, lr: float, fmt,
                             work: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
                             stream=None) -> torch.Tensor:
     """Predicted per-tensor scale of the next step's weights (weight auto-scaling)."""
+    if _other(stream):
+        return _run_on(stream, mx_predict_tensor_scale, locals())
     src = _src(w)
     if _src(g) != src or tuple(g.shape) != tuple(w.shape):
         raise ValueError("w and g must have the same dtype and shape")

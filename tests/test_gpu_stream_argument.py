@@ -42,3 +42,12 @@ def test_norm_backward(rows, cols):
     for _ in range(3):
         got = _beside(lambda s: mx.mx_norm_backward(dy, r, x=x, weight=w, want_dbias=True, stream=s), sizes)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,cols", [(4096, 4096), (96, 160)])
+def test_predict_tensor_scale(rows, cols):
+    w, g = dev(rand(1, rows, cols), torch.bfloat16), dev(rand(2, rows, cols), torch.bfloat16)
+    want = mx.mx_predict_tensor_scale(w, g, 1e-3, "e4m3")
+    for _ in range(3):
+        got = _beside(lambda s: mx.mx_predict_tensor_scale(w, g, 1e-3, "e4m3", stream=s), [4096, 512])
+        assert torch.equal(got, want)

@@ -105,3 +105,10 @@ def test_the_current_stream_given(world):
     with world:
         mx.mx_norm_backward(X, R, x=X, stream=world.main)
     assert world.on == [11] and set(world.owner.values()) == {11} and not world.recorded
+
+
+def test_predict_tensor_scale(world):
+    _check(world, lambda s: mx.mx_predict_tensor_scale(X, X, 1e-3, "e4m3", stream=s), 1)
+    world.on.clear()
+    world.recorded.clear()
+    _check(world, lambda s: mx.mx_predict_tensor_scale(X, X, 1e-3, "e4m3", None, V[:1], s), 0)
