@@ -217,6 +217,8 @@ def mx_quantize(x: torch.Tensor, axis: int, cfg: mx_qconfig, q: Optional[torch.T
                 scales: Optional[torch.Tensor] = None,
                 tensor_scale: Optional[torch.Tensor] = None, stream=None
                 ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    if (q is None or scales is None or tensor_scale is None) and _other(stream):
+        return _run_on(stream, mx_quantize, locals())
     src = _src(x)
     rows, cols = x.shape
     qs, ss = copy_shapes(rows, cols, axis, cfg.fmt)
@@ -233,6 +235,8 @@ def mx_quantize(x: torch.Tensor, axis: int, cfg: mx_qconfig, q: Optional[torch.T
 
 def mx_quantize_dual_layout(x: torch.Tensor, cfg: mx_qconfig, q_row=None, s_row=None,
                             q_col=None, s_col=None, tensor_scale=None, stream=None):
+    if (q_row is None or s_row is None or q_col is None or s_col is None or tensor_scale is None) and _other(stream):
+        return _run_on(stream, mx_quantize_dual_layout, locals())
     src = _src(x)
     rows, cols = x.shape
     qrs, srs = copy_shapes(rows, cols, MX_AXIS_ROW, cfg.fmt)
@@ -254,6 +258,8 @@ def mx_quantize_dual_layout(x: torch.Tensor, cfg: mx_qconfig, q_row=None, s_row=
 def mx_gemm(qa, sa, ta, fa, qb, sb, tb, fb, M: int, N: int, K: int, alpha: float = 1.0,
             hadamard_k: bool = False, out_dtype: int = MX_OUT_BF16, c=None, ldc=None,
             stream=None) -> torch.Tensor:
+    if c is None and _other(stream):
+        return _run_on(stream, mx_gemm, locals())
     if c is None:
         c = torch.empty((M, N), dtype=torch.float32 if out_dtype == MX_OUT_F32 else torch.bfloat16,
                         device=qa.device)
@@ -267,6 +273,8 @@ def mx_gemm(qa, sa, ta, fa, qb, sb, tb, fb, M: int, N: int, K: int, alpha: float
 def mx_gemm_quantized(qa, sa, ta, fa, qb, sb, tb, fb, M: int, N: int, K: int, out_fmt="e4m3",
                       alpha: float = 1.0, hadamard_k: bool = False, qc=None, sc=None, stream=None):
     """GEMM with the output written as MX codes [M][N] and E8M0 scales [M][N/32]."""
+    if (qc is None or sc is None) and _other(stream):
+        return _run_on(stream, mx_gemm_quantized, locals())
     if qc is None:
         qc = torch.empty((M, N), dtype=torch.uint8, device=qa.device)
     if sc is None:
@@ -302,6 +310,8 @@ def mx_predict_tensor_scale_noalloc(w: torch.Tensor, g: torch.Tensor, lr: float,
                                     scale_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """mx_predict_tensor_scale without a workspace: the library's per-GPU
     scratch holds the partial maxima (calls overlapping on one GPU race)."""
+    if scale_out is None and _other(stream):
+        return _run_on(stream, mx_predict_tensor_scale_noalloc, locals())
     src = _src(w)
     if _src(g) != src or tuple(g.shape) != tuple(w.shape):
         raise ValueError("w and g must have the same dtype and shape")
@@ -316,6 +326,8 @@ def mx_predict_tensor_scale_noalloc(w: torch.Tensor, g: torch.Tensor, lr: float,
 def mx_dequantize(q, scales, tensor_scale, fmt, rows: int, cols: int, axis: int,
                   hadamard: bool = False, out_dtype: int = MX_OUT_F32, out=None,
                   stream=None) -> torch.Tensor:
+    if out is None and _other(stream):
+        return _run_on(stream, mx_dequantize, locals())
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.float32 if out_dtype == MX_OUT_F32 else torch.bfloat16,
                           device=q.device)
@@ -328,6 +340,8 @@ def mx_quantize_optstate(x: torch.Tensor, fmt="e4m3", group: int = 128, q=None, 
                          stream=None):
     """FP8 codes of an fp32 optimizer state after the per-group dynamic
     range expansion; returns (q uint8 [n], amax fp32 [n/group], k fp32 [n/group])."""
+    if (q is None or amax is None or kexp is None) and _other(stream):
+        return _run_on(stream, mx_quantize_optstate, locals())
     if x.dtype != torch.float32 or not x.is_contiguous():
         raise TypeError("x must be a contiguous float32 tensor")
     n = x.numel()
@@ -341,6 +355,8 @@ def mx_quantize_optstate(x: torch.Tensor, fmt="e4m3", group: int = 128, q=None, 
 
 
 def mx_dequantize_optstate(q, amax, kexp, fmt="e4m3", group: int = 128, out=None, stream=None) -> torch.Tensor:
+    if out is None and _other(stream):
+        return _run_on(stream, mx_dequantize_optstate, locals())
     n = q.numel()
     out = torch.empty(n, dtype=torch.float32, device=q.device) if out is None else out
     _check(load().mx_dequantize_optstate(_ptr(q), _ptr(amax), _ptr(kexp), n, group, _fmt(fmt), _ptr(out),
@@ -358,6 +374,8 @@ def mx_quantize_nvfp(x: torch.Tensor, axis: int = MX_AXIS_ROW, local: bool = Fal
                      tscale=None, stream=None):
     """NVFP4 copy of x with a global (local=False) or per-32-row-panel
     (local=True) second-level scale; returns (q, scales, tscale)."""
+    if (q is None or scales is None or tscale is None) and _other(stream):
+        return _run_on(stream, mx_quantize_nvfp, locals())
     src = _src(x)
     rows, cols = x.shape
     qs, ss, ts = nvfp_shapes(rows, cols, axis, local)
@@ -372,6 +390,8 @@ def mx_quantize_nvfp(x: torch.Tensor, axis: int = MX_AXIS_ROW, local: bool = Fal
 
 def mx_dequantize_nvfp(q, scales, tscale, rows: int, cols: int, axis: int = MX_AXIS_ROW, local: bool = False,
                        out_dtype: int = MX_OUT_F32, out=None, stream=None) -> torch.Tensor:
+    if out is None and _other(stream):
+        return _run_on(stream, mx_dequantize_nvfp, locals())
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.float32 if out_dtype == MX_OUT_F32 else torch.bfloat16,
                           device=q.device)
@@ -382,6 +402,8 @@ def mx_dequantize_nvfp(q, scales, tscale, rows: int, cols: int, axis: int = MX_A
 
 def mx_gemm_nvfp(qa, sa, ta, local_a: bool, qb, sb, tb, local_b: bool, M: int, N: int, K: int,
                  alpha: float = 1.0, out_dtype: int = MX_OUT_BF16, c=None, ldc=None, stream=None) -> torch.Tensor:
+    if c is None and _other(stream):
+        return _run_on(stream, mx_gemm_nvfp, locals())
     if c is None:
         c = torch.empty((M, N), dtype=torch.float32 if out_dtype == MX_OUT_F32 else torch.bfloat16,
                         device=qa.device)
@@ -596,6 +618,8 @@ def mx_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias
     """RMS norm or layer norm of x (+ residual), with y as a tensor, as an MX
     row copy (y_fmt) or both, and the 8-bit checkpoint (ckpt_fmt) of what was
     normalised.  stats: also mean (layer norm) and rstd for the backward."""
+    if _other(stream):
+        return _run_on(stream, mx_norm_forward, locals())
     src, shape, dtype, at, px, ld_x = _first(x, "x")
     rows, cols = shape
     k = NORMS[kind]
@@ -678,6 +702,8 @@ def mx_glu_forward(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", writ
                    qg=None, sg=None, qu=None, su=None, stream=None) -> GluForward:
     """h = act(gate) * up as a tensor, as an MX row copy (h_fmt) or both, and
     the 8-bit checkpoints (ckpt_fmt) of gate and up."""
+    if _other(stream):
+        return _run_on(stream, mx_glu_forward, locals())
     src, shape, dtype, at, pg, ld_g = _first(gate, "gate")
     rows, cols = shape
     pu, ld_u = _matrix(up, shape, dtype, at, "up")
@@ -711,6 +737,8 @@ def mx_glu_backward(dh: torch.Tensor, gate: Optional[torch.Tensor] = None, up: O
                     stream=None) -> GluBackward:
     """Gradients of mx_glu_forward from gate and up, or from their
     checkpoints; recompute_h: also h = act(gate) * up."""
+    if _other(stream):
+        return _run_on(stream, mx_glu_backward, locals())
     shape, dtype, at, head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
     dgate, pdg, ld_dg = _out_matrix(dgate, dh, shape, dtype, at, "dgate")
     dup, pdu, ld_du = _out_matrix(dup, dh, shape, dtype, at, "dup")
@@ -729,6 +757,8 @@ def mx_glu_backward_dual_layout(dh: torch.Tensor, gate: Optional[torch.Tensor] =
                                 qh_col=None, sh_col=None, stream=None) -> GluBackwardDual:
     """mx_glu_backward straight into the backward GEMMs' operands: the row and
     column copies of [dgate | dup] and (h_fmt) the column copy of h."""
+    if _other(stream):
+        return _run_on(stream, mx_glu_backward_dual_layout, locals())
     shape, _, at, head = _glu_inputs(dh, gate, up, gate_ckpt, up_ckpt, act)
     rows, cols = shape
     f, q_row, s_row, pqr, psr = _copy_out(fmt, q_row, s_row, (rows, 2 * cols), dh, at, _ROW)

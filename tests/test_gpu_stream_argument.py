@@ -51,3 +51,30 @@ def test_predict_tensor_scale(rows, cols):
     for _ in range(3):
         got = _beside(lambda s: mx.mx_predict_tensor_scale(w, g, 1e-3, "e4m3", stream=s), [4096, 512])
         assert torch.equal(got, want)
+
+
+def test_other_calls():
+    """The calls that write new tensors: quantizers, the GEMM, and the activation operators."""
+    rows, cols = 256, 1024
+    x, u, r = (dev(rand(k, rows, cols), torch.bfloat16) for k in (1, 2, 3))
+    xf, cfg = x.float().view(-1), mx.qconfig("e4m3", two_level=True)
+    q, s, t = mx.mx_quantize(x, mx.MX_AXIS_ROW, cfg)
+    c = dict(gate_ckpt=mx.checkpoint("e4m3", q, s), up_ckpt=mx.checkpoint("e4m3", q, s))
+    torch.cuda.synchronize()
+    calls = [
+        lambda k: mx.mx_quantize(x, mx.MX_AXIS_COL, cfg, stream=k),
+        lambda k: mx.mx_quantize_dual_layout(x, cfg, stream=k),
+        lambda k: (mx.mx_gemm(q, s, t, "e4m3", q, s, t, "e4m3", rows, rows, cols, stream=k),),
+        lambda k: mx.mx_gemm_quantized(q, s, t, "e4m3", q, s, t, "e4m3", rows, rows, cols, stream=k),
+        lambda k: (mx.mx_dequantize(q, s, t, "e4m3", rows, cols, mx.MX_AXIS_ROW, stream=k),),
+        lambda k: mx.mx_quantize_nvfp(x, stream=k),
+        lambda k: mx.mx_quantize_optstate(xf, stream=k),
+        lambda k: mx.mx_norm_forward(x, kind="layer", residual=r, y_fmt="e4m3", ckpt_fmt="e5m2", stream=k),
+        lambda k: mx.mx_glu_forward(x, u, h_fmt="e4m3", ckpt_fmt="e4m3", stream=k),
+        lambda k: mx.mx_glu_backward(r, x, u, recompute_h=True, stream=k),
+        lambda k: mx.mx_glu_backward_dual_layout(r, h_fmt="e4m3", stream=k, **c),
+    ]
+    for n, call in enumerate(calls):
+        want = call(None)
+        got = _beside(call, [rows * cols * b for b in (1, 2, 4)])
+        assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(got, want)), f"call {n}"

@@ -112,3 +112,32 @@ def test_predict_tensor_scale(world):
     world.on.clear()
     world.recorded.clear()
     _check(world, lambda s: mx.mx_predict_tensor_scale(X, X, 1e-3, "e4m3", None, V[:1], s), 0)
+
+
+E4M3 = mx.qconfig("e4m3")
+A = (CODES, SCALES, None, "e4m3")
+CK = dict(gate_ckpt=mx.checkpoint("e4m3", CODES, SCALES), up_ckpt=mx.checkpoint("e4m3", CODES, SCALES))
+CALLS = {
+    "quantize": (lambda s: mx.mx_quantize(X, mx.MX_AXIS_ROW, E4M3, stream=s), 2),
+    "quantize, two levels": (lambda s: mx.mx_quantize(X, mx.MX_AXIS_ROW, mx.qconfig("e4m3", two_level=True), stream=s), 3),
+    "quantize, positional": (lambda s: mx.mx_quantize(X, 0, E4M3, CODES, None, None, s), 1),
+    "dual layout": (lambda s: mx.mx_quantize_dual_layout(X, E4M3, stream=s), 4),
+    "gemm": (lambda s: mx.mx_gemm(*A, *A, ROWS, ROWS, COLS, stream=s), 1),
+    "gemm, quantized": (lambda s: mx.mx_gemm_quantized(*A, *A, ROWS, ROWS, COLS, stream=s), 2),
+    "predict, no workspace": (lambda s: mx.mx_predict_tensor_scale_noalloc(X, X, 1e-3, "e4m3", stream=s), 1),
+    "dequantize": (lambda s: mx.mx_dequantize(CODES, SCALES, None, "e4m3", ROWS, COLS, 0, stream=s), 1),
+    "quantize optstate": (lambda s: mx.mx_quantize_optstate(X.view(-1), stream=s), 3),
+    "dequantize optstate": (lambda s: mx.mx_dequantize_optstate(CODES.view(-1), V, V, stream=s), 1),
+    "quantize nvfp": (lambda s: mx.mx_quantize_nvfp(X, stream=s), 3),
+    "dequantize nvfp": (lambda s: mx.mx_dequantize_nvfp(CODES, SCALES, V, ROWS, COLS, stream=s), 1),
+    "gemm nvfp": (lambda s: mx.mx_gemm_nvfp(CODES, SCALES, V, False, CODES, SCALES, V, False, ROWS, ROWS, COLS, stream=s), 1),
+    "norm": (lambda s: mx.mx_norm_forward(X, kind="layer", residual=X, y_fmt="e4m3", ckpt_fmt="e4m3", stream=s), 8),
+    "glu": (lambda s: mx.mx_glu_forward(X, X, h_fmt="e4m3", ckpt_fmt="e4m3", stream=s), 7),
+    "glu gradient": (lambda s: mx.mx_glu_backward(X, X, X, recompute_h=True, stream=s), 3),
+    "glu gradient, dual layout": (lambda s: mx.mx_glu_backward_dual_layout(X, h_fmt="e4m3", stream=s, **CK), 6),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_results(name, world):
+    _check(world, *CALLS[name])
