@@ -693,8 +693,11 @@ hipError_t by_source(const GluBwdJob& j, F&& f)
 
 hipError_t launch_glu_fwd(const GluFwdJob& j, hipStream_t s)
 {
+    // (checkpoints and row copies of odd rows are refused: what the overlapping
+    // chunks can write over is h)
+    const bool in_place = j.h && (j.h == j.gate || j.h == j.up);
     return by_act(j.act, [&](auto A) {
-        return by_mode(j.cols, false, [&](auto mode) {
+        return by_mode(j.cols, in_place, [&](auto mode) {
             return j.src == SRC_F32 ? run_fwd<SRC_F32, A, mode>(j, s) : run_fwd<SRC_BF16, A, mode>(j, s);
         });
     });

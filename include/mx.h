@@ -466,9 +466,10 @@ int64_t mx_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *   MX_ACT_GELU_TANH  act(g) = g/2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
  * gate, up: `src_dtype`, strides of their own (e.g. the halves of one fused
  *        projection's output).
- * h:     `out_dtype` matrix, or NULL.   qh, sh: h as a row copy of format
- *        h_fmt (the down projection's A operand), or both NULL.  At least
- *        one of h and qh.
+ * h:     `out_dtype` matrix, or NULL; it may be gate or up themselves (same
+ *        pointer, stride and type).   qh, sh: h as a row copy of format h_fmt
+ *        (the down projection's A operand), or both NULL.  At least one of h
+ *        and qh.
  * qg, sg, qu, su: checkpoints of gate and up in ckpt_fmt; all four or none.
  */
 mx_status mx_glu_forward(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t src_dtype,
