@@ -707,7 +707,9 @@ int64_t norm_bwd_partials(int64_t rows, int64_t cols)
 
 hipError_t launch_norm_fwd(const NormFwdJob& j, hipStream_t s)
 {
-    const bool in_place = j.residual && (j.sum == j.x || j.sum == j.residual);
+    // a wide row's y is written while what was normalised is read again
+    const bool in_place = (j.residual && (j.sum == j.x || j.sum == j.residual)) ||
+                          (j.cols > NORM_WIDE && j.y && (j.y == j.x || j.y == j.sum));
     return by_mode(j.cols, in_place, [&](auto mode) {
         return j.src == SRC_F32 ? launch_fwd<SRC_F32, mode>(j, s) : launch_fwd<SRC_BF16, mode>(j, s);
     });

@@ -416,9 +416,10 @@ mx_status mx_gemm_nvfp(const uint8_t* qa, const uint8_t* sa, const float* ta, in
  * weight, bias: cols values of `param_dtype` (MX_SRC_F32 / MX_SRC_BF16), or
  *        NULL (1 and 0; param_dtype is then ignored).
  * eps:   finite, >= 0.
- * y:     `out_dtype` matrix, or NULL.   qy, sy: y as a row copy of format
- *        y_fmt (the next GEMM's A operand), or both NULL.  At least one of y
- *        and qy.
+ * y:     `out_dtype` matrix, or NULL; it may be x, residual or sum (which is
+ *        then lost) themselves (same pointer, stride and type).   qy, sy: y as
+ *        a row copy of format y_fmt (the next GEMM's A operand), or both NULL.
+ *        At least one of y and qy.
  * qx, sx: checkpoint of s in ckpt_fmt, or both NULL.
  * mean, rstd: rows fp32 each, mu and r for the backward pass, or NULL; mean
  *        is not written for MX_NORM_RMS.

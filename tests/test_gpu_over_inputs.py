@@ -42,3 +42,27 @@ def test_glu_forward_over_a_half(over):
     mx.mx_glu_forward(*half, "silu", h=half[over])
     assert torch.equal(half[over], mx.mx_glu_forward(g, u, "silu").h) and torch.equal(half[1 - over], (u, g)[over])
     both.check("gate, up")
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("over", ["x", "x beside a sum", "residual", "sum"])
+@pytest.mark.parametrize("cols", [5, 40, 99, 515, 4097, 16383, 16385, 16392, 20001, 40967])
+def test_norm_forward(cols, over, dtype, kind):
+    """Up to 16384 columns a row is in registers before y is written, and y is
+    the same bit for bit; wider rows are read again, and each y is within the
+    bounds of its definition (the order of the sums may be another)."""
+    rows, dt = 9 if cols > 4096 else 300, DT[dtype]
+    x, w, b = dev(rand(1, rows, cols) + 0.5, dt), dev(rand(3, cols), dt), dev(rand(4, cols), dt)
+    res = None if over == "x" else dev(rand(2, rows, cols), dt)
+    s = x.clone() if res is None else (x.float() + res.float()).to(dt)
+    total = None if res is None else torch.empty_like(x)
+    want = mx.mx_norm_forward(x, w, b, kind=kind, residual=res).y
+    into = {"x": x, "x beside a sum": x, "residual": res, "sum": total}[over]
+    r = mx.mx_norm_forward(x, w, b, kind=kind, residual=res, sum_out=total, y=into)
+    assert r.y is into
+    if cols <= 16384:
+        assert torch.equal(r.y, want)
+    y, err, *_ = R.norm(s.cpu().double(), w.cpu().double(), b.cpu().double(), 1e-5, kind == "layer")
+    R.within(r.y, y, err, f"y over {over}")
+    assert over in ("x", "sum") or torch.equal(total, s)
