@@ -6,6 +6,7 @@
 
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/mx.h"
 #include "mx_internal.h"
@@ -466,6 +467,31 @@ mx_status check_params(const void* weight, const void* bias, int32_t dtype)
     return MX_OK;
 }
 
+// Outputs at an input's address.  A matrix may be written over one that lies
+// alike: a thread then writes the elements that it has read.  Over one of
+// another stride or type, or as codes over a matrix, it would write what other
+// threads have still to read.
+struct Mat { const void* p; int64_t ld; int32_t dtype; };
+
+mx_status check_over(const Mat& out, std::initializer_list<Mat> others, int64_t rows, const char* what)
+{
+    for (const Mat& m : others) {
+        if (!out.p || out.p != m.p || (out.dtype == m.dtype && (rows == 1 || out.ld == m.ld))) continue;
+        char text[96];
+        std::snprintf(text, sizeof text, "%s over another matrix needs its row stride and type", what);
+        return fail(MX_ERR_INVALID_ARG, text);
+    }
+    return MX_OK;
+}
+
+mx_status check_apart(std::initializer_list<const void*> outs, std::initializer_list<const void*> inputs)
+{
+    for (const void* o : outs)
+        for (const void* i : inputs)
+            if (o && o == i) return fail(MX_ERR_INVALID_ARG, "codes and scales must not be written over an input, nor outputs over them");
+    return MX_OK;
+}
+
 }  // namespace
 
 mx_status mx_norm_forward(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, int32_t src_dtype,
@@ -493,6 +519,10 @@ mx_status mx_norm_forward(const void* x, int64_t ld_x, const void* residual, int
     if ((s = check_copy(y_fmt, qy, sy, cols)) != MX_OK) return s;
     if ((s = check_copy(ckpt_fmt, qx, sx, cols)) != MX_OK) return s;
     if ((s = check_f32(mean)) != MX_OK || (s = check_f32(rstd)) != MX_OK) return s;
+    const Mat mi{x, ld_x, src_dtype}, mr{residual, ld_res, src_dtype}, ms{sum, ld_sum, src_dtype};
+    if ((s = check_over(ms, {mi, mr}, rows, "sum")) != MX_OK) return s;
+    if ((s = check_over({y, ld_y, out_dtype}, {mi, mr, ms}, rows, "y")) != MX_OK) return s;
+    if ((s = check_apart({qy, sy, qx, sx}, {x, residual})) != MX_OK) return s;
     mx::NormFwdJob j{};
     j.x = x; j.ld_x = ld_x; j.residual = residual; j.ld_res = ld_res;
     j.src = src_dtype; j.rows = rows; j.cols = cols; j.layer = kind == MX_NORM_LAYER;
@@ -539,6 +569,9 @@ mx_status mx_norm_backward(const void* dy, int64_t ld_dy, int32_t src_dtype, int
     }
     if (cols > mx::NORM_WIDE && (dx == dy || (x && dx == x)))
         return fail(MX_ERR_UNSUPPORTED, "dx over dy or x needs cols <= 16384 (wider rows are read again)");
+    const std::initializer_list<Mat> in = {{dy, ld_dy, src_dtype}, {x, ld_x, src_dtype}, {dsum, ld_dsum, src_dtype}};
+    if ((s = check_over({dx, ld_dx, src_dtype}, in, rows, "dx")) != MX_OK) return s;
+    if ((s = check_apart({dx}, {qx, sx})) != MX_OK) return s;
     mx::NormBwdJob j{};
     j.dy = dy; j.ld_dy = ld_dy; j.src = src_dtype; j.rows = rows; j.cols = cols;
     j.x = x; j.ld_x = ld_x; j.ckpt_fmt = ckpt_fmt; j.qx = (const uint8_t*)qx; j.sx = sx;
@@ -608,6 +641,8 @@ mx_status mx_glu_forward(const void* gate, int64_t ld_gate, const void* up, int6
     if ((s = check_copy(h_fmt, qh, sh, cols)) != MX_OK) return s;
     if ((s = check_copy(ckpt_fmt, qg, sg, cols)) != MX_OK || (s = check_copy(ckpt_fmt, qu, su, cols)) != MX_OK) return s;
     if ((qg != nullptr) != (qu != nullptr)) return fail(MX_ERR_INVALID_ARG, "gate and up are checkpointed together");
+    if ((s = check_over({h, ld_h, out_dtype}, {{gate, ld_gate, src_dtype}, {up, ld_up, src_dtype}}, rows, "h")) != MX_OK) return s;
+    if ((s = check_apart({qh, sh, qg, sg, qu, su}, {gate, up})) != MX_OK) return s;
     mx::GluFwdJob j{};
     j.gate = gate; j.ld_gate = ld_gate; j.up = up; j.ld_up = ld_up;
     j.src = src_dtype; j.rows = rows; j.cols = cols; j.act = act;
@@ -630,6 +665,11 @@ mx_status mx_glu_backward(const void* dh, int64_t ld_dh, int32_t src_dtype, int6
     if ((s = check_matrix(dgate, ld_dgate, cols, src_dtype, "dgate")) != MX_OK) return s;
     if ((s = check_matrix(dup, ld_dup, cols, src_dtype, "dup")) != MX_OK) return s;
     if (h && (s = check_matrix(h, ld_h, cols, src_dtype, "h")) != MX_OK) return s;
+    const std::initializer_list<Mat> in = {{dh, ld_dh, src_dtype}, {gate, ld_gate, src_dtype}, {up, ld_up, src_dtype}};
+    if ((s = check_over({dgate, ld_dgate, src_dtype}, in, rows, "dgate")) != MX_OK) return s;
+    if ((s = check_over({dup, ld_dup, src_dtype}, in, rows, "dup")) != MX_OK) return s;
+    if ((s = check_over({h, ld_h, src_dtype}, in, rows, "h")) != MX_OK) return s;
+    if ((s = check_apart({dgate, dup, h}, {qg, sg, qu, su})) != MX_OK) return s;
     mx::GluBwdJob j = glu_job(dh, ld_dh, src_dtype, rows, cols, gate, ld_gate, up, ld_up, ckpt_fmt, qg, sg, qu, su, act);
     j.dgate = dgate; j.ld_dgate = ld_dgate; j.dup = dup; j.ld_dup = ld_dup;
     j.h = h; j.ld_h = ld_h;
@@ -658,6 +698,7 @@ mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src
     if (!q_row || !s_row || !q_col || !s_col) return fail(MX_ERR_INVALID_ARG, "an output pointer is NULL");
     if ((s = check_copy(fmt, q_row, s_row, cols)) != MX_OK || (s = check_copy(fmt, q_col, s_col, cols)) != MX_OK) return s;
     if ((s = check_copy(h_fmt, qh, sh, cols)) != MX_OK) return s;
+    if ((s = check_apart({q_row, s_row, q_col, s_col, qh, sh}, {dh, gate, up, qg, sg, qu, su})) != MX_OK) return s;
     mx::GluBwdJob j = glu_job(dh, ld_dh, src_dtype, rows, cols, gate, ld_gate, up, ld_up, ckpt_fmt, qg, sg, qu, su, act);
     j.fmt = fmt; j.q_row = (uint8_t*)q_row; j.s_row = s_row; j.q_col = (uint8_t*)q_col; j.s_col = s_col;
     j.h_fmt = h_fmt; j.qh = (uint8_t*)qh; j.sh = sh;

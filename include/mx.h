@@ -403,7 +403,9 @@ mx_status mx_gemm_nvfp(const uint8_t* qa, const uint8_t* sa, const float* ta, in
  * cols < 2^31.  Arithmetic is fp32, each output rounded once (to nearest
  * even); sums are in an order fixed by the shape, with no atomics, so results
  * repeat bit for bit.  NaN and Inf follow the formulas.  Outputs must not
- * overlap inputs or each other, except where said.  Errors as mx_quantize.
+ * overlap inputs or each other, except where said; an output at an input's own
+ * address is refused where it is not (MX_ERR_INVALID_ARG).  Errors as
+ * mx_quantize.
  */
 
 /*
