@@ -529,14 +529,15 @@ __global__ __launch_bounds__(256) void k_norm_cols(NormBwdJob a, int64_t rows_pe
     if (a.dbias) store_row<SRC_F32>(a.work + ((a.dweight ? parts : 0) + part) * a.cols, p, db);
 }
 
-// dw (blockIdx.y 0) and db (1, or 0 without dw): 32 columns per workgroup, 32
-// threads down the partial rows of each column, added by halves at the end
-__global__ __launch_bounds__(1024) void k_norm_colsum(const float* work, int64_t parts, int64_t cols, float* out0,
-                                                      float* out1)
+// dw (blockIdx.y 0) and db (1, or 0 without dw): 32 columns per workgroup, from
+// column c0 on, 32 threads down the partial rows of each column, added by
+// halves at the end
+__global__ __launch_bounds__(1024) void k_norm_colsum(const float* work, int64_t parts, int64_t cols, int64_t c0,
+                                                      float* out0, float* out1)
 {
     __shared__ float sum[32][33];
     const int x = (int)threadIdx.x & 31, y = (int)threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + x;
+    const int64_t c = c0 + (int64_t)blockIdx.x * 32 + x;
     const float* p = work + (int64_t)blockIdx.y * parts * cols;
     float s = 0.0f;
     if (c < cols) {
@@ -598,7 +599,7 @@ hipError_t by_width(int64_t cols, F&& f)
 }
 
 // A launch counts its threads in 32 bits: f(first row, rows) for slices of
-// rows that need at most 2^31, at T threads a row.
+// rows (or of columns) that need at most 2^31, at T threads each.
 template <class F>
 hipError_t sliced(int64_t rows, int64_t T, F&& f)
 {
@@ -682,10 +683,12 @@ hipError_t launch_bwd(const NormBwdJob& j, hipStream_t s)
     }
     if (j.dweight || j.dbias) {
         const bool both = j.dweight && j.dbias;
-        k_norm_colsum<<<dim3((unsigned)((j.cols + 31) / 32), both ? 2u : 1u), dim3(1024), 0, s>>>(
-            j.work, parts, j.cols, j.dweight ? j.dweight : j.dbias, j.dbias);
+        return sliced(j.cols, 32, [&](int64_t c0, int64_t n) {
+            k_norm_colsum<<<dim3((unsigned)((n + 31) / 32), both ? 2u : 1u), dim3(1024), 0, s>>>(
+                j.work, parts, j.cols, c0, j.dweight ? j.dweight : j.dbias, j.dbias);
+        });
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 // f(how the rows are spread): `in_place` where an output is written over an input

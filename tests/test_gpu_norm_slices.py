@@ -98,3 +98,18 @@ def test_wide_rows():
     for p in parts:
         _same(g, mx.mx_norm_backward(x[p], f.rstd[p], x=x[p], mean=f.mean[p], weight=w, kind="layer",
                                      want_dweight=False), p, "gradient")
+
+
+def test_column_sums_of_very_wide_rows():
+    """2^27 and some columns, at 32 threads each: 2^32 threads and more, which
+    the column sums take in three launches.  With rstd = 1 the products of bf16 values are exact in fp32, and a
+    sum of two of them is rounded once."""
+    rows, cols = 2, (1 << 27) + 40
+    x, dy = (torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV).normal_(
+        generator=torch.Generator(device=DEV).manual_seed(k)) for k in (1, 2))
+    one = torch.ones(rows, device=DEV)
+    g = mx.mx_norm_backward(dy, one, x=x, kind="rms", want_dbias=True)
+    p = dy.float() * x.float()
+    assert torch.equal(g.dweight, p[0] + p[1]) and torch.equal(g.dbias, dy[0].float() + dy[1].float())
+    alone = mx.mx_norm_backward(dy, one, x=x, kind="rms", want_dweight=False, want_dbias=True)
+    assert torch.equal(alone.dbias, g.dbias) and torch.equal(alone.dx, g.dx)
