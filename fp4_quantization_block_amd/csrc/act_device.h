@@ -302,8 +302,11 @@ enum : int { FROM_TENSOR = -1, FROM_E4M3 = E4M3, FROM_E5M2 = E5M2 };
 //              (1 + tanh z) / 2 = 1 / (1 + e^-2z) = s, so a = x s and
 //              d = s + a (1 - s) z2',  z2' = 2 dz/dx,  1 - s = e^-2z s
 // Exponentials are the hardware's base-2 one, divisions its reciprocal, each
-// within 1 ulp; the product with log2 e is rounded once, so e^-x is off by a
-// relative |x| 2^-24 more.  e^-x overflows to Inf for x < -88 and s becomes 0.
+// within 1 ulp.  What the exponent's roundings add, relative to the result, for
+// an exponent z: |z| 2^-24 for each rounding, of which SILU's product with
+// log2 e is one (the rounded constant less than a third of that), GELU's square
+// two and GELU_TANH's polynomial three.  e^-x overflows to Inf for x < -88 and
+// s becomes 0.
 // ---------------------------------------------------------------------
 enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
@@ -311,8 +314,11 @@ enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 // e^(-x^2/2): e t Q(t) with t = 1 / (1 + 0.37 |x|).  e^(x^2/2) P(-|x|) / t is
 // smooth in t on (0, 1] (0.37 / sqrt(2 pi) at t = 0), and Q is its polynomial
 // of degree 10, fitted to scipy's erfcx with weights moved to the largest
-// relative errors (Lawson's method): within 2.3e-8 of it, and the whole within
-// 6 units of 2^-24 for |x| < 3 in fp32.  One exponential serves this and the
+// relative errors (Lawson's method).  The coefficients as stored are within
+// 4.1e-8 of it.  The whole, evaluated in fp32 with correctly rounded
+// reciprocals and exponentials, is off by at most 7 units of 2^-24 for |x| < 2,
+// 11 below 3 and 33 below 6, where nearly all of it is the exponent's
+// roundings; they grow with x^2.  One exponential serves this and the
 // density in the slope.  (The forward at 4096 x 14336 bf16: 62 us, bound by
 // memory; with the math library's erfcf 92 us, bound by its instructions.)
 __device__ __forceinline__ float normal_tail(float x, float e)

@@ -29,9 +29,10 @@ namespace mx {
 
 namespace {
 
-// n / d for 32-bit n and a divisor known to the host: d = 2^l' - ... by the
-// round-up method (T. Granlund and P. Montgomery, "Division by Invariant
-// Integers using Multiplication", PLDI 1994, figure 4.1)
+// n / d for 32-bit n and a divisor known to the host, by the round-up method
+// (T. Granlund and P. Montgomery, "Division by Invariant Integers using
+// Multiplication", PLDI 1994, figure 4.1): floor((2^32 + m) n / 2^(32 + l)), 2^l
+// the power of two at or above d and m = floor(2^32 (2^l - d) / d) + 1
 struct FastDiv { uint32_t d, m, s1, s2; };
 
 FastDiv fast_div(uint32_t d)
