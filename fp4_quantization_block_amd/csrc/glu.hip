@@ -601,7 +601,12 @@ __global__ __launch_bounds__(64 * WR * WC) void k_glu_bwd_dual(GluBwdJob a, Dual
                 h[i][c] = act * u[i][c];
                 g[i][c] = dh * u[i][c] * slope;
                 u[i][c] = dh * act;
-                if constexpr (!EARLY) __builtin_amdgcn_sched_barrier(0);   // one at a time: few temporaries
+                // fp32 tensors fill the registers: one element at a time, its
+                // results computed here and not where they are used (178
+                // registers; with the order left to the compiler GELU and
+                // GELU_TANH take 256 and keep more in scratch, 262 and 352 us
+                // at 4096 x 14336 against 217 and 214)
+                if constexpr (!EARLY) asm volatile("" : "+v"(g[i][c]), "+v"(u[i][c]), "+v"(h[i][c]));
             }
         }
         const bool row_writer = (k8 & 3) == 0, col_writer = m == 0;
