@@ -78,3 +78,31 @@ def test_other_calls():
         want = call(None)
         got = _beside(call, [rows * cols * b for b in (1, 2, 4)])
         assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(got, want)), f"call {n}"
+
+
+def test_captured_on_a_joined_stream():
+    """A graph whose gradient runs on a side stream that the capture has been
+    joined to: every replay, with eager work between, gives the eager result."""
+    rows, cols = 200, 2048
+    x, dy = dev(rand(1, rows, cols), torch.bfloat16), dev(rand(2, rows, cols), torch.bfloat16)
+    w, r = dev(rand(3, cols), torch.bfloat16), dev(rand(4, rows).abs(), torch.float32)
+    side = torch.cuda.Stream()
+
+    def step(stream):
+        return mx.mx_norm_backward(dy, r, x=x, weight=w, want_dbias=True, stream=stream)
+
+    step(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        held = step(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for k in range(4):
+        x.copy_(dev(rand(10 + k, rows, cols), torch.bfloat16))
+        dy.copy_(dev(rand(20 + k, rows, cols), torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
