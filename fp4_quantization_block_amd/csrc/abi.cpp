@@ -705,4 +705,123 @@ mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src
     return hip_status(mx::launch_glu_bwd_dual(j, (hipStream_t)stream));
 }
 
+namespace {
+
+constexpr int64_t MOST_ELEMENTS = (int64_t)1 << 35;     // of one tensor: chunks are counted with 32 bits
+
+static bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+static mx_status check_list(const void* tensors, int32_t count)
+{
+    if (count < 0) return fail(MX_ERR_INVALID_ARG, "count must be >= 0");
+    if (count > 0 && !tensors) return fail(MX_ERR_INVALID_ARG, "tensors is NULL");
+    return MX_OK;
+}
+
+static mx_status check_length(int64_t n)
+{
+    if (n < 0 || n > MOST_ELEMENTS) return fail(MX_ERR_INVALID_ARG, "a tensor's n must be in [0, 2^35]");
+    return MX_OK;
+}
+
+static mx_status check_source_dtype(int32_t d)
+{
+    if (d != MX_SRC_F32 && d != MX_SRC_BF16) return fail(MX_ERR_INVALID_ARG, "unknown source dtype");
+    return MX_OK;
+}
+
+static bool in_range(double x, double end) { return x >= 0.0 && x < end; }      // false for NaN
+
+// an output may be its own input, but no other tensor that the step reads or writes
+static mx_status check_adamw_apart(const mx_adamw_tensor& t, bool fp8)
+{
+    const void* in[] = {t.p, t.m, t.v, t.g, t.m_amax, t.m_kexp, t.v_amax, t.v_kexp};
+    const void* out[] = {t.p_out, t.m_out, t.v_out, t.copy, t.m_amax_out, t.m_kexp_out, t.v_amax_out, t.v_kexp_out};
+    const int own[] = {0, 1, 2, -1, 4, 5, 6, 7}, most = fp8 ? 8 : 4;
+    for (int o = 0; o < most; o++) {
+        if (!out[o]) continue;
+        for (int i = 0; i < most; i++)
+            if (out[o] == in[i] && i != own[o]) return fail(MX_ERR_INVALID_ARG, "an output lies over another input than its own");
+        for (int i = 0; i < o; i++)
+            if (out[o] == out[i]) return fail(MX_ERR_INVALID_ARG, "two outputs have one address");
+    }
+    return MX_OK;
+}
+
+}  // namespace
+
+int64_t mx_grad_norm_workspace_bytes(int32_t count) { return count < 0 ? 0 : mx::grad_norm_work_bytes(count); }
+
+mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, int32_t src_dtype, double max_norm, void* work,
+                       int64_t work_bytes, float* out, void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_list(tensors, count);
+    if (s != MX_OK || (s = check_source_dtype(src_dtype)) != MX_OK) return s;
+    if (!(max_norm > 0.0)) return fail(MX_ERR_INVALID_ARG, "max_norm must be > 0");
+    if (!work || !out) return fail(MX_ERR_INVALID_ARG, "work and out must not be NULL");
+    if (work_bytes < mx_grad_norm_workspace_bytes(count))
+        return fail(MX_ERR_INVALID_ARG, "work is smaller than mx_grad_norm_workspace_bytes()");
+    if ((reinterpret_cast<uintptr_t>(work) & 7u) != 0 || off4(out))
+        return fail(MX_ERR_ALIGNMENT, "work must be 8-byte and out 4-byte aligned");
+    for (int32_t i = 0; i < count; i++) {
+        if ((s = check_length(tensors[i].n)) != MX_OK) return s;
+        if (tensors[i].n == 0) continue;
+        if (!tensors[i].x) return fail(MX_ERR_INVALID_ARG, "a tensor is NULL");
+        if (reinterpret_cast<uintptr_t>(tensors[i].x) % elem_bytes(src_dtype) != 0)
+            return fail(MX_ERR_ALIGNMENT, "a tensor is not aligned to its element size");
+        if (tensors[i].x == work || tensors[i].x == out)
+            return fail(MX_ERR_INVALID_ARG, "work and out must not lie over a tensor");
+    }
+    mx::GradNormJob j{};
+    j.tensors = tensors; j.count = count; j.src = src_dtype; j.max_norm = max_norm;
+    j.work = (double*)work; j.out = out;
+    return hip_status(mx::launch_grad_norm(j, (hipStream_t)stream));
+}
+
+mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int32_t count, int32_t p_dtype, int32_t g_dtype,
+                        int32_t state_fmt, int32_t group, const mx_adamw_config* cfg, const float* scale,
+                        void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_list(tensors, count);
+    if (s != MX_OK || (s = check_source_dtype(p_dtype)) != MX_OK || (s = check_source_dtype(g_dtype)) != MX_OK) return s;
+    const bool fp8 = state_fmt != MX_STATE_F32;
+    if (fp8 && (s = check_optstate(group, group, state_fmt)) != MX_OK) return s;
+    if (!cfg) return fail(MX_ERR_INVALID_ARG, "cfg is NULL");
+    const double inf = __builtin_inf();
+    if (!in_range(cfg->lr, inf) || !in_range(cfg->eps, inf) || !in_range(cfg->weight_decay, inf))
+        return fail(MX_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite and >= 0");
+    if (!in_range(cfg->beta1, 1.0) || !in_range(cfg->beta2, 1.0))
+        return fail(MX_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+    if (!cfg->step_dev && cfg->step < 1) return fail(MX_ERR_INVALID_ARG, "step must be >= 1");
+    if (off4(cfg->lr_dev) || off4(scale) || (reinterpret_cast<uintptr_t>(cfg->step_dev) & 7u) != 0)
+        return fail(MX_ERR_ALIGNMENT, "lr_dev and scale must be 4-byte, step_dev 8-byte aligned");
+    for (int32_t i = 0; i < count; i++) {
+        const mx_adamw_tensor& t = tensors[i];
+        if ((s = check_length(t.n)) != MX_OK) return s;
+        if (t.n == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || !t.p_out || !t.m_out || !t.v_out)
+            return fail(MX_ERR_INVALID_ARG, "p, g, m, v and their outputs must not be NULL");
+        if ((reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.p_out)) % elem_bytes(p_dtype) != 0 ||
+            reinterpret_cast<uintptr_t>(t.g) % elem_bytes(g_dtype) != 0 || reinterpret_cast<uintptr_t>(t.copy) % 2 != 0)
+            return fail(MX_ERR_ALIGNMENT, "p, g and copy must be aligned to their element size");
+        if (off4(t.m) || off4(t.v) || off4(t.m_out) || off4(t.v_out))
+            return fail(MX_ERR_ALIGNMENT, "m and v must be 4-byte aligned");
+        if (fp8) {
+            for (const float* f : {t.m_amax, t.m_kexp, t.v_amax, t.v_kexp, (const float*)t.m_amax_out, (const float*)t.m_kexp_out,
+                                   (const float*)t.v_amax_out, (const float*)t.v_kexp_out}) {
+                if (!f) return fail(MX_ERR_INVALID_ARG, "FP8 moments need amax and kexp, in and out");
+                if (off4(f)) return fail(MX_ERR_ALIGNMENT, "amax and kexp must be 4-byte aligned");
+            }
+        }
+        if ((s = check_adamw_apart(t, fp8)) != MX_OK) return s;
+    }
+    mx::AdamJob j{};
+    j.tensors = tensors; j.count = count; j.psrc = p_dtype; j.gsrc = g_dtype;
+    j.fmt = state_fmt; j.group = group; j.scale = scale;
+    j.h = {cfg->lr, cfg->beta1, cfg->beta2, cfg->eps, cfg->weight_decay, cfg->step, cfg->lr_dev, cfg->step_dev};
+    return hip_status(mx::launch_adamw(j, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,463 @@
+// adamw.hip -- the optimizer's side of a training step, over many tensors at
+// once: the global norm of the gradients (mx_grad_norm) and the AdamW step
+// (mx_adamw_step) with moments in fp32 or in the FP8 optimizer-state format.
+//
+// [COAT, "解決方案：動態範圍擴充套件"] for the format of the 8-bit moments: a
+// group is decoded, stepped and encoded by the lanes that hold it, so that the
+// moments cross memory in one byte each, and no fp32 copy of them exists.
+//
+// Tensors reach a kernel as a table in its arguments (no device memory to keep
+// alive, and a captured launch keeps its own copy): a launch takes as many
+// tensors as fit the 4 KiB that arguments may have.  A workgroup takes one
+// chunk of one tensor, which it finds by its number among the chunks that the
+// table counts.
+#include <math.h>
+
+#include "../../include/mx.h"
+#include "act_device.h"
+#include "mx_internal.h"
+#include "optstate_device.h"
+
+namespace mx {
+
+namespace {
+
+constexpr int CHUNK = 4096;             // elements of a workgroup's chunk: 256 threads x 16
+constexpr int MOST_CHUNKS = 1 << 23;    // of a launch (a launch counts its threads with 32 bits)
+
+// ---------------------------------------------------------------------------
+// scalars of a step
+// ---------------------------------------------------------------------------
+struct AdamScalars {
+    float b1, c1, b2, c2;               // beta and 1 - beta
+    float eps, decay, rate, root;       // lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+};
+
+// b^t by squaring, in the same order on the host and on the device
+__host__ __device__ inline double int_pow(double b, int64_t t)
+{
+#pragma clang fp contract(off)
+    double r = 1.0;
+    for (; t > 0; t >>= 1) {
+        if (t & 1) r *= b;
+        b *= b;
+    }
+    return r;
+}
+
+__host__ __device__ inline AdamScalars adam_scalars(const AdamHyper& h, double lr, int64_t t)
+{
+#pragma clang fp contract(off)
+    AdamScalars s;
+    s.b1 = (float)h.beta1; s.c1 = (float)(1.0 - h.beta1);
+    s.b2 = (float)h.beta2; s.c2 = (float)(1.0 - h.beta2);
+    s.eps = (float)h.eps;
+    s.decay = (float)(lr * h.weight_decay);
+    s.rate = (float)(lr / (1.0 - int_pow(h.beta1, t)));
+    s.root = (float)(1.0 / sqrt(1.0 - int_pow(h.beta2, t)));
+    return s;
+}
+
+// what a launch needs beside its tensors
+struct AdamCommon {
+    AdamScalars s;
+    AdamHyper h;                        // lr, t on the device: the scalars are formed there
+    const float* scale;
+};
+
+__device__ __forceinline__ AdamScalars scalars_of(const AdamCommon& c)
+{
+    if (!c.h.lr_dev && !c.h.step_dev) return c.s;
+    const double lr = c.h.lr_dev ? (double)*c.h.lr_dev : c.h.lr;
+    const int64_t t = c.h.step_dev ? *c.h.step_dev : c.h.step;
+    return adam_scalars(c.h, lr, t < 1 ? 1 : t);
+}
+
+// One element:
+//   m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,
+//   p' = p - lr wd p - lr/(1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+// each line's sums fused, in this order.
+__device__ __forceinline__ void adam_element(const AdamScalars& s, float g, float& p, float& m, float& v)
+{
+#pragma clang fp contract(off)
+    m = __builtin_fmaf(s.b1, m, s.c1 * g);
+    v = __builtin_fmaf(s.b2, v, s.c2 * g * g);
+    const float d = __builtin_fmaf(__builtin_sqrtf(v), s.root, s.eps);
+    p = __builtin_fmaf(-s.rate, m / d, __builtin_fmaf(-s.decay, p, p));
+}
+
+// ---------------------------------------------------------------------------
+// tables
+// ---------------------------------------------------------------------------
+struct Adam32 {
+    const uint8_t* p; const uint8_t* g; const float* m; const float* v;
+    uint8_t* po; float* mo; float* vo; uint16_t* copy;
+    int64_t n;
+};
+
+struct Adam8 {
+    const uint8_t* p; const uint8_t* g;
+    const uint8_t* m; const float* ma; const float* mk;
+    const uint8_t* v; const float* va; const float* vk;
+    uint8_t* po; uint16_t* copy;
+    uint8_t* mo; float* mao; float* mko;
+    uint8_t* vo; float* vao; float* vko;
+    int64_t n;
+};
+
+template <typename E, int N>
+struct Table {
+    static constexpr int most = N;
+    E t[N];
+    int32_t first[N];                   // number of the tensor's first chunk
+    int32_t count;
+};
+
+typedef Table<Adam32, 48> Table32;
+typedef Table<Adam8, 26> Table8;
+static_assert(sizeof(Table32) + sizeof(AdamCommon) <= 4096 && sizeof(Table8) + sizeof(AdamCommon) <= 4096,
+              "a kernel's arguments are at most 4 KiB");
+
+// the tensor that chunk `c` belongs to
+template <typename T>
+__device__ __forceinline__ int tensor_of(const T& table, int c)
+{
+    int t = 0;
+#pragma unroll
+    for (int step = 32; step > 0; step >>= 1)
+        if (t + step < table.count && table.first[t + step] <= c) t += step;
+    return __builtin_amdgcn_readfirstlane(t);
+}
+
+// four consecutive elements, or those of them before n
+template <int SRC>
+__device__ __forceinline__ void load4(const void* base, int64_t at, int64_t n, float (&v)[4])
+{
+    if (at + 4 <= n) {
+        const Chunk<SRC, 4> c = load_chunk<SRC, 4>(base, at);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = chunk_value<SRC, 4>(c, i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = at + i < n ? load_elem<SRC>(base, at + i) : 0.0f;
+    }
+}
+
+template <int SRC>
+__device__ __forceinline__ void store4(void* base, int64_t at, int64_t n, const float (&v)[4])
+{
+    if (at + 4 <= n) {
+        Chunk<SRC, 4> c;
+        if constexpr (SRC == SRC_F32) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) c.w[i] = __float_as_uint(v[i]);
+        } else {
+            c.w[0] = pack_bf16(v[0], v[1]);
+            c.w[1] = pack_bf16(v[2], v[3]);
+        }
+        __builtin_memcpy((typename ElemT<SRC>::raw*)base + at, &c, sizeof c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (at + i < n) store_elem<SRC>(base, at + i, v[i]);
+    }
+}
+
+__device__ __forceinline__ void load4(int src, const void* base, int64_t at, int64_t n, float (&v)[4])
+{
+    if (src == SRC_F32) load4<SRC_F32>(base, at, n, v);
+    else load4<SRC_BF16>(base, at, n, v);
+}
+
+__device__ __forceinline__ void store4(int src, void* base, int64_t at, int64_t n, const float (&v)[4])
+{
+    if (src == SRC_F32) store4<SRC_F32>(base, at, n, v);
+    else store4<SRC_BF16>(base, at, n, v);
+}
+
+// ---------------------------------------------------------------------------
+// moments in fp32
+// ---------------------------------------------------------------------------
+template <int PS, int GS>
+__global__ __launch_bounds__(256) void k_adamw32(const Table32 table, const AdamCommon c)
+{
+    const int ti = tensor_of(table, (int)blockIdx.x);
+    const Adam32& t = table.t[ti];
+    const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - table.first[ti]) * CHUNK + 4 * threadIdx.x;
+    const float scale = c.scale ? *c.scale : 1.0f;
+    const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
+    const AdamScalars s = scalars_of(c);
+    float p[4][4], g[4][4], m[4][4], v[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int64_t at = base + 1024 * u;
+        load4<PS>(t.p, at, n, p[u]);
+        load4<GS>(t.g, at, n, g[u]);
+        load4<SRC_F32>(t.m, at, n, m[u]);
+        load4<SRC_F32>(t.v, at, n, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int64_t at = base + 1024 * u;
+        if (!skip)
+#pragma unroll
+            for (int i = 0; i < 4; i++) adam_element(s, g[u][i] * scale, p[u][i], m[u][i], v[u][i]);
+        store4<PS>(t.po, at, n, p[u]);
+        store4<SRC_F32>(t.mo, at, n, m[u]);
+        store4<SRC_F32>(t.vo, at, n, v[u]);
+        if (t.copy) store4<SRC_BF16>(t.copy, at, n, p[u]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// moments in FP8.  T = G / 16 neighbouring lanes hold a group; lane j of them
+// the float4s (and code words) j, j + T, j + 2 T, j + 3 T of it.  A group that
+// the tensor's end cuts short is completed with zeros, which change neither
+// its largest nor its smallest nonzero magnitude; their codes are not written.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* q, int64_t at, int64_t n)
+{
+    if (at + 4 <= n) return *(const uint32_t*)(q + at);
+    uint32_t w = 0;
+    for (int i = 0; i < 4; i++)
+        if (at + i < n) w |= (uint32_t)q[at + i] << (8 * i);
+    return w;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* q, int64_t at, int64_t n, uint32_t w)
+{
+    if (at + 4 <= n) {
+        *(uint32_t*)(q + at) = w;
+        return;
+    }
+    for (int i = 0; i < 4; i++)
+        if (at + i < n) q[at + i] = (uint8_t)(w >> (8 * i));
+}
+
+template <int FMT, int G>
+__global__ __launch_bounds__(256) void k_adamw8(const Table8 table, const AdamCommon c, int psrc, int gsrc)
+{
+    constexpr int T = G / 16;
+    __shared__ float lg[128];
+    fill_log_table<FMT>(lg);
+    __syncthreads();
+    const int ti = tensor_of(table, (int)blockIdx.x);
+    const Adam8& t = table.t[ti];
+    const int64_t n = t.n, chunk = (int64_t)((int)blockIdx.x - table.first[ti]) * CHUNK;
+    const int64_t group = chunk / G + threadIdx.x / T;
+    const int j = threadIdx.x % T;
+    const bool live = group * G < n;    // lanes of groups past the end run along with zeros
+    auto at = [&](int i) { return group * G + 4 * (j + i * T); };
+
+    const float scale = c.scale ? *c.scale : 1.0f;
+    const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
+    uint32_t qm[4], qv[4];
+    float p[4][4], g[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        qm[i] = load_codes(t.m, at(i), n);
+        qv[i] = load_codes(t.v, at(i), n);
+        load4(psrc, t.p, at(i), n, p[i]);
+        load4(gsrc, t.g, at(i), n, g[i]);
+    }
+    float ma = 1.0f, mk = 1.0f, va = 1.0f, vk = 1.0f;
+    if (live) ma = t.ma[group], mk = t.mk[group], va = t.va[group], vk = t.vk[group];
+    if (!skip) {
+        const AdamScalars s = scalars_of(c);
+        float m[16], v[16];
+        decode_state<FMT, 16>(qm, lg, ma, mk, m);
+        decode_state<FMT, 16>(qv, lg, va, vk, v);
+#pragma unroll
+        for (int i = 0; i < 16; i++) adam_element(s, g[i / 4][i % 4] * scale, p[i / 4][i % 4], m[i], v[i]);
+        // what lies past the end must not reach the group's extrema
+        if (at(3) + 4 > n)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                if (at(i / 4) + i % 4 >= n) m[i] = v[i] = 0.0f;
+        encode_state<FMT, T, 16>(m, qm, ma, mk);
+        encode_state<FMT, T, 16>(v, qv, va, vk);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        store_codes(t.mo, at(i), n, qm[i]);
+        store_codes(t.vo, at(i), n, qv[i]);
+        store4(psrc, t.po, at(i), n, p[i]);
+        if (t.copy) store4<SRC_BF16>(t.copy, at(i), n, p[i]);
+    }
+    if (live && j == 0) {
+        t.mao[group] = ma; t.mko[group] = mk;
+        t.vao[group] = va; t.vko[group] = vk;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient norm
+// ---------------------------------------------------------------------------
+struct NormEntry { const uint8_t* x; int64_t n; };
+typedef Table<NormEntry, 64> NormTable;
+
+constexpr int NORM_WGS = 1024;          // of a launch, at most: four on each CU
+
+template <int SRC>
+__device__ __forceinline__ double square_sum(const uint8_t* x, int64_t n, int64_t base)
+{
+    double sum = 0.0;
+    float v[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) load4<SRC>(x, base + 1024 * u, n, v[u]);
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) sum = __builtin_fma((double)v[u][i], (double)v[u][i], sum);
+    return sum;
+}
+
+// the sum over a workgroup of 256 threads, in every thread, in a fixed order
+__device__ __forceinline__ double workgroup_sum(double v, double (&red)[4])
+{
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+__device__ __forceinline__ void write_norm(double sum, double max_norm, float* out)
+{
+    const double norm = sqrt(sum);
+    out[0] = (float)norm;
+    out[1] = !(norm < __builtin_inf()) ? __builtin_nanf("") : norm > max_norm ? (float)(max_norm / norm) : 1.0f;
+}
+
+// a partial sum of the table's chunks from each workgroup
+template <int SRC>
+__global__ __launch_bounds__(256) void k_grad_norm(const NormTable table, int chunks, double* partial)
+{
+    __shared__ double red[4];
+    double sum = 0.0;
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int ti = tensor_of(table, c);
+        sum += square_sum<SRC>(table.t[ti].x, table.t[ti].n, (int64_t)(c - table.first[ti]) * CHUNK + 4 * threadIdx.x);
+    }
+    sum = workgroup_sum(sum, red);
+    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+__global__ __launch_bounds__(256) void k_grad_norm_join(const double* partial, int n, float* out, double max_norm)
+{
+    __shared__ double red[4];
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < n; i += 256) sum += partial[i];
+    sum = workgroup_sum(sum, red);
+    if (threadIdx.x == 0) write_norm(sum, max_norm, out);
+}
+
+// ---------------------------------------------------------------------------
+// Walks the tensors of a call, filling tables: put(slot, tensor) fills one
+// slot, flush(table, chunks) launches a full table.  Empty tensors are passed over.
+// ---------------------------------------------------------------------------
+template <typename T, typename Entry, typename Put, typename Flush>
+hipError_t walk(const Entry* tensors, int count, int most_chunks, Put put, Flush flush)
+{
+    T table;
+    int chunks = 0;
+    table.count = 0;
+    for (int i = 0; i < count; i++) {
+        if (tensors[i].n == 0) continue;
+        const int more = (int)((tensors[i].n + CHUNK - 1) / CHUNK);
+        if (table.count > 0 && (table.count == T::most || chunks > most_chunks - more)) {
+            const hipError_t e = flush(table, chunks);
+            if (e != hipSuccess) return e;
+            chunks = table.count = 0;
+        }
+        table.first[table.count] = chunks;
+        put(table.t[table.count++], tensors[i]);
+        chunks += more;
+    }
+    return table.count > 0 ? flush(table, chunks) : hipSuccess;
+}
+
+void put32(Adam32& e, const mx_adamw_tensor& t)
+{
+    e.p = (const uint8_t*)t.p; e.g = (const uint8_t*)t.g; e.m = (const float*)t.m; e.v = (const float*)t.v;
+    e.po = (uint8_t*)t.p_out; e.mo = (float*)t.m_out; e.vo = (float*)t.v_out; e.copy = (uint16_t*)t.copy;
+    e.n = t.n;
+}
+
+void put8(Adam8& e, const mx_adamw_tensor& t)
+{
+    e.p = (const uint8_t*)t.p; e.g = (const uint8_t*)t.g; e.po = (uint8_t*)t.p_out; e.copy = (uint16_t*)t.copy;
+    e.m = (const uint8_t*)t.m; e.ma = t.m_amax; e.mk = t.m_kexp;
+    e.v = (const uint8_t*)t.v; e.va = t.v_amax; e.vk = t.v_kexp;
+    e.mo = (uint8_t*)t.m_out; e.mao = t.m_amax_out; e.mko = t.m_kexp_out;
+    e.vo = (uint8_t*)t.v_out; e.vao = t.v_amax_out; e.vko = t.v_kexp_out;
+    e.n = t.n;
+}
+
+template <int PS, int GS>
+hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
+{
+    return walk<Table32>(j.tensors, j.count, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
+        k_adamw32<PS, GS><<<chunks, 256, 0, s>>>(t, c);
+        return hipGetLastError();
+    });
+}
+
+template <int FMT, int G>
+hipError_t run8(const AdamJob& j, const AdamCommon& c, hipStream_t s)
+{
+    return walk<Table8>(j.tensors, j.count, MOST_CHUNKS, put8, [&](const Table8& t, int chunks) {
+        k_adamw8<FMT, G><<<chunks, 256, 0, s>>>(t, c, j.psrc, j.gsrc);
+        return hipGetLastError();
+    });
+}
+
+template <int FMT>
+hipError_t run8(const AdamJob& j, const AdamCommon& c, hipStream_t s)
+{
+    switch (j.group) {
+    case 32: return run8<FMT, 32>(j, c, s);
+    case 64: return run8<FMT, 64>(j, c, s);
+    case 128: return run8<FMT, 128>(j, c, s);
+    default: return run8<FMT, 256>(j, c, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamJob& j, hipStream_t s)
+{
+    AdamCommon c;
+    c.h = j.h;
+    c.scale = j.scale;
+    c.s = adam_scalars(j.h, j.h.lr, j.h.step < 1 ? 1 : j.h.step);
+    if (j.fmt == E4M3) return run8<E4M3>(j, c, s);
+    if (j.fmt == E5M2) return run8<E5M2>(j, c, s);
+    if (j.psrc == SRC_F32) return j.gsrc == SRC_F32 ? run32<SRC_F32, SRC_F32>(j, c, s) : run32<SRC_F32, SRC_BF16>(j, c, s);
+    return j.gsrc == SRC_F32 ? run32<SRC_BF16, SRC_F32>(j, c, s) : run32<SRC_BF16, SRC_BF16>(j, c, s);
+}
+
+int64_t grad_norm_work_bytes(int count)
+{
+    return ((int64_t)(count < 1 ? 1 : count) + NormTable::most - 1) / NormTable::most * NORM_WGS * (int64_t)sizeof(double);
+}
+
+hipError_t launch_grad_norm(const GradNormJob& j, hipStream_t s)
+{
+    int partials = 0;
+    const hipError_t e = walk<NormTable>(
+        j.tensors, j.count, 1 << 30,
+        [](NormEntry& e, const mx_tensor& t) { e.x = (const uint8_t*)t.x; e.n = t.n; },
+        [&](const NormTable& t, int chunks) {
+            const int wgs = chunks < NORM_WGS ? chunks : NORM_WGS;
+            if (j.src == SRC_F32) k_grad_norm<SRC_F32><<<wgs, 256, 0, s>>>(t, chunks, j.work + partials);
+            else k_grad_norm<SRC_BF16><<<wgs, 256, 0, s>>>(t, chunks, j.work + partials);
+            partials += wgs;
+            return hipGetLastError();
+        });
+    if (e != hipSuccess) return e;
+    k_grad_norm_join<<<1, 256, 0, s>>>(j.work, partials, j.out, j.max_norm);
+    return hipGetLastError();
+}
+
+}  // namespace mx

@@ -5,6 +5,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+struct mx_tensor;
+struct mx_adamw_tensor;
+
 namespace mx {
 
 struct QuantJob {
@@ -46,6 +49,33 @@ struct OptStateJob {
 };
 
 hipError_t launch_optstate(const OptStateJob& j, hipStream_t stream);
+
+// AdamW over many tensors.  lr and step from the host, or, where the pointers
+// are given, from the device when the kernel runs
+struct AdamHyper {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    const float* lr_dev; const int64_t* step_dev;
+};
+
+struct AdamJob {
+    const mx_adamw_tensor* tensors; int count;
+    int psrc, gsrc;         // SRC_F32 / SRC_BF16: parameters, gradients
+    int fmt, group;         // E4M3 / E5M2 moments in groups; -1: fp32
+    AdamHyper h;
+    const float* scale;     // factor of the gradients (nullptr: 1); not finite: nothing changes
+};
+
+hipError_t launch_adamw(const AdamJob& j, hipStream_t stream);
+
+struct GradNormJob {
+    const mx_tensor* tensors; int count; int src;
+    double max_norm;
+    double* work; float* out;
+};
+
+int64_t grad_norm_work_bytes(int count);
+hipError_t launch_grad_norm(const GradNormJob& j, hipStream_t stream);
 
 // nvfp routes: NVFP4 copies (E2M1, E4M3 scale per 16, FP32 second-level
 // scale over the tensor or per 32 stored rows)

@@ -34,7 +34,9 @@ EXPORTED = ("mx_quantize", "mx_quantize_dual_layout", "mx_gemm", "mx_dequantize"
             "mx_predict_tensor_scale_noalloc", "mx_quantize_optstate", "mx_dequantize_optstate",
             "mx_quantize_nvfp", "mx_dequantize_nvfp", "mx_gemm_nvfp",
             "mx_norm_forward", "mx_norm_backward", "mx_norm_backward_workspace_bytes",
-            "mx_glu_forward", "mx_glu_backward", "mx_glu_backward_dual_layout")
+            "mx_glu_forward", "mx_glu_backward", "mx_glu_backward_dual_layout",
+            "mx_grad_norm", "mx_grad_norm_workspace_bytes", "mx_adamw_step")
+MX_STATE_F32 = -1
 NV_PANEL = 32                      # stored rows per CTA-local nvfp scale domain
 
 
@@ -50,6 +52,21 @@ class mx_qconfig(ctypes.Structure):
                 ("rounding", ctypes.c_int32), ("hadamard", ctypes.c_int32),
                 ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32)]
+
+
+class mx_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class mx_adamw_tensor(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in (
+        "p", "g", "m", "v", "m_amax", "m_kexp", "v_amax", "v_kexp", "p_out", "m_out", "v_out", "m_amax_out",
+        "m_kexp_out", "v_amax_out", "v_kexp_out", "copy")] + [("n", ctypes.c_int64)]
+
+
+class mx_adamw_config(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p)]
 
 
 _lib = None
@@ -113,6 +130,12 @@ def load() -> ctypes.CDLL:
     L.mx_glu_backward_dual_layout.restype = _i32
     L.mx_glu_backward_dual_layout.argtypes = [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp,
                                               _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+    L.mx_grad_norm.restype = _i32
+    L.mx_grad_norm.argtypes = [_vp, _i32, _i32, ctypes.c_double, _vp, _i64, _vp, _vp]
+    L.mx_grad_norm_workspace_bytes.restype = _i64
+    L.mx_grad_norm_workspace_bytes.argtypes = [_i32]
+    L.mx_adamw_step.restype = _i32
+    L.mx_adamw_step.argtypes = [_vp, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(mx_adamw_config), _vp, _vp]
     L.mx_predict_workspace_bytes.restype = _i64
     L.mx_predict_workspace_bytes.argtypes = []
     L.mx_status_string.restype = ctypes.c_char_p
@@ -766,3 +789,184 @@ def mx_glu_backward_dual_layout(dh: torch.Tensor, gate: Optional[torch.Tensor] =
     hf, qh_col, sh_col, pqh, psh = _copy_out(h_fmt, qh_col, sh_col, (cols, rows), dh, at, _H)
     _check(load().mx_glu_backward_dual_layout(*head, f, pqr, psr, pqc, psc, hf, pqh, psh, _stream_on(stream, at)))
     return GluBackwardDual(q_row, s_row, q_col, s_col, qh_col, sh_col)
+
+
+# ---------------------------------------------------------------------------
+# the optimizer's side of a step, over many tensors at once
+# ---------------------------------------------------------------------------
+class TensorList:
+    """The addresses of tensors of one type and device, as mx_grad_norm takes
+    them; keeps the tensors."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        self.src, self.at = MX_SRC_F32, -1
+        if self.tensors:
+            self.src, self.at = _src_code(self.tensors[0], "tensor 0"), self.tensors[0].get_device()
+        for i, t in enumerate(self.tensors):
+            _dense(t, t.shape, self.tensors[0].dtype, self.at, f"tensor {i}")
+        self.array = (mx_tensor * max(1, len(self.tensors)))(*((t.data_ptr(), t.numel()) for t in self.tensors))
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def tensor_list(tensors) -> TensorList:
+    """A TensorList; a program whose gradients stay where they are keeps it."""
+    return TensorList(tensors)
+
+
+def _src_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype is torch.bfloat16:
+        return MX_SRC_BF16
+    if t.dtype is torch.float32:
+        return MX_SRC_F32
+    raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def mx_grad_norm(grads, max_norm: float = float("inf"), out: Optional[torch.Tensor] = None, work=None,
+                 stream=None) -> torch.Tensor:
+    """float32 [norm, scale]: the global norm of the gradients (a TensorList or
+    tensors) and the factor that clips it at max_norm, NaN where a gradient is
+    not finite.  out[1:] is what mx_adamw_step takes as scale."""
+    if (out is None or work is None) and _other(stream):
+        return _run_on(stream, mx_grad_norm, locals())
+    if not isinstance(grads, TensorList):
+        grads = TensorList(grads)
+    L, n = load(), len(grads)
+    at = grads.at
+    if n == 0:
+        at = _device() if out is None else out.get_device()
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=f"cuda:{at}") if n == 0 or at < 0 else \
+            grads.tensors[0].new_empty_strided((2,), (1,), dtype=torch.float32)
+    if work is None:
+        nbytes = L.mx_grad_norm_workspace_bytes(n)
+        work = out.new_empty_strided((nbytes,), (1,), dtype=torch.uint8)
+    elif work.get_device() != at or not work.is_contiguous():
+        raise ValueError("work must be contiguous and on the device of the gradients")
+    else:
+        nbytes = work.numel() * work.element_size()
+    _check(L.mx_grad_norm(grads.array, n, grads.src, max_norm, work.data_ptr(), nbytes,
+                          _dense(out, (2,), torch.float32, at, "out"), _stream_on(stream, at)))
+    return out
+
+
+class AdamWPlan:
+    """The addresses of parameters, gradients and moments, as mx_adamw_step
+    takes them; keeps the tensors.  grads is their TensorList."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, fmt, group, copies, out):
+        params, ms, vs = list(params), list(exp_avg), list(exp_avg_sq)
+        n = len(params)
+        self.grads = TensorList(grads)
+        if out is None:
+            out = params, ms, vs
+        outs = [list(x) for x in out]
+        copies = [None] * n if copies is None else list(copies)
+        if any(len(x) != n for x in (self.grads, ms, vs, *outs, copies)):
+            raise ValueError("params, grads, exp_avg, exp_avg_sq, copies and out must have one length")
+        self.fmt, self.group, self.count = MX_STATE_F32 if fmt is None else _fmt(fmt), int(group), n
+        if self.fmt != MX_STATE_F32 and self.group not in (32, 64, 128, 256):
+            raise ValueError("group must be 32, 64, 128 or 256")
+        self.src, self.at = (_src_code(params[0], "parameter 0"), params[0].get_device()) if n else (MX_SRC_F32, -1)
+        self.kept = params, ms, vs, outs, copies
+        self.array = (mx_adamw_tensor * max(1, n))()
+        spans = []
+        for i in range(n):
+            self._one(self.array[i], i, params[i], self.grads.tensors[i], ms[i], vs[i], [x[i] for x in outs],
+                      copies[i], params[0].dtype, spans)
+        _check_apart(spans)
+
+    def _one(self, a, i, p, g, m, v, outs, copy, dtype, spans):
+        a.n = n = p.numel()
+
+        def put(field, t, kind, length=n, name=None):
+            name = f"{name or field} {i}"
+            if t.numel() != length:
+                raise ValueError(f"{name} must have {length} elements")
+            _dense(t, t.shape, kind, self.at, name)
+            setattr(a, field, t.data_ptr())
+            if length:
+                start = t.data_ptr()
+                spans.append((start, start + length * t.element_size(), field.endswith("_out") or field == "copy",
+                              (i, field[:-4] if field.endswith("_out") else field)))
+
+        put("p", p, dtype, name="parameter")
+        put("g", g, self.grads.tensors[0].dtype, name="gradient")
+        put("p_out", outs[0], dtype, name="the new parameter")
+        if copy is not None:
+            put("copy", copy, torch.bfloat16)
+        groups = -(-n // self.group) if self.fmt != MX_STATE_F32 else 0
+        for field, state in (("m", m), ("v", v), ("m_out", outs[1]), ("v_out", outs[2])):
+            if self.fmt == MX_STATE_F32:
+                put(field, state, torch.float32)
+                continue
+            base, end = field[0], field[1:]
+            q, amax, kexp = state
+            put(field, q, torch.uint8)
+            put(f"{base}_amax{end}", amax, torch.float32, groups)
+            put(f"{base}_kexp{end}", kexp, torch.float32, groups)
+
+
+def _check_apart(spans):
+    """No output over another tensor than the input that it updates in place."""
+    inputs = {(s[3], s[0], s[1]) for s in spans if not s[2]}
+    places = {(s[3], s[0], s[1]) for s in spans if s[2]} & inputs
+    end = write_end = 0                          # where the spans so far end, and those that are written
+    for start, stop, out, key in sorted(spans):
+        if not out and (key, start, stop) in places:
+            continue                             # counted as the output
+        if start < write_end or (out and start < end):
+            raise ValueError(f"{key[1]} {key[0]} overlaps a tensor that the step writes, or the step would write it twice")
+        end = max(end, stop)
+        if out:
+            write_end = max(write_end, stop)
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, fmt=None, group: int = 128, copies=None, out=None) -> AdamWPlan:
+    """The plan of mx_adamw_step over these tensors.  Moments are float32
+    tensors, or (fmt) triples (q, amax, kexp) as mx_quantize_optstate returns
+    them, with ceil(n / group) groups.  copies: bfloat16 tensors that take the
+    new parameters, or None for some or all.  out: (params, exp_avg,
+    exp_avg_sq) to write instead of updating in place."""
+    return AdamWPlan(params, grads, exp_avg, exp_avg_sq, fmt, group, copies, out)
+
+
+def adamw_state(p: torch.Tensor, fmt=None, group: int = 128):
+    """A zero moment of p: a float32 tensor, or (fmt) codes, amax and kexp."""
+    if fmt is None:
+        return torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
+    _fmt(fmt)
+    groups = -(-p.numel() // group)
+    return (torch.zeros(p.numel(), dtype=torch.uint8, device=p.device),
+            torch.ones(groups, dtype=torch.float32, device=p.device),
+            torch.ones(groups, dtype=torch.float32, device=p.device))
+
+
+def mx_adamw_step(plan: AdamWPlan, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                  scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step over a plan's tensors.  step: 1 at the first step.  lr
+    and step may be device tensors of one element (float32, int64), which the
+    step reads when it runs.  scale: float32 of one element, a factor of the
+    gradients; if it is not finite the step is skipped."""
+    at, cfg = plan.at, mx_adamw_config(0.0, betas[0], betas[1], eps, weight_decay, 1, None, None)
+    if isinstance(lr, torch.Tensor):
+        cfg.lr_dev = _one_element(lr, torch.float32, at, "lr")
+    else:
+        cfg.lr = lr
+    if isinstance(step, torch.Tensor):
+        cfg.step_dev = _one_element(step, torch.int64, at, "step")
+    else:
+        cfg.step = step
+    pscale = None if scale is None else _one_element(scale, torch.float32, at, "scale")
+    if plan.count == 0:
+        at = _device()
+    _check(load().mx_adamw_step(plan.array, plan.count, plan.src, plan.grads.src, plan.fmt, plan.group,
+                                ctypes.byref(cfg), pscale, _stream_on(stream, at)))
+
+
+def _one_element(t: torch.Tensor, dtype, at: int, name: str) -> int:
+    if t.numel() != 1:
+        raise ValueError(f"{name} must have one element")
+    return _dense(t, t.shape, dtype, at, name)

@@ -519,6 +519,111 @@ mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src
                                       void* q_col, uint8_t* s_col, int32_t h_fmt, void* qh, uint8_t* sh,
                                       void* stream);
 
+/*
+ * The optimizer's side of a training step, over many tensors at once.  The
+ * tensors of a call are `count` entries of a HOST array, which is read during
+ * the call only (a captured launch keeps its own copy of the addresses).  A
+ * tensor is n consecutive elements, aligned to their size; n may be any number
+ * up to 2^35, and 0 (its pointers are then not looked at), and count may be 0.
+ * No output may overlap another tensor's, or an input that it is not allowed
+ * to be below: the call cannot tell.
+ */
+
+/* one input tensor */
+typedef struct mx_tensor {
+    const void* x;
+    int64_t n;
+} mx_tensor;
+
+/*
+ * mx_grad_norm -- the global norm of the gradients, and the factor that clips it:
+ *   norm = sqrt(sum over all tensors and elements of x^2),
+ *   out[0] = norm,  out[1] = norm > max_norm ? max_norm / norm : 1,
+ * or out[1] = NaN if a gradient is not finite.  out + 1 is what mx_adamw_step
+ * takes as `scale`.  The sum is held in 64 bits and taken in an order that the
+ * sizes fix, with no atomics: the result repeats bit for bit, and no finite
+ * gradient's square overflows or vanishes.
+ *
+ * tensors:  all of `src_dtype`.
+ * max_norm: > 0; Inf does not clip.
+ * work:  at least mx_grad_norm_workspace_bytes(count) bytes, 8-byte aligned;
+ *        contents undefined afterwards.
+ * out:   two fp32 in device memory, 4-byte aligned.
+ * Errors: MX_ERR_INVALID_ARG, MX_ERR_ALIGNMENT, MX_ERR_HIP.
+ */
+mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, int32_t src_dtype, double max_norm, void* work,
+                       int64_t work_bytes, float* out, void* stream);
+
+/* Bytes of workspace mx_grad_norm needs for `count` tensors (0 for a count it refuses). */
+int64_t mx_grad_norm_workspace_bytes(int32_t count);
+
+/*
+ * One parameter with its gradient and moments.  m, v: n fp32; or FP8 codes in
+ * the format of mx_quantize_optstate (n bytes, 4-byte aligned) with their
+ * groups' amax and kexp, ceil(n / group) fp32 each: groups of consecutive
+ * elements, the last one shorter where group does not divide n.  Zero moments
+ * are zero codes with amax = kexp = 1.  The outputs p_out, m_out, ... may be the
+ * inputs of the same name (an update in place) or other memory; copy, if not
+ * NULL, takes p_out rounded to bf16.
+ */
+typedef struct mx_adamw_tensor {
+    const void* p;
+    const void* g;
+    const void* m;
+    const void* v;
+    const float* m_amax;      /* fp32 moments: the amax and kexp pointers are not looked at */
+    const float* m_kexp;
+    const float* v_amax;
+    const float* v_kexp;
+    void* p_out;
+    void* m_out;
+    void* v_out;
+    float* m_amax_out;
+    float* m_kexp_out;
+    float* v_amax_out;
+    float* v_kexp_out;
+    void* copy;
+    int64_t n;
+} mx_adamw_tensor;
+
+/* format of the moments beside MX_E4M3 and MX_E5M2 */
+enum { MX_STATE_F32 = -1 };
+
+typedef struct mx_adamw_config {
+    double lr;                /* >= 0 */
+    double beta1, beta2;      /* in [0, 1) */
+    double eps;               /* >= 0 */
+    double weight_decay;      /* >= 0 */
+    int64_t step;             /* t >= 1: 1 at the first step */
+    const float* lr_dev;      /* not NULL: lr is read from the device when the step runs */
+    const int64_t* step_dev;  /* not NULL: t is read from the device when the step runs */
+} mx_adamw_config;
+
+/*
+ * mx_adamw_step -- one AdamW step over many tensors.  Per element, with g' = g
+ * * scale and t the step's number:
+ *   m' = beta1 m + (1 - beta1) g',      v' = beta2 v + (1 - beta2) g'^2,
+ *   p' = p - lr wd p - lr (m' / (1 - beta1^t)) / (sqrt(v' / (1 - beta2^t)) + eps)
+ * in fp32, p' from m' and v' before they are rounded to what is kept.  The
+ * factors of lr and t are formed in 64 bits and rounded to fp32.  Moments in
+ * FP8 ([COAT, "解決方案：動態範圍擴充套件"]) are decoded as
+ * mx_dequantize_optstate does and encoded as mx_quantize_optstate does, bit for
+ * bit, the elements of a short last group alone making up its amax and kexp.
+ *
+ * tensors: parameters of `p_dtype`, gradients of `g_dtype` (MX_SRC_F32 /
+ *        MX_SRC_BF16), moments in `state_fmt` (MX_STATE_F32, MX_E4M3, MX_E5M2;
+ *        MX_E2M1: MX_ERR_UNSUPPORTED), with FP8 in groups of `group` (32, 64,
+ *        128 or 256).
+ * scale: one fp32 in device memory, or NULL (1).  If it is not finite the step
+ *        is skipped: outputs are the inputs as they are, copy is p as it is.
+ * lr_dev, step_dev, scale: read when the step runs, so a captured step follows
+ *        them.  t < 1 from step_dev counts as 1.
+ * Errors: MX_ERR_INVALID_ARG, MX_ERR_UNSUPPORTED, MX_ERR_ALIGNMENT, MX_ERR_HIP.
+ */
+mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int32_t count, int32_t p_dtype, int32_t g_dtype,
+                        int32_t state_fmt, int32_t group, const mx_adamw_config* cfg, const float* scale,
+                        void* stream);
+
 /* Static text for a status code. */
 const char* mx_status_string(mx_status status);
 

@@ -1,0 +1,131 @@
+"""mx_grad_norm against the sum in 64 bits: sizes around a chunk, many tensors,
+odd addresses, values whose squares leave fp32's range, non-finite gradients,
+streams and captured graphs."""
+import math
+
+import pytest
+import torch
+
+from fp4_quantization_block_amd import mx
+from gpu_util import DEV, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+# the sum in 64 bits is off by n 2^-53 at most, the root halves that: below 2^-30 for these; then one rounding to fp32
+TOL = 2.0 ** -24 * 1.01
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _reference(grads):
+    return math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+
+
+def _check(out, grads, max_norm):
+    norm, scale = (float(v) for v in out.cpu())
+    ref = _reference(grads)
+    assert abs(norm - ref) <= TOL * ref
+    want = max_norm / ref if ref > max_norm else 1.0
+    assert abs(scale - want) <= TOL * want
+
+
+def _make(sizes, dtype, seed=0, size=1e-3):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return [(torch.randn(n, generator=g, device=DEV) * size).to(dtype) for n in sizes]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [
+    [1], [2, 1, 3], [4095], [4096], [4097], [8191, 0, 1], [4096 * 1024 + 1], [4096 * 2500 + 17, 5],
+    [7] * 64, [9] * 65, [1 + 37 * i for i in range(200)],
+])
+@pytest.mark.parametrize("max_norm", [1e-4, 1e6])
+def test_norm(sizes, dtype, max_norm):
+    grads = _make(sizes, dtype, seed=len(sizes))
+    _check(mx.mx_grad_norm(grads, max_norm=max_norm), grads, max_norm)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_odd_addresses(dtype):
+    flat = _make([100000], dtype)[0]
+    grads = [flat[1:5000], flat[5003:5004], flat[7001:70000]]
+    _check(mx.mx_grad_norm(grads, max_norm=1e-4), grads, 1e-4)
+
+
+@pytest.mark.parametrize("size", [1e30, 1e-30, 1e-38])
+def test_range(size):
+    """Squares beyond fp32's range on either side."""
+    grads = _make([5000, 33], torch.float32, size=size)
+    _check(mx.mx_grad_norm(grads, max_norm=size), grads, size)
+
+
+def test_norm_beyond_fp32_still_clips():
+    grads = [torch.full((5000,), 3e38, device=DEV)]
+    norm, scale = mx.mx_grad_norm(grads, max_norm=1.0).tolist()
+    want = 1.0 / (math.sqrt(5000) * float(grads[0][0]))
+    assert norm == math.inf
+    assert abs(scale - want) <= 2.0 ** -149                      # a subnormal: half its step, and some
+
+
+def test_nothing_to_add():
+    zero = torch.zeros(10, device=DEV)
+    for grads in ([], [zero[:0]], [zero], [zero[:0], zero]):
+        assert mx.mx_grad_norm(grads, max_norm=1.0).tolist() == [0.0, 1.0]
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_non_finite(bad):
+    grads = _make([5000, 4097], torch.float32)
+    grads[1][4096] = bad
+    norm, scale = mx.mx_grad_norm(grads, max_norm=1.0).tolist()
+    assert math.isnan(scale)
+    assert math.isnan(norm) if math.isnan(bad) else norm == math.inf
+
+
+def test_repeats_bit_for_bit():
+    grads = _make([4096 * 3000 + 5, 70001], torch.float32)
+    first = mx.mx_grad_norm(grads)
+    assert all(torch.equal(first, mx.mx_grad_norm(grads)) for _ in range(5))
+
+
+def test_no_clip_by_default():
+    grads = _make([5000], torch.float32, size=1e3)
+    assert float(mx.mx_grad_norm(grads)[1]) == 1.0
+
+
+def test_more_than_2_to_31_elements():
+    x = torch.zeros(2 ** 31 + 4099, dtype=torch.bfloat16, device=DEV)
+    x[-3:] = 2.0
+    x[0] = 1.0
+    assert float(mx.mx_grad_norm([x])[0]) == float(torch.tensor(math.sqrt(13.0), dtype=torch.float32))
+
+
+def test_graph_on_a_side_stream():
+    """Captured on another stream than the default one and replayed over new values."""
+    grads = _make([5000, 4096 * 40 + 3], torch.bfloat16)
+    out, side = torch.empty(2, device=DEV), torch.cuda.Stream()
+    lists = mx.tensor_list(grads)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        mx.mx_grad_norm(lists, max_norm=1e-3, out=out)
+    for k in range(4):
+        for g, new in zip(grads, _make([5000, 4096 * 40 + 3], torch.bfloat16, seed=k)):
+            g.copy_(new)
+        out.zero_()
+        eager = mx.mx_grad_norm(grads, max_norm=1e-3)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+
+
+def test_stream_argument():
+    grads, side = _make([4096 * 500], torch.float32), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = mx.mx_grad_norm(grads, max_norm=1e-3, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    _check(out, grads, 1e-3)

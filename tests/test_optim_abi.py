@@ -1,0 +1,180 @@
+"""Argument checks of the optimizer operators, on the CPU: the C entry points
+refuse before any HIP call (the pointers here are never dereferenced), and the
+binding refuses tensors of the wrong type, shape, layout or place."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from fp4_quantization_block_amd import mx
+
+INV, UNS, ALI = mx.MX_ERR_INVALID_ARG, mx.MX_ERR_UNSUPPORTED, mx.MX_ERR_ALIGNMENT
+P = 0x10000
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(mx.LIB_PATH):
+        pytest.skip("libmx.so not built")
+    return mx.load()
+
+
+def _norm(lib, x=P, n=64, count=1, src=0, max_norm=1.0, work=P * 2, nbytes=1 << 20, out=P * 3, array=True):
+    a = (mx.mx_tensor * 2)((P * 5, 64), (x, n))
+    return lib.mx_grad_norm(ctypes.byref(a, ctypes.sizeof(mx.mx_tensor)) if array else None, count, src, max_norm,
+                            work, nbytes, out, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(count=-1), INV), (dict(array=False), INV), (dict(src=2), INV), (dict(max_norm=0.0), INV),
+    (dict(max_norm=-1.0), INV), (dict(max_norm=NAN), INV), (dict(work=None), INV), (dict(out=None), INV),
+    (dict(nbytes=8191), INV), (dict(work=P + 4), ALI), (dict(out=P + 2), ALI), (dict(n=-1), INV),
+    (dict(n=(1 << 35) + 1), INV), (dict(x=None), INV), (dict(x=P + 2), ALI), (dict(x=P + 1, src=1), ALI),
+    (dict(x=P * 2), INV), (dict(x=P * 3), INV),
+])
+def test_grad_norm_refuses(lib, kw, status):
+    assert _norm(lib, **kw) == status
+    assert lib.mx_last_error_message().decode() != ""
+
+
+def test_grad_norm_workspace_grows_with_the_tensors(lib):
+    size = lib.mx_grad_norm_workspace_bytes
+    assert size(-1) == 0 and size(0) == size(1) == size(64) > 0
+    assert size(65) == 2 * size(64) and size(1000) == 16 * size(64)
+
+
+_IN = dict(p=1, g=2, m=3, v=4, m_amax=5, m_kexp=6, v_amax=7, v_kexp=8)
+_OUT = dict(p_out=9, m_out=10, v_out=11, m_amax_out=12, m_kexp_out=13, v_amax_out=14, v_kexp_out=15, copy=16)
+
+
+def _step(lib, count=1, pd=0, gd=0, fmt=mx.MX_E4M3, group=128, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8,
+          weight_decay=0.1, step=1, lr_dev=None, step_dev=None, scale=None, n=100, array=True, cfg=True, **at):
+    t = mx.mx_adamw_tensor(**{k: P * v for k, v in {**_IN, **_OUT}.items()}, n=n)
+    for k, v in at.items():
+        setattr(t, k, v)
+    c = mx.mx_adamw_config(lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev)
+    return lib.mx_adamw_step(ctypes.byref(t) if array else None, count, pd, gd, fmt, group,
+                             ctypes.byref(c) if cfg else None, scale, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(count=-1), INV), (dict(array=False), INV), (dict(pd=2), INV), (dict(gd=-1), INV),
+    (dict(fmt=mx.MX_E2M1), UNS), (dict(fmt=3), INV), (dict(fmt=-2), INV), (dict(group=0), INV),
+    (dict(group=48), INV), (dict(group=512), INV), (dict(cfg=False), INV), (dict(lr=-1e-3), INV), (dict(lr=NAN), INV),
+    (dict(lr=INF), INV), (dict(eps=-1.0), INV), (dict(eps=NAN), INV), (dict(weight_decay=-0.1), INV),
+    (dict(weight_decay=INF), INV), (dict(beta1=1.0), INV), (dict(beta1=-0.1), INV), (dict(beta2=1.0), INV),
+    (dict(beta2=NAN), INV), (dict(step=0), INV), (dict(step=-3), INV), (dict(lr_dev=P + 2), ALI),
+    (dict(step_dev=P + 4), ALI), (dict(scale=P + 1), ALI), (dict(n=-1), INV), (dict(n=(1 << 35) + 1), INV),
+    *[({k: None}, INV) for k in [*_IN, *_OUT] if k != "copy"],
+    *[({k: P * v + 2}, ALI) for k, v in {**_IN, **_OUT}.items() if k != "copy"],
+    (dict(copy=P + 1), ALI), (dict(pd=1, p=P + 1), ALI), (dict(gd=1, g=P + 1), ALI),
+    # an output over another input than its own, or two at one address
+    (dict(p_out=P * 2), INV), (dict(m_out=P * 4), INV), (dict(v_out=P * 3), INV), (dict(copy=P), INV),
+    (dict(copy=P * 2), INV), (dict(m_out=P * 11), INV), (dict(copy=P * 9), INV), (dict(m_amax_out=P * 6), INV),
+    (dict(v_kexp_out=P * 14), INV), (dict(m_amax_out=P * 3), INV),
+])
+def test_adamw_refuses(lib, kw, status):
+    assert _step(lib, **kw) == status
+    assert lib.mx_last_error_message().decode() != ""
+
+
+@pytest.mark.parametrize("kw,status", [(dict(m=None), INV), (dict(v_out=P * 11 + 2), ALI), (dict(p_out=P * 4), INV)])
+def test_adamw_refuses_with_fp32_moments(lib, kw, status):
+    at = {k: None for k in {**_IN, **_OUT} if "amax" in k or "kexp" in k}
+    assert _step(lib, fmt=mx.MX_STATE_F32, **{**at, **kw}) == status
+
+
+# --- the binding -----------------------------------------------------------------------------------------------
+def _tensors(n=100, group=0):
+    p = [torch.zeros(n), torch.zeros(n + 1)]
+    g = [torch.zeros_like(t) for t in p]
+    fmt = "e4m3" if group else None
+    return p, g, [mx.adamw_state(t, fmt, group or 128) for t in p], [mx.adamw_state(t, fmt, group or 128) for t in p]
+
+
+def test_plan_accepts():
+    p, g, m, v = _tensors()
+    plan = mx.adamw_plan(p, g, m, v)
+    assert plan.count == 2 and plan.array[1].n == 101 and plan.array[0].p_out == p[0].data_ptr()
+    p, g, m, v = _tensors(group=64)
+    plan = mx.adamw_plan(p, g, m, v, fmt="e4m3", group=64, copies=[None, torch.zeros(101, dtype=torch.bfloat16)])
+    assert plan.array[0].copy is None and plan.array[1].m_amax == m[1][1].data_ptr()
+    assert m[1][1].numel() == 2
+    assert mx.adamw_plan([], [], [], []).count == 0
+    flat = torch.zeros(201)                       # views of one buffer that touch, and an empty tensor
+    views = [flat[:100], flat[100:100], flat[100:]]
+    mx.adamw_plan(views, [torch.zeros_like(t) for t in views], *[[torch.zeros_like(t) for t in views] for _ in "mv"])
+    same = torch.zeros(100)                       # one gradient of two parameters is only read
+    p, g, m, v = _tensors()
+    mx.adamw_plan([p[0], torch.zeros(100)], [same, same], [m[0], torch.zeros(100)], [v[0], torch.zeros(100)])
+
+
+def _bad(change):
+    p, g, m, v = _tensors()
+    kw = dict(params=p, grads=g, exp_avg=m, exp_avg_sq=v)
+    change(kw)
+    return kw
+
+
+@pytest.mark.parametrize("change,error", [
+    (lambda k: k["grads"].pop(), ValueError), (lambda k: k["params"].pop(), ValueError),
+    (lambda k: k.update(copies=[None]), ValueError), (lambda k: k.update(fmt="e4m3", group=100), ValueError),
+    (lambda k: k["params"].__setitem__(1, torch.zeros(101, dtype=torch.bfloat16)), TypeError),
+    (lambda k: k["params"].__setitem__(0, torch.zeros(100, dtype=torch.float16)), TypeError),
+    (lambda k: k["grads"].__setitem__(0, torch.zeros(99)), ValueError),
+    (lambda k: k["grads"].__setitem__(0, torch.zeros(100, dtype=torch.bfloat16)), TypeError),
+    (lambda k: k["exp_avg"].__setitem__(0, torch.zeros(100, dtype=torch.bfloat16)), TypeError),
+    (lambda k: k["params"].__setitem__(0, torch.zeros(200)[::2]), ValueError),
+    (lambda k: k["exp_avg_sq"].__setitem__(1, torch.zeros(100)), ValueError),
+    (lambda k: k.update(copies=[torch.zeros(100), None]), TypeError),
+    # the same tensor twice, a moment that is the other, an output over a gradient, two that overlap in part
+    (lambda k: k["params"].__setitem__(1, k["params"][0]), ValueError),
+    (lambda k: k["exp_avg"].__setitem__(0, k["exp_avg_sq"][0]), ValueError),
+    (lambda k: k["grads"].__setitem__(0, k["params"][0]), ValueError),
+])
+def test_plan_refuses(change, error):
+    with pytest.raises(error):
+        mx.adamw_plan(**_bad(change))
+
+
+def test_plan_refuses_partial_overlap():
+    p, g, m, v = _tensors()
+    flat = torch.zeros(200)
+    with pytest.raises(ValueError):
+        mx.adamw_plan([flat[:100], flat[99:200]], g, m, v)
+    with pytest.raises(ValueError):               # out of place, one element over its own input
+        mx.adamw_plan([flat[:100], p[1]], g, m, v, out=([flat[99:199], torch.zeros(101)], m, v))
+    with pytest.raises(ValueError):               # a gradient inside another tensor's output
+        mx.adamw_plan(p, [flat[50:150], g[1]], m, v, out=([flat[:100], torch.zeros(101)], m, v))
+
+
+def test_fp8_plan_refuses():
+    p, g, m, v = _tensors(group=64)
+    q, amax, k = m[0]
+    for bad, error in ((q[:99], ValueError), (q.float(), TypeError)):
+        with pytest.raises(error):
+            mx.adamw_plan(p, g, [(bad, amax, k), m[1]], v, fmt="e4m3", group=64)
+    with pytest.raises(ValueError):
+        mx.adamw_plan(p, g, [(q, amax[:1], k), m[1]], v, fmt="e4m3", group=64)
+    with pytest.raises(ValueError):               # one k for both moments
+        mx.adamw_plan(p, g, [(q, amax, v[0][2]), m[1]], v, fmt="e4m3", group=64)
+
+
+def test_calls_refuse_cpu_tensors_and_wrong_scalars():
+    plan = mx.adamw_plan(*_tensors())
+    with pytest.raises(ValueError):
+        mx.mx_adamw_step(plan, 1e-3, 1)
+    with pytest.raises(ValueError):
+        mx.mx_adamw_step(plan, 1e-3, 1, scale=torch.zeros(2))
+    with pytest.raises(TypeError):
+        mx.mx_adamw_step(plan, 1e-3, torch.ones(1))
+    with pytest.raises(TypeError):
+        mx.mx_adamw_step(plan, torch.ones(1, dtype=torch.float64), 1)
+    with pytest.raises(ValueError):
+        mx.mx_grad_norm(plan.grads, out=torch.zeros(2), work=torch.zeros(8192, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        mx.tensor_list([torch.zeros(3, dtype=torch.float16)])
+    with pytest.raises(ValueError):
+        mx.tensor_list([torch.zeros(4, 4).t()[1:]])
