@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmx.so")
 SOURCES = ["abi.cpp", "quant.hip", "dequant.hip", "gemm.hip", "optstate.hip", "nvfp.hip",
-           "norm.hip", "glu.hip", "adamw.hip"]
+           "norm.hip", "glu.hip", "adamw.hip", "gemm_glu.hip"]
 ARCH = os.environ.get("MX_OFFLOAD_ARCH", "gfx950")
 
 

@@ -705,6 +705,49 @@ mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src
     return hip_status(mx::launch_glu_bwd_dual(j, (hipStream_t)stream));
 }
 
+mx_status mx_gemm_glu(const void* qa, const uint8_t* sa, const float* ta, int32_t fa, const void* qg,
+                      const uint8_t* sg, const float* tg, const void* qu, const uint8_t* su, const float* tu,
+                      int32_t fb, int64_t M, int64_t F, int64_t K, float alpha, int32_t hadamard_k, int32_t act,
+                      void* h, int64_t ld_h, int32_t out_dtype, int32_t h_fmt, void* qh, uint8_t* sh, void* gate,
+                      int64_t ld_gate, void* up, int64_t ld_up, int32_t ckpt_fmt, void* qgc, uint8_t* sgc,
+                      void* quc, uint8_t* suc, void* stream)
+{
+    g_msg[0] = '\0';
+    mx_status s = check_gemm_operands(qa, sa, ta, fa, qg, sg, tg, fb, M, F, K, hadamard_k);
+    if (s != MX_OK || (s = check_gemm_operands(qa, sa, ta, fa, qu, su, tu, fb, M, F, K, hadamard_k)) != MX_OK) return s;
+    // tiles of 32 elements of F, in eights, by tiles of at least 32 rows, and 512 threads each
+    if ((F + 255) / 256 * 8 * ((M + 31) / 32) >= (int64_t)1 << 22)
+        return fail(MX_ERR_INVALID_ARG, "M x F must be fewer than 2^22 tiles of 32 x 32");
+    if ((s = check_act(act)) != MX_OK) return s;
+    if (!h && !qh) return fail(MX_ERR_INVALID_ARG, "one of h and qh is needed");
+    if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return fail(MX_ERR_INVALID_ARG, "unknown output dtype");
+    if (h && (s = check_matrix(h, ld_h, F, out_dtype, "h")) != MX_OK) return s;
+    if ((gate != nullptr) != (up != nullptr)) return fail(MX_ERR_INVALID_ARG, "gate and up are written together");
+    if (gate && ((s = check_matrix(gate, ld_gate, F, out_dtype, "gate")) != MX_OK ||
+                 (s = check_matrix(up, ld_up, F, out_dtype, "up")) != MX_OK))
+        return s;
+    if ((s = check_copy(h_fmt, qh, sh, F)) != MX_OK) return s;
+    if ((s = check_copy(ckpt_fmt, qgc, sgc, F)) != MX_OK || (s = check_copy(ckpt_fmt, quc, suc, F)) != MX_OK) return s;
+    if ((qgc != nullptr) != (quc != nullptr)) return fail(MX_ERR_INVALID_ARG, "gate and up are checkpointed together");
+    const void* out[] = {h, qh, sh, gate, up, qgc, sgc, quc, suc};
+    for (const void* o : out)
+        for (const void* i : {qa, (const void*)sa, (const void*)ta, qg, (const void*)sg, (const void*)tg, qu, (const void*)su, (const void*)tu})
+            if (o && o == i) return fail(MX_ERR_INVALID_ARG, "an output lies over an input");
+    for (int i = 0; i < 9; i++)
+        for (int k = 0; k < i; k++)
+            if (out[i] && out[i] == out[k]) return fail(MX_ERR_INVALID_ARG, "two outputs have one address");
+    mx::GemmGluJob j{};
+    j.qa = (const uint8_t*)qa; j.sa = sa; j.ta = ta; j.fa = fa;
+    j.qg = (const uint8_t*)qg; j.sg = sg; j.tg = tg;
+    j.qu = (const uint8_t*)qu; j.su = su; j.tu = tu; j.fb = fb;
+    j.M = M; j.F = F; j.K = K; j.alpha = alpha; j.hadamard_k = hadamard_k != 0; j.act = act;
+    j.h = h; j.ld_h = ld_h; j.gate = gate; j.ld_gate = ld_gate; j.up = up; j.ld_up = ld_up;
+    j.out_f32 = out_dtype == MX_OUT_F32;
+    j.h_fmt = h_fmt; j.qh = (uint8_t*)qh; j.sh = sh;
+    j.ckpt_fmt = ckpt_fmt; j.qgc = (uint8_t*)qgc; j.sgc = sgc; j.quc = (uint8_t*)quc; j.suc = suc;
+    return hip_status(mx::launch_gemm_glu(j, (hipStream_t)stream));
+}
+
 namespace {
 
 constexpr int64_t MOST_ELEMENTS = (int64_t)1 << 35;     // of one tensor: chunks are counted with 32 bits

@@ -120,6 +120,24 @@ hipError_t launch_gemm(const GemmJob& j, hipStream_t stream);
 // codes, 4-byte aligned scale arrays
 bool gemm_w4_eligible(const GemmJob& j);
 
+// gate and up projections with their activation and product: A [M][K], the
+// weights [F][K] each; outputs that are nullptr are not written
+struct GemmGluJob {
+    const uint8_t* qa; const uint8_t* sa; const float* ta; int fa;
+    const uint8_t* qg; const uint8_t* sg; const float* tg;
+    const uint8_t* qu; const uint8_t* su; const float* tu; int fb;
+    int64_t M, F, K;
+    float alpha; bool hadamard_k;
+    int act;
+    void* h; int64_t ld_h;
+    void* gate; int64_t ld_gate; void* up; int64_t ld_up;
+    bool out_f32;           // h, gate, up: fp32, otherwise bf16
+    int h_fmt; uint8_t* qh; uint8_t* sh;
+    int ckpt_fmt; uint8_t* qgc; uint8_t* sgc; uint8_t* quc; uint8_t* suc;
+};
+
+hipError_t launch_gemm_glu(const GemmGluJob& j, hipStream_t stream);
+
 // norm forward: s = x (+ residual, rounded; written to sum), its statistics,
 // y and / or the row copy of y, and the checkpoint (row copy) of s
 struct NormFwdJob {

@@ -35,7 +35,7 @@ EXPORTED = ("mx_quantize", "mx_quantize_dual_layout", "mx_gemm", "mx_dequantize"
             "mx_quantize_nvfp", "mx_dequantize_nvfp", "mx_gemm_nvfp",
             "mx_norm_forward", "mx_norm_backward", "mx_norm_backward_workspace_bytes",
             "mx_glu_forward", "mx_glu_backward", "mx_glu_backward_dual_layout",
-            "mx_grad_norm", "mx_grad_norm_workspace_bytes", "mx_adamw_step")
+            "mx_gemm_glu", "mx_grad_norm", "mx_grad_norm_workspace_bytes", "mx_adamw_step")
 MX_STATE_F32 = -1
 NV_PANEL = 32                      # stored rows per CTA-local nvfp scale domain
 
@@ -130,6 +130,10 @@ def load() -> ctypes.CDLL:
     L.mx_glu_backward_dual_layout.restype = _i32
     L.mx_glu_backward_dual_layout.argtypes = [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp,
                                               _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+    L.mx_gemm_glu.restype = _i32
+    L.mx_gemm_glu.argtypes = [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                              ctypes.c_float, _i32, _i32, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i64, _i32,
+                              _vp, _vp, _vp, _vp, _vp]
     L.mx_grad_norm.restype = _i32
     L.mx_grad_norm.argtypes = [_vp, _i32, _i32, ctypes.c_double, _vp, _i64, _vp, _vp]
     L.mx_grad_norm_workspace_bytes.restype = _i64
@@ -789,6 +793,66 @@ def mx_glu_backward_dual_layout(dh: torch.Tensor, gate: Optional[torch.Tensor] =
     hf, qh_col, sh_col, pqh, psh = _copy_out(h_fmt, qh_col, sh_col, (cols, rows), dh, at, _H)
     _check(load().mx_glu_backward_dual_layout(*head, f, pqr, psr, pqc, psc, hf, pqh, psh, _stream_on(stream, at)))
     return GluBackwardDual(q_row, s_row, q_col, s_col, qh_col, sh_col)
+
+
+# ---------------------------------------------------------------------------
+# the gate and up projections with their activation and product
+# ---------------------------------------------------------------------------
+class GemmGlu(NamedTuple):
+    h: Optional[torch.Tensor]
+    qh: Optional[torch.Tensor]
+    sh: Optional[torch.Tensor]
+    gate: Optional[torch.Tensor]
+    up: Optional[torch.Tensor]
+    qg: Optional[torch.Tensor]
+    sg: Optional[torch.Tensor]
+    qu: Optional[torch.Tensor]
+    su: Optional[torch.Tensor]
+
+
+def _operand(q: torch.Tensor, s: torch.Tensor, t: Optional[torch.Tensor], rows: int, K: int, bits: int, at: int,
+             name: str):
+    """Addresses of an MX operand's codes [rows][K], scales and tensor scale."""
+    return (_dense(q, (rows, K * bits // 8), torch.uint8, at, f"the codes of {name}"),
+            _dense(s, (rows, K // 32), torch.uint8, at, f"the scales of {name}"),
+            None if t is None else _one_element(t, torch.float32, at, f"the tensor scale of {name}"))
+
+
+def mx_gemm_glu(qa: torch.Tensor, sa, ta, fa, qg, sg, tg, qu, su, tu, fb, M: int, F: int, K: int, act: str = "silu",
+                alpha: float = 1.0, hadamard_k: bool = False, write_h: bool = True,
+                out_dtype: torch.dtype = torch.bfloat16, h_fmt=None, keep: bool = False, ckpt_fmt=None, h=None,
+                qh=None, sh=None, gate=None, up=None, qgc=None, sgc=None, quc=None, suc=None,
+                stream=None) -> GemmGlu:
+    """h = act(gate) * up with gate = A . Wg^T and up = A . Wu^T from MX operands
+    (A [M][K], the weights [F][K] each), as a tensor, as an MX row copy (h_fmt)
+    or both; gate and up for the backward as tensors (keep) or as 8-bit
+    checkpoints (ckpt_fmt, into qgc, sgc, quc, suc)."""
+    if _other(stream):
+        return _run_on(stream, mx_gemm_glu, locals())
+    at, a, b = qa.get_device(), _fmt(fa), _fmt(fb)
+    pa = _operand(qa, sa, ta, M, K, elem_bits(a), at, "A")
+    pg = _operand(qg, sg, tg, F, K, elem_bits(b), at, "the gate projection")
+    pu = _operand(qu, su, tu, F, K, elem_bits(b), at, "the up projection")
+    shape = (M, F)
+    out_dtype, out = _out_dtype(out_dtype, None)
+
+    def matrix(t, wanted, name):
+        if not wanted:
+            return None, None, 0
+        if t is None:
+            t = qa.new_empty_strided(shape, (F, 1), dtype=out_dtype)
+            return t, t.data_ptr(), F
+        return (t, *_matrix(t, shape, out_dtype, at, name))
+
+    h, ph, ld_h = matrix(h, write_h, "h")
+    gate, pgo, ld_g = matrix(gate, keep, "gate")
+    up, puo, ld_u = matrix(up, keep, "up")
+    hf, qh, sh, pqh, psh = _copy_out(h_fmt, qh, sh, shape, qa, at, _H)
+    cf, qgc, sgc, pqg, psg = _copy_out(ckpt_fmt, qgc, sgc, shape, qa, at, _GATE)
+    _, quc, suc, pqu, psu = _copy_out(ckpt_fmt, quc, suc, shape, qa, at, _UP)
+    _check(load().mx_gemm_glu(*pa, a, *pg, *pu, b, M, F, K, alpha, int(bool(hadamard_k)), ACTS[act], ph, ld_h, out,
+                              hf, pqh, psh, pgo, ld_g, puo, ld_u, cf, pqg, psg, pqu, psu, _stream_on(stream, at)))
+    return GemmGlu(h, qh, sh, gate, up, qgc, sgc, quc, suc)
 
 
 # ---------------------------------------------------------------------------

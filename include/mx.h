@@ -520,6 +520,35 @@ mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src
                                       void* stream);
 
 /*
+ * mx_gemm_glu -- the gate and up projections of a gated MLP block with their
+ * activation and product, in one kernel:
+ *   gate = a_g * A . Wg^T,  up = a_u * A . Wu^T,  h = act(gate) * up,
+ * as mx_gemm and mx_glu_forward compute them, but with gate and up as the fp32
+ * values that mx_gemm would write with MX_OUT_F32 (up to the order of the
+ * sums), rounded only where they are kept.  One row (serving a token) or many.
+ *
+ * qa, sa, ta, fa: A as mx_gemm takes it: [M][K] codes, [M][K/32] scales.
+ * qg, sg, tg, qu, su, tu, fb: Wg and Wu, [F][K] codes and [F][K/32] scales each
+ *        (the halves of one fused projection's column copy, or two).
+ * a_g = alpha * ta * tg * (hadamard_k ? 1/32 : 1), a_u with tu.
+ * h:     [M][F] of `out_dtype` with row stride ld_h, or NULL.  qh, sh: h as a
+ *        row copy of format h_fmt, or both NULL.  At least one of h and qh.
+ * gate, up: [M][F] of `out_dtype` for a backward call from tensors; both or
+ *        neither.
+ * qgc, sgc, quc, suc: checkpoints of gate and up in ckpt_fmt; all four or none.
+ * Formats and M, F, K as mx_gemm (for N: F), F % 32 == 0 where a row copy or
+ * checkpoint is written; any K that mx_gemm takes, any alignment of the scales.
+ * Codes 16-byte aligned.  Outputs must not overlap inputs or each other.
+ * Errors: MX_ERR_INVALID_ARG, MX_ERR_UNSUPPORTED, MX_ERR_ALIGNMENT, MX_ERR_HIP.
+ */
+mx_status mx_gemm_glu(const void* qa, const uint8_t* sa, const float* ta, int32_t fa, const void* qg,
+                      const uint8_t* sg, const float* tg, const void* qu, const uint8_t* su, const float* tu,
+                      int32_t fb, int64_t M, int64_t F, int64_t K, float alpha, int32_t hadamard_k, int32_t act,
+                      void* h, int64_t ld_h, int32_t out_dtype, int32_t h_fmt, void* qh, uint8_t* sh, void* gate,
+                      int64_t ld_gate, void* up, int64_t ld_up, int32_t ckpt_fmt, void* qgc, uint8_t* sgc,
+                      void* quc, uint8_t* suc, void* stream);
+
+/*
  * The optimizer's side of a training step, over many tensors at once.  The
  * tensors of a call are `count` entries of a HOST array, which is read during
  * the call only (a captured launch keeps its own copy of the addresses).  A

@@ -1,0 +1,76 @@
+"""Argument checks of mx_gemm_glu, on the CPU: the C entry point refuses before
+any HIP call (the pointers here are never dereferenced), and the binding
+refuses tensors of the wrong type, shape or place."""
+import os
+
+import pytest
+import torch
+
+from fp4_quantization_block_amd import mx
+
+INV, UNS, ALI = mx.MX_ERR_INVALID_ARG, mx.MX_ERR_UNSUPPORTED, mx.MX_ERR_ALIGNMENT
+P = 0x10000
+AT = dict(qa=1, sa=2, ta=None, qg=3, sg=4, tg=None, qu=5, su=6, tu=None, h=7, qh=8, sh=9, gate=10, up=11, qgc=12, sgc=13,
+          quc=14, suc=15)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(mx.LIB_PATH):
+        pytest.skip("libmx.so not built")
+    return mx.load()
+
+
+def _call(lib, fa=0, fb=0, M=4, F=64, K=64, alpha=1.0, had=0, act=0, ld_h=64, out=1, hf=0, ld_g=64, ld_u=64, cf=0, **at):
+    a = {k: None if v is None else P * v for k, v in AT.items()}
+    a.update(at)
+    return lib.mx_gemm_glu(a["qa"], a["sa"], a["ta"], fa, a["qg"], a["sg"], a["tg"], a["qu"], a["su"], a["tu"], fb, M, F,
+                           K, alpha, had, act, a["h"], ld_h, out, hf, a["qh"], a["sh"], a["gate"], ld_g, a["up"], ld_u,
+                           cf, a["qgc"], a["sgc"], a["quc"], a["suc"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    *[({k: None}, INV) for k in AT if k not in ("ta", "tg", "tu", "h")],
+    (dict(h=None, qh=None, sh=None), INV), (dict(fa=3), INV), (dict(fb=-1), INV), (dict(fa=2), UNS), (dict(fb=2), UNS),
+    (dict(M=0), INV), (dict(F=0), INV), (dict(K=0), INV), (dict(M=-1), INV), (dict(K=48), INV),
+    (dict(K=(1 << 23) + 32), INV), (dict(M=1 << 31), INV), (dict(F=1 << 31), INV), (dict(had=2), INV),
+    (dict(act=3), INV), (dict(act=-1), INV), (dict(out=2), INV), (dict(ld_h=63), INV), (dict(ld_g=63), INV),
+    (dict(ld_u=0), INV), (dict(hf=2), UNS), (dict(hf=3), INV), (dict(cf=2), UNS), (dict(cf=9), INV),
+    (dict(F=40), INV), *[({k: P * AT[k] + 8}, ALI) for k in ("qa", "qg", "qu", "qh", "qgc", "quc")],
+    (dict(ta=P + 2), ALI), (dict(tg=P + 1), ALI), (dict(tu=P + 2), ALI), (dict(h=P * 7 + 1), ALI),
+    (dict(up=P * 11 + 1), ALI), (dict(gate=P * 10 + 2, out=0), ALI), (dict(gate=None, up=None, qgc=None, sgc=None), INV),
+    # outputs over inputs, and over each other
+    (dict(h=P), INV), (dict(qh=P * 3), INV), (dict(sh=P * 6), INV), (dict(suc=P * 2), INV), (dict(gate=P * 5), INV),
+    (dict(h=P * 10), INV), (dict(qgc=P * 14), INV), (dict(sh=P * 13), INV),
+])
+def test_refuses(lib, kw, status):
+    assert _call(lib, **kw) == status
+    assert lib.mx_last_error_message().decode() != ""
+
+
+def _args(M=4, F=64, K=128):
+    def op(rows):
+        return torch.zeros(rows, K, dtype=torch.uint8), torch.zeros(rows, K // 32, dtype=torch.uint8), None
+
+    a, g, u = op(M), op(F), op(F)
+    return [*a, "e4m3", *g, *u, "e4m3", M, F, K]
+
+
+@pytest.mark.parametrize("change,kw,error", [
+    ({}, {}, ValueError),                                                     # on the CPU
+    ({0: torch.zeros(4, 64, dtype=torch.uint8)}, {}, ValueError),             # the shapes of the operands
+    ({1: torch.zeros(4, 3, dtype=torch.uint8)}, {}, ValueError), ({4: torch.zeros(64, 128)}, {}, TypeError),
+    ({8: torch.zeros(64, 8, dtype=torch.uint8)[:, ::2]}, {}, ValueError),
+    ({2: torch.zeros(2)}, {}, ValueError), ({6: torch.zeros(1, dtype=torch.float64)}, {}, TypeError),
+    ({}, dict(out_dtype=torch.float16), TypeError), ({}, dict(h=torch.zeros(4, 64)), TypeError),
+    ({}, dict(h=torch.zeros(4, 63, dtype=torch.bfloat16)), ValueError),
+    ({}, dict(qh=torch.zeros(4, 64, dtype=torch.uint8)), ValueError),         # codes without a format
+    ({}, dict(h_fmt="e4m3", sh=torch.zeros(4, 3, dtype=torch.uint8)), ValueError),
+    ({}, dict(act="relu"), KeyError),
+])
+def test_binding_refuses(change, kw, error):
+    args = _args()
+    for k, v in change.items():
+        args[k] = v
+    with pytest.raises(error):
+        mx.mx_gemm_glu(*args, **kw)

@@ -1,0 +1,246 @@
+"""mx_gemm_glu.  gate and up in fp32 against the oracle's GEMM and the FP8
+matrix instruction's rule, h against act(gate) up in 64 bits of those fp32
+values, and every rounded or quantized output as the fp32 outputs rounded or
+quantized (by the oracle), bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import act_ref as R
+import oracle as O
+from act_util import Guarded, assert_row_copy
+from fp4_quantization_block_amd import mx
+from gpu_util import DEV, check_model, gemm_check, mfma_model, require_gpu, to_device, u8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+class Operands:
+    """A, Wg and Wu quantized on the device, and their codes on the host."""
+
+    def __init__(self, M, F, K, fa="e4m3", fb="e4m3", hadamard=False, two_level=False, unaligned=False, seed=0):
+        rng = np.random.default_rng(seed)
+        a = (rng.standard_normal((M, K)) * np.exp2(rng.integers(-3, 4, (M, 1)))).astype(np.float32)
+        w = (rng.standard_normal((2 * F, K)) * K ** -0.5).astype(np.float32)
+        self.M, self.F, self.K, self.fa, self.fb, self.hadamard = M, F, K, fa, fb, hadamard
+        cfg = [mx.qconfig(f, hadamard=hadamard, two_level=two_level) for f in (fa, fb)]
+        self.a = self._quantize(a, cfg[0], unaligned)
+        # the halves of one projection, each with the scale of the whole
+        q, s, t = self._quantize(w, cfg[1], unaligned)
+        self.gate, self.up = (q[:F], s[:F], t), (q[F:], s[F:], t)
+        if F * q.shape[1] % 16:
+            self.up = (q[F:].clone(), s[F:], t)
+
+    @staticmethod
+    def _quantize(x, cfg, unaligned):
+        q, s, t = mx.mx_quantize(to_device(x), mx.MX_AXIS_ROW, cfg)
+        if unaligned:                               # scales from an odd address on
+            s = torch.cat([s.new_zeros(1), s.flatten()])[1:].view(s.shape)
+        return q, s, t
+
+    def run(self, **kw):
+        return mx.mx_gemm_glu(*self.a, self.fa, *self.gate, *self.up, self.fb, self.M, self.F, self.K,
+                              hadamard_k=self.hadamard, **kw)
+
+    def check_products(self, r, alpha, what):
+        (qa, sa, ta) = self.a
+        for got, (qb, sb, tb), name in ((r.gate, self.gate, "gate"), (r.up, self.up, "up")):
+            host = [u8(x) for x in (qa, sa, qb, sb)]
+            t = [None if x is None else float(x) for x in (ta, tb)]
+            C, bound = O.gemm(host[0], host[1], t[0], self.fa, host[2], host[3], t[1], self.fb, self.M, self.F, self.K,
+                              alpha=alpha, hadamard_k=self.hadamard)
+            got = got.cpu().numpy().astype(np.float64)
+            if self.fa == "e2m1":
+                gemm_check(got, C, bound, False, f"{what} {name}")
+                continue
+            ap = alpha * float(np.prod([x for x in t if x is not None])) / (32 if self.hadamard else 1)
+            rule = mfma_model(host[0], host[1], self.fa, host[2], host[3], self.fb, ap)
+            check_model(got, rule, bound, self.K, f"{what} {name}")
+
+
+def _check(op, act="silu", alpha=1.0, fmts=("e4m3", "e5m2"), what=""):
+    """Everything at once in fp32, then each output on its own and in bf16."""
+    codes = op.F % 32 == 0
+    kw = dict(act=act, alpha=alpha)
+    copies = dict(h_fmt=fmts[0], ckpt_fmt=fmts[1]) if codes else {}
+    r = op.run(out_dtype=torch.float32, keep=True, **copies, **kw)
+    op.check_products(r, alpha, what)
+    g, u = r.gate.cpu().double(), r.up.cpu().double()
+    a, _, err, _ = R.gate(g, act)
+    R.within(r.h, a * u, err * u.abs() + R.U * (a * u).abs(), f"{what} h")
+    b = op.run(out_dtype=torch.bfloat16, keep=True, **kw)
+    for name in ("h", "gate", "up"):
+        assert torch.equal(getattr(b, name), getattr(r, name).bfloat16()), f"{what} {name} in bf16"
+    if codes:
+        only = op.run(write_h=False, h_fmt=fmts[0], **kw)
+        assert only.h is None and only.gate is None and only.qg is None
+        assert_row_copy(only.qh, only.sh, r.h, fmts[0], f"{what} h")
+        assert torch.equal(only.qh, r.qh) and torch.equal(only.sh, r.sh)
+        for name, q, s, src in (("gate", r.qg, r.sg, r.gate), ("up", r.qu, r.su, r.up)):
+            assert_row_copy(q, s, src, fmts[1], f"{what} {name}")
+    return r
+
+
+# rows around the tiles of tokens, F around the tiles of weights, K around the units of 128 bytes and the workgroup's
+# eight waves; larger ones with K that the large tiles take or do not take
+SHAPES = [(1, 32, 32), (1, 1, 64), (2, 33, 96), (31, 64, 128), (32, 31, 160), (33, 96, 1024), (64, 257, 1056),
+          (65, 128, 1152), (7, 320, 2304), (300, 200, 96), (257, 513, 384), (129, 260, 640), (512, 384, 512),
+          (255, 160, 256), (520, 130, 224)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e2m1", "e2m1")])
+def test_shapes(shape, fa, fb):
+    _check(Operands(*shape, fa, fb, seed=sum(shape)), what=f"{shape} {fa} {fb}")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("shape", [(3, 96, 256), (300, 288, 256)], ids=str)
+def test_activations(act, shape):
+    _check(Operands(*shape, seed=3), act=act, alpha=3.0, fmts=("e5m2", "e4m3"), what=act)
+
+
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e5m2"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("shape", [(9, 64, 288), (260, 192, 384)], ids=str)
+def test_formats(fa, fb, shape):
+    _check(Operands(*shape, fa, fb, seed=4), what=f"{fa} {fb}")
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("M", [5, 300])
+def test_hadamard_tensor_scales_and_alpha(fmt, M):
+    _check(Operands(M, 160, 512, fmt, fmt, hadamard=True, two_level=True, seed=5), alpha=0.75, what="all factors")
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("M", [5, 300])
+def test_unaligned_scales(fmt, M):
+    _check(Operands(M, 96, 512, fmt, fmt, unaligned=True, seed=6), what="scales from an odd address on")
+
+
+@pytest.mark.parametrize("M,F", [(3, 77), (300, 271), (1, 40)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_strided_outputs_stay_inside(M, F, dtype):
+    op = Operands(M, F, 256, seed=7)
+    want = op.run(out_dtype=dtype, keep=True)
+    out = {k: Guarded(M, F, dtype, offset=3, pad=5) for k in ("h", "gate", "up")}
+    op.run(out_dtype=dtype, keep=True, **{k: v.view for k, v in out.items()})
+    for k, v in out.items():
+        assert torch.equal(v.view, getattr(want, k)), k
+        v.check(k)
+
+
+@pytest.mark.parametrize("M,F", [(3, 96), (300, 288)])
+def test_copies_stay_inside(M, F):
+    op = Operands(M, F, 256, seed=8)
+    want = op.run(h_fmt="e4m3", ckpt_fmt="e4m3")
+    kw, bufs = {}, {}
+    for q, s, name in (("qh", "sh", "h"), ("qgc", "sgc", "g"), ("quc", "suc", "u")):
+        bufs[name] = [torch.full((n + 64,), 9, dtype=torch.uint8, device=DEV) for n in (M * F, M * F // 32)]
+        kw[q], kw[s] = bufs[name][0][16:16 + M * F].view(M, F), bufs[name][1][3:3 + M * F // 32].view(M, F // 32)
+    op.run(write_h=False, h_fmt="e4m3", ckpt_fmt="e4m3", **kw)
+    for name, (bq, bs) in bufs.items():
+        assert torch.equal(bq[16:16 + M * F].view(M, F), getattr(want, "q" + name))
+        assert torch.equal(bs[3:3 + M * F // 32].view(M, F // 32), getattr(want, "s" + name))
+        assert torch.all(bq[:16] == 9) and torch.all(bq[16 + M * F:] == 9)
+        assert torch.all(bs[:3] == 9) and torch.all(bs[3 + M * F // 32:] == 9)
+
+
+@pytest.mark.parametrize("M", [4, 300])
+def test_non_finite_rows_and_columns(M):
+    """A NaN block makes its row (of A) or its column (of a weight) NaN, and nothing else."""
+    op = Operands(M, 96, 512, seed=9)
+    clean = op.run(out_dtype=torch.float32, keep=True, h_fmt="e4m3")
+    (qa, sa, _), (qg, sg, _) = op.a, op.gate
+    sa[2, 3], sg[33, 1] = 0xFF, 0xFF
+    r = op.run(out_dtype=torch.float32, keep=True, h_fmt="e4m3", ckpt_fmt="e4m3")
+    for name, whole in (("gate", False), ("up", True), ("h", False)):
+        got, bad = getattr(r, name), torch.zeros(M, 96, dtype=torch.bool, device=DEV)
+        bad[2] = True
+        if not whole:
+            bad[:, 33] = True
+        assert torch.all(torch.isnan(got[bad])), name
+        assert torch.equal(got[~bad], getattr(clean, name)[~bad]), name
+    assert torch.all(r.sh[2] == 0xFF) and torch.all(r.sh[:, 1] == 0xFF) and torch.all(r.qg[:, 32:64] == 0x7F)
+    keep = [i for i in range(M) if i != 2]
+    assert torch.equal(r.sh[keep][:, [0, 2]], clean.sh[keep][:, [0, 2]])
+
+
+def test_zero_operands():
+    for M in (2, 300):
+        op = Operands(M, 64, 256, seed=10)
+        op.a[0].zero_()
+        r = op.run(out_dtype=torch.float32, keep=True, h_fmt="e4m3")
+        assert not r.h.any() and not r.gate.any() and not r.qh.bitwise_and(0x7F).any() and not r.sh.any()
+
+
+@pytest.mark.parametrize("M", [1, 24, 300])
+def test_graph_on_a_side_stream(M):
+    op = Operands(M, 96, 512, seed=11)
+    qh, sh = (torch.empty(M, n, dtype=torch.uint8, device=DEV) for n in (96, 3))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        op.run(write_h=False, h_fmt="e4m3", qh=qh, sh=sh)
+    for k in range(3):
+        other = Operands(M, 96, 512, seed=20 + k)
+        op.a[0].copy_(other.a[0])
+        op.a[1].copy_(other.a[1])
+        qh.zero_()
+        want = op.run(write_h=False, h_fmt="e4m3")
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(qh, want.qh) and torch.equal(sh, want.sh)
+
+
+def test_stream_argument():
+    op, side = Operands(300, 288, 512, seed=12), torch.cuda.Stream()
+    want = op.run(keep=True)
+    side.wait_stream(torch.cuda.current_stream())
+    got = op.run(keep=True, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(getattr(got, k), getattr(want, k)) for k in ("h", "gate", "up"))
+
+
+@pytest.mark.parametrize("M,F,K,fmt", [(1, 14336, 4096, "e4m3"), (17, 14336, 4096, "e2m1"), (1000, 4096, 4096, "e4m3")])
+def test_full_size_entries(M, F, K, fmt):
+    """Full inner lengths: sampled entries of gate and up."""
+    op = Operands(M, F, K, fmt, fmt, seed=13)
+    r = op.run(out_dtype=torch.float32, keep=True)
+    rng = np.random.default_rng(0)
+    ii, jj = rng.integers(0, M, 500), rng.integers(0, F, 500)
+    ii[:2], jj[:2] = (0, M - 1), (0, F - 1)
+    (qa, sa, _) = op.a
+    for got, (qb, sb, _) in ((r.gate, op.gate), (r.up, op.up)):
+        host = [u8(x) for x in (qa, sa, qb, sb)]
+        C, bound = O.gemm_entries(host[0], host[1], None, fmt, host[2], host[3], None, fmt, M, F, K, ii, jj)
+        got = got.cpu().numpy()[ii, jj].astype(np.float64)
+        if fmt == "e2m1":
+            gemm_check(got, C, bound, False, "entries")
+        else:
+            import mfma_model as MM
+            rule = MM.model(host[0], host[1], O._fmt(fmt), host[2], host[3], O._fmt(fmt), 1.0, ii, jj)[0]
+            check_model(got, rule, bound, K, "entries")
+
+
+def test_backward_reads_what_it_keeps():
+    """The backward from the checkpoints, and from the tensors, is the one of mx_glu_forward's."""
+    op = Operands(320, 288, 512, seed=14)
+    r = op.run(keep=True, ckpt_fmt="e4m3")
+    dh = torch.randn(320, 288, device=DEV).bfloat16()
+    d = mx.mx_glu_backward_dual_layout(dh, act="silu", gate_ckpt=mx.checkpoint("e4m3", r.qg, r.sg),
+                                       up_ckpt=mx.checkpoint("e4m3", r.qu, r.su), fmt="e5m2", h_fmt="e4m3")
+    f32 = op.run(out_dtype=torch.float32, keep=True)
+    f = mx.mx_glu_forward(f32.gate, f32.up, "silu", ckpt_fmt="e4m3")
+    e = mx.mx_glu_backward_dual_layout(dh, act="silu", gate_ckpt=mx.checkpoint("e4m3", f.qg, f.sg),
+                                       up_ckpt=mx.checkpoint("e4m3", f.qu, f.su), fmt="e5m2", h_fmt="e4m3")
+    assert all(torch.equal(a, b) for a, b in zip(d, e))
+    b = mx.mx_glu_backward(dh, r.gate, r.up, "silu")
+    c = mx.mx_glu_backward(dh, f32.gate.bfloat16(), f32.up.bfloat16(), "silu")
+    assert torch.equal(b.dgate, c.dgate) and torch.equal(b.dup, c.dup)
