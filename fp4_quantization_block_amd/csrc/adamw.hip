@@ -298,17 +298,45 @@ typedef Table<NormEntry, 64> NormTable;
 
 constexpr int NORM_WGS = 1024;          // of a launch, at most: four on each CU
 
+// A workgroup's chunk: four 16-byte loads a thread, of N consecutive elements each
+template <int SRC> struct NormChunk {
+    static constexpr int N = 16 / ElemT<SRC>::bytes, elements = 256 * 4 * N;
+    Chunk<SRC, N> c[4];
+};
+
 template <int SRC>
-__device__ __forceinline__ double square_sum(const uint8_t* x, int64_t n, int64_t base)
+__device__ __forceinline__ void load_norm_chunk(NormChunk<SRC>& k, const uint8_t* x, int64_t n, int64_t base)
+{
+    constexpr int N = NormChunk<SRC>::N;
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int64_t at = base + 256 * N * u + N * threadIdx.x;
+        if (at + N <= n) {
+            k.c[u] = load_chunk<SRC, N>(x, at);
+        } else {
+#pragma unroll
+            for (int w = 0; w < 4; w++) k.c[u].w[w] = 0;
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                if (at + i < n) {
+                    if constexpr (SRC == SRC_F32) k.c[u].w[i] = __float_as_uint(((const float*)x)[at + i]);
+                    else k.c[u].w[i / 2] |= (uint32_t)((const uint16_t*)x)[at + i] << (16 * (i % 2));
+                }
+        }
+    }
+}
+
+template <int SRC>
+__device__ __forceinline__ double square_sum(const NormChunk<SRC>& k)
 {
     double sum = 0.0;
-    float v[4][4];
-#pragma unroll
-    for (int u = 0; u < 4; u++) load4<SRC>(x, base + 1024 * u, n, v[u]);
 #pragma unroll
     for (int u = 0; u < 4; u++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) sum = __builtin_fma((double)v[u][i], (double)v[u][i], sum);
+        for (int i = 0; i < NormChunk<SRC>::N; i++) {
+            const double v = (double)chunk_value<SRC, NormChunk<SRC>::N>(k.c[u], i);
+            sum = __builtin_fma(v, v, sum);
+        }
     return sum;
 }
 
@@ -329,15 +357,31 @@ __device__ __forceinline__ void write_norm(double sum, double max_norm, float* o
     out[1] = !(norm < __builtin_inf()) ? __builtin_nanf("") : norm > max_norm ? (float)(max_norm / norm) : 1.0f;
 }
 
-// a partial sum of the table's chunks from each workgroup
+// A partial sum from each workgroup, of a run of neighbouring chunks; the next
+// chunk is asked for before the last one is summed.
 template <int SRC>
 __global__ __launch_bounds__(256) void k_grad_norm(const NormTable table, int chunks, double* partial)
 {
     __shared__ double red[4];
+    const int per = chunks / (int)gridDim.x, more = chunks % (int)gridDim.x, wg = blockIdx.x;
+    int c = wg * per + min(wg, more);
+    const int end = c + per + (wg < more ? 1 : 0);
+    int t = tensor_of(table, c);
+    auto load = [&](NormChunk<SRC>& k) __attribute__((always_inline)) {
+        while (t + 1 < table.count && table.first[t + 1] <= c) t++;
+        load_norm_chunk<SRC>(k, table.t[t].x, table.t[t].n, (int64_t)(c - table.first[t]) * NormChunk<SRC>::elements);
+        c++;
+    };
     double sum = 0.0;
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int ti = tensor_of(table, c);
-        sum += square_sum<SRC>(table.t[ti].x, table.t[ti].n, (int64_t)(c - table.first[ti]) * CHUNK + 4 * threadIdx.x);
+    NormChunk<SRC> a, b;
+    load(a);                                         // (a launch has no more workgroups than chunks)
+    for (;;) {
+        if (c < end) load(b);
+        else b = NormChunk<SRC>{};
+        sum += square_sum<SRC>(a);
+        if (c >= end) { sum += square_sum<SRC>(b); break; }
+        load(a);
+        sum += square_sum<SRC>(b);
     }
     sum = workgroup_sum(sum, red);
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -354,17 +398,17 @@ __global__ __launch_bounds__(256) void k_grad_norm_join(const double* partial, i
 
 // ---------------------------------------------------------------------------
 // Walks the tensors of a call, filling tables: put(slot, tensor) fills one
-// slot, flush(table, chunks) launches a full table.  Empty tensors are passed over.
+// slot, in chunks of so many elements; flush(table, chunks) launches a full table.  Empty tensors are passed over.
 // ---------------------------------------------------------------------------
 template <typename T, typename Entry, typename Put, typename Flush>
-hipError_t walk(const Entry* tensors, int count, int most_chunks, Put put, Flush flush)
+hipError_t walk(const Entry* tensors, int count, int elements, int most_chunks, Put put, Flush flush)
 {
     T table;
     int chunks = 0;
     table.count = 0;
     for (int i = 0; i < count; i++) {
         if (tensors[i].n == 0) continue;
-        const int more = (int)((tensors[i].n + CHUNK - 1) / CHUNK);
+        const int more = (int)((tensors[i].n + elements - 1) / elements);
         if (table.count > 0 && (table.count == T::most || chunks > most_chunks - more)) {
             const hipError_t e = flush(table, chunks);
             if (e != hipSuccess) return e;
@@ -397,7 +441,7 @@ void put8(Adam8& e, const mx_adamw_tensor& t)
 template <int PS, int GS>
 hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
-    return walk<Table32>(j.tensors, j.count, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
+    return walk<Table32>(j.tensors, j.count, CHUNK, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
         k_adamw32<PS, GS><<<chunks, 256, 0, s>>>(t, c);
         return hipGetLastError();
     });
@@ -406,7 +450,7 @@ hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 template <int FMT, int G>
 hipError_t run8(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
-    return walk<Table8>(j.tensors, j.count, MOST_CHUNKS, put8, [&](const Table8& t, int chunks) {
+    return walk<Table8>(j.tensors, j.count, CHUNK, MOST_CHUNKS, put8, [&](const Table8& t, int chunks) {
         k_adamw8<FMT, G><<<chunks, 256, 0, s>>>(t, c, j.psrc, j.gsrc);
         return hipGetLastError();
     });
@@ -442,19 +486,24 @@ int64_t grad_norm_work_bytes(int count)
     return ((int64_t)(count < 1 ? 1 : count) + NormTable::most - 1) / NormTable::most * NORM_WGS * (int64_t)sizeof(double);
 }
 
-hipError_t launch_grad_norm(const GradNormJob& j, hipStream_t s)
+template <int SRC>
+hipError_t run_norm(const GradNormJob& j, int& partials, hipStream_t s)
 {
-    int partials = 0;
-    const hipError_t e = walk<NormTable>(
-        j.tensors, j.count, 1 << 30,
+    return walk<NormTable>(
+        j.tensors, j.count, NormChunk<SRC>::elements, 1 << 30,
         [](NormEntry& e, const mx_tensor& t) { e.x = (const uint8_t*)t.x; e.n = t.n; },
         [&](const NormTable& t, int chunks) {
             const int wgs = chunks < NORM_WGS ? chunks : NORM_WGS;
-            if (j.src == SRC_F32) k_grad_norm<SRC_F32><<<wgs, 256, 0, s>>>(t, chunks, j.work + partials);
-            else k_grad_norm<SRC_BF16><<<wgs, 256, 0, s>>>(t, chunks, j.work + partials);
+            k_grad_norm<SRC><<<wgs, 256, 0, s>>>(t, chunks, j.work + partials);
             partials += wgs;
             return hipGetLastError();
         });
+}
+
+hipError_t launch_grad_norm(const GradNormJob& j, hipStream_t s)
+{
+    int partials = 0;
+    const hipError_t e = j.src == SRC_F32 ? run_norm<SRC_F32>(j, partials, s) : run_norm<SRC_BF16>(j, partials, s);
     if (e != hipSuccess) return e;
     k_grad_norm_join<<<1, 256, 0, s>>>(j.work, partials, j.out, j.max_norm);
     return hipGetLastError();

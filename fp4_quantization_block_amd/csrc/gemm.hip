@@ -54,7 +54,7 @@
 // with its own L2); the tile order below gives each XCD a compact block of
 // tiles (4 tile rows x 8 tile columns when the grid allows), so the A rows
 // and B columns one XCD streams are shared by its tiles through its L2.
-#include "mx_device.h"
+#include "act_device.h"
 #include "mx_internal.h"
 
 namespace mx {
@@ -81,6 +81,16 @@ struct GArgs {
     int reg_path;             // 1: scale arrays not 4-byte aligned -> every stage via registers
 };
 
+// GLU: a second operand beside B, and what the epilogue writes (see glu_slab)
+struct GluArgs : GArgs {
+    const uint8_t* qu; const uint8_t* su; const float* tu;
+    int act;
+    void* h; int64_t ld_h; void* gate; int64_t ld_gate; void* up; int64_t ld_up;
+    bool out_f32;
+    int h_fmt; uint8_t* qh; uint8_t* sh;
+    int ckpt_fmt; uint8_t* qgc; uint8_t* sgc; uint8_t* quc; uint8_t* suc;
+};
+
 template <int FMT> struct MfmaFmt;
 template <> struct MfmaFmt<E4M3> { static constexpr int code = 0; };
 template <> struct MfmaFmt<E5M2> { static constexpr int code = 1; };
@@ -97,12 +107,7 @@ __device__ __forceinline__ int swz(int row, int chunk) { return row * BKB + ((ch
 // cold on every launch; one convert per pair instead of a five-instruction
 // software rounding per value halves that code (and measurably the
 // kernel's fixed cost).
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t f32x2_to_bf16x2_rne(float a, float b)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
-}
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2_rne(float a, float b) { return pack_bf16(a, b); }
 
 // tile index of this workgroup: XCD-aware, then grouped row-major order
 __device__ __forceinline__ void tile_of(int wg, int tiles_m, int tiles_n, int& tm, int& tn)
@@ -622,11 +627,86 @@ __device__ __forceinline__ void store_nt16(void* p, uint4 v)
     __builtin_nontemporal_store(u32x4v{v.x, v.y, v.z, v.w}, (u32x4v*)p);
 }
 
+// Output kinds of k_gemm_w4 beside fp32 (0), bf16 (1) and MX codes (2 E4M3, 3 E5M2)
+constexpr int GLU = 4;
+
+// OUT == GLU: the gated activation of a 32 x 64 slab of a wave's part, gate
+// and up staged as fp32 in the wave's LDS (rows of GLU_PITCH floats).  Eight
+// lanes take a row, eight consecutive elements each, so that the four lanes of
+// a 1x32 block are neighbours (encode_row_chunk) and a row's 64 elements leave
+// as one run.
+constexpr int GLU_PITCH = 68;
+
+template <int ACT>
+__device__ __forceinline__ void glu8(const float (&g)[8], const float (&u)[8], float (&h)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        float a, d;
+        gate<ACT, false>(g[e], a, d);
+        h[e] = a * u[e];
+    }
+}
+
+__device__ __forceinline__ void store8(bool f32, void* base, int64_t at, int n, const float (&v)[8])
+{
+    if (n >= 8) {
+        if (f32) store_chunk<SRC_F32>(base, at, make_chunk<SRC_F32>(v));
+        else store_chunk<SRC_BF16>(base, at, make_chunk<SRC_BF16>(v));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (e < n) {
+                if (f32) store_elem<SRC_F32>(base, at + e, v[e]);
+                else store_elem<SRC_BF16>(base, at + e, v[e]);
+            }
+    }
+}
+
+__device__ __forceinline__ void glu_slab(const GluArgs& a, const float* fg, const float* fu, int64_t m0, int64_t f0, int lane)
+{
+    const int64_t f = f0 + 8 * (lane & 7);
+    const int n = (int)min((int64_t)8, a.N - f);             // elements of the row that are there (none: <= 0)
+#pragma unroll 1
+    for (int it = 0; it < 4; it++) {
+        const int row = 8 * it + (lane >> 3);
+        const int64_t m = m0 + row;
+        const int at = row * GLU_PITCH + 8 * (lane & 7);
+        float g[8], u[8], h[8];
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+            const float4 x = *(const float4*)(fg + at + k), y = *(const float4*)(fu + at + k);
+            g[k] = x.x; g[k + 1] = x.y; g[k + 2] = x.z; g[k + 3] = x.w;
+            u[k] = y.x; u[k + 1] = y.y; u[k + 2] = y.z; u[k + 3] = y.w;
+        }
+        if (a.act == ACT_SILU) glu8<ACT_SILU>(g, u, h);
+        else if (a.act == ACT_GELU) glu8<ACT_GELU>(g, u, h);
+        else glu8<ACT_GELU_TANH>(g, u, h);
+        const bool valid = m < a.M && n > 0;
+        if (valid) {
+            if (a.h) store8(a.out_f32, a.h, m * a.ld_h + f, n, h);
+            if (a.gate) {
+                store8(a.out_f32, a.gate, m * a.ld_gate + f, n, g);
+                store8(a.out_f32, a.up, m * a.ld_up + f, n, u);
+            }
+        }
+        // (F is then a multiple of 32: the four lanes of a block are valid or not together)
+        if (a.qh) encode_row_chunk(a.h_fmt, h, valid, m * a.N + f, a.qh, a.sh);
+        if (a.qgc) {
+            encode_row_chunk(a.ckpt_fmt, g, valid, m * a.N + f, a.qgc, a.sgc);
+            encode_row_chunk(a.ckpt_fmt, u, valid, m * a.N + f, a.quc, a.suc);
+        }
+    }
+}
+
 // NB: tile columns (256, or 128 for the half tiles of a last partial round:
 // each wave then computes 128 x 64 and the B tile has 128 rows).
+// OUT == GLU: B is Wg, and the tile's 256 "columns" are 128 of gate and the
+// same 128 of up, in runs of 32 rows of Wg, Wg, Wu, Wu for each half: a wave's
+// accumulators j = 0, 1 hold gate and j + 2 up of the same elements.
 template <int FA, int FB, int OUT, int NB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void k_gemm_w4(GArgs g)
+void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr bool FP4 = (FA == E2M1);
@@ -637,6 +717,7 @@ void k_gemm_w4(GArgs g)
     constexpr int RB = NB / 32;                      // 32-row load runs of the B tile (8 or 4)
     constexpr int NM = 4 * JT;                       // MFMAs per k-step and wave
     static_assert(NB == 256 || (NB == 128 && OUT < 2), "half tiles serve the fp32 / bf16 outputs");
+    constexpr int NT = OUT == GLU ? NB / 2 : NB;     // columns of N that the tile covers
     typedef W4Frag<FP4, JT> Frag;
     __shared__ __align__(16) uint8_t lA0[TILE_BYTES], lA1[TILE_BYTES];
     __shared__ __align__(16) uint8_t lB0[NB * BKB], lB1[NB * BKB];
@@ -654,7 +735,7 @@ void k_gemm_w4(GArgs g)
 
     int tm, tn;
     tile_of(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * NB;
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * NT;
     const int64_t kbytes = g.K / EPB;
     const int64_t kblocks = g.K / 32;
     const int nstages = (int)(kbytes / BKB);
@@ -671,12 +752,20 @@ void k_gemm_w4(GArgs g)
                                                  (int)(uint32_t)n, 0x00020000);
     };
     // B rows past the tile (a half tile's other half) also read as zero
-    const int64_t nend = min(g.N, n0 + NB);
+    const int64_t nend = min(g.N, n0 + NT);
     const auto ra = rsrc(g.qa, m0, g.M, kbytes), rb = rsrc(g.qb, n0, nend, kbytes);
-    const auto rsa_ = rsrc(g.sa, m0, g.M, kblocks), rsb_ = rsrc(g.sb, n0, nend, kblocks);
+    const auto rsa_ = rsrc(g.sa, m0, g.M, kblocks);
+    auto rsb_ = rsrc(g.sb, n0, nend, kblocks);
+    auto rb2 = rb;                                   // GLU: of Wu
+    if constexpr (OUT == GLU) {
+        rb2 = rsrc(g.qu, n0, nend, kbytes);
+        if (wave & 1) rsb_ = rsrc(g.su, n0, nend, kblocks);
+    }
     const int lr = tid >> 3, lc = tid & 7;
     const uint32_t voff = (uint32_t)(lr * kbytes + lc * 16);
     const uint32_t vsoff = (uint32_t)(tid * kblocks);
+    // scale row of B: tile row tid (GLU: waves 0, 1 the first 64 rows of Wg and of Wu, waves 2, 3 the other 64)
+    const uint32_t vsoffb = OUT == GLU ? (uint32_t)((64 * (wave >> 1) + lane) * kblocks) : vsoff;
     const uint32_t prow = (uint32_t)(32 * kbytes);        // offset of run p: p * prow
     // LDS byte offset of the thread's chunk in run p: p * 32 * BKB + wofs
     const uint32_t wofs = (uint32_t)swz(lr, lc);
@@ -694,28 +783,36 @@ void k_gemm_w4(GArgs g)
     __shared__ __align__(16) uint8_t lPF[4 * 1024];
     const uint32_t pfa = (uint32_t)((32 * (tn & 7) + 8 * wave + (lane >> 3)) * kbytes + (lane & 7) * 16);
     // (half tiles: 32 B rows by tile row, one load)
-    const uint32_t pfb = (uint32_t)(((NB / 4) * (tm & 3) + (NB / 16) * wave + (lane >> 3)) * kbytes + (lane & 7) * 16);
+    // (GLU: 64 rows of Wg or of Wu by tile row)
+    const int pfq = OUT == GLU ? (tm >> 1) & 1 : tm & 3;
+    const uint32_t pfb = (uint32_t)(((NB / 4) * pfq + (NB / 16) * wave + (lane >> 3)) * kbytes + (lane & 7) * 16);
+    const auto rpf = OUT == GLU && (tm & 1) ? rb2 : rb;
     auto prefetch = [&](int s) __attribute__((always_inline)) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(lPF + wave * 1024), 16, pfa, s * BKB, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(lPF + wave * 1024), 16, pfb, s * BKB, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rpf, (lds_void*)(lPF + wave * 1024), 16, pfb, s * BKB, 0, 0);
         if constexpr (NB == 256)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(lPF + wave * 1024), 16, pfb + 8 * (uint32_t)kbytes, s * BKB, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rpf, (lds_void*)(lPF + wave * 1024), 16, pfb + 8 * (uint32_t)kbytes, s * BKB, 0, 0);
     };
     auto gl16 = [&](__amdgpu_buffer_rsrc_t r, int p, int s) __attribute__((always_inline)) {
         return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, voff + p * prow, s * BKB, 0));
+    };
+    // run p of the B tile
+    auto gl16b = [&](int p, int s) __attribute__((always_inline)) {
+        if constexpr (OUT == GLU) return gl16((p & 2) ? rb2 : rb, 2 * (p >> 2) + (p & 1), s);
+        else return gl16(rb, p, s);
     };
     auto gload_scales = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int d = 0; d < SBD; d++) {
             stSA[d] = __builtin_amdgcn_raw_buffer_load_b32(rsa_, vsoff, s * 4 * SBD + 4 * d, 0);
-            stSB[d] = __builtin_amdgcn_raw_buffer_load_b32(rsb_, vsoff, s * 4 * SBD + 4 * d, 0);
+            stSB[d] = __builtin_amdgcn_raw_buffer_load_b32(rsb_, vsoffb, s * 4 * SBD + 4 * d, 0);
         }
     };
     auto gload = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < 8; p++) {
             stA[p] = gl16(ra, p, s);
-            if (p < RB) stB[p] = gl16(rb, p, s);
+            if (p < RB) stB[p] = gl16b(p, s);
         }
         gload_scales(s);
     };
@@ -791,13 +888,13 @@ void k_gemm_w4(GArgs g)
 #pragma unroll
         for (int p = 0; p < 8; p++) {
             uA[p] = gl16(ra, p, s1);
-            if (p < RB) uB[p] = gl16(rb, p, s1);
+            if (p < RB) uB[p] = gl16b(p, s1);
         }
         uint32_t uSA[SBD], uSB[SBD];
 #pragma unroll
         for (int d = 0; d < SBD; d++) {
             uSA[d] = __builtin_amdgcn_raw_buffer_load_b32(rsa_, vsoff, s1 * 4 * SBD + 4 * d, 0);
-            uSB[d] = __builtin_amdgcn_raw_buffer_load_b32(rsb_, vsoff, s1 * 4 * SBD + 4 * d, 0);
+            uSB[d] = __builtin_amdgcn_raw_buffer_load_b32(rsb_, vsoffb, s1 * 4 * SBD + 4 * d, 0);
         }
 #pragma unroll
         for (int p = 0; p < 8; p++) {
@@ -862,7 +959,7 @@ void k_gemm_w4(GArgs g)
             if constexpr (ks == 0) {
                 if (m < RB) {
                     swrite_b(yB, m);
-                    stB[m] = gl16(rb, m, s2);
+                    stB[m] = gl16b(m, s2);
                 }
                 if (m == (NB == 256 ? 9 : 5)) prefetch(min(s + 4, nstages - 1));
             }
@@ -943,6 +1040,40 @@ void k_gemm_w4(GArgs g)
                 for (int k = 0; k < 8; k++)
                     if (gcol + k < g.N) dst[k] = e[k];
             }
+        }
+    } else if constexpr (OUT == GLU) {
+        float ag = g.alpha, au;
+        if (g.ta) ag = ag * *g.ta;
+        au = ag;
+        if (g.tb) ag = ag * *g.tb;
+        if (g.tu) au = au * *g.tu;
+        if (g.hadamard_k) ag = ag * 0.03125f, au = au * 0.03125f;
+        uint8_t* buf = wave == 0 ? lA0 : wave == 1 ? lA1 : wave == 2 ? lB0 : lB1;
+        float* fg = (float*)buf;
+        float* fu = fg + 32 * GLU_PITCH;
+        auto put = [&](auto IC) __attribute__((always_inline)) {
+            constexpr int i = decltype(IC)::value;
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const int at = (8 * (r / 4) + 4 * h + (r % 4)) * GLU_PITCH + j * 32 + l32;
+                    fg[at] = acc[i][j][r] * ag;
+                    fu[at] = acc[i][j + 2][r] * au;
+                }
+        };
+        // one copy of the slab's code, run four times: the code is fetched cold
+#pragma unroll 1
+        for (int i = 0; i < 4; i++) {
+            if (i == 0) put(std::integral_constant<int, 0>{});
+            else if (i == 1) put(std::integral_constant<int, 1>{});
+            else if (i == 2) put(std::integral_constant<int, 2>{});
+            else put(std::integral_constant<int, 3>{});
+            __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_wave_barrier();
+            glu_slab(g, fg, fu, m0 + wm * 128 + i * 32, n0 + wn * 64, lane);
+            __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_wave_barrier();
         }
     } else if constexpr (OUT >= 2) {
         // MX-quantized output (OUT 2: E4M3, 3: E5M2), 1x32 blocks along the
@@ -1063,12 +1194,46 @@ hipError_t launch2(const GArgs& a, int out, hipStream_t s)
     }
 }
 
+template <int FA, int FB>
+hipError_t launch_glu(const GluArgs& a, hipStream_t s)
+{
+    k_gemm_w4<FA, FB, GLU, 256><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 bool gemm_w4_eligible(const GemmJob& j)
 {
     const int64_t kbytes = j.fa == E2M1 ? j.K / 2 : j.K;
     return kbytes % BKB == 0 && (((uintptr_t)j.sa | (uintptr_t)j.sb) & 3u) == 0;
+}
+
+bool gemm_glu_w4_eligible(const GemmGluJob& j)
+{
+    const int64_t kbytes = j.fa == E2M1 ? j.K / 2 : j.K;
+    return kbytes % BKB == 0 && (((uintptr_t)j.sa | (uintptr_t)j.sg | (uintptr_t)j.su) & 3u) == 0;
+}
+
+hipError_t launch_gemm_glu_w4(const GemmGluJob& j, hipStream_t stream)
+{
+    GluArgs a{};
+    a.qa = j.qa; a.sa = j.sa; a.ta = j.ta;
+    a.qb = j.qg; a.sb = j.sg; a.tb = j.tg;
+    a.qu = j.qu; a.su = j.su; a.tu = j.tu;
+    a.M = j.M; a.N = j.F; a.K = j.K;
+    a.alpha = j.alpha; a.hadamard_k = j.hadamard_k; a.act = j.act;
+    a.h = j.h; a.ld_h = j.ld_h; a.gate = j.gate; a.ld_gate = j.ld_gate; a.up = j.up; a.ld_up = j.ld_up;
+    a.out_f32 = j.out_f32;
+    a.h_fmt = j.h_fmt; a.qh = j.qh; a.sh = j.sh;
+    a.ckpt_fmt = j.ckpt_fmt; a.qgc = j.qgc; a.sgc = j.sgc; a.quc = j.quc; a.suc = j.suc;
+    a.tiles_m = (int)((j.M + BM - 1) / BM);
+    a.tiles_n = (int)((j.F + BN / 2 - 1) / (BN / 2));
+    if (j.fa == E2M1) return launch_glu<E2M1, E2M1>(a, stream);
+    if (j.fa == E4M3 && j.fb == E4M3) return launch_glu<E4M3, E4M3>(a, stream);
+    if (j.fa == E5M2 && j.fb == E4M3) return launch_glu<E5M2, E4M3>(a, stream);
+    if (j.fa == E4M3 && j.fb == E5M2) return launch_glu<E4M3, E5M2>(a, stream);
+    return launch_glu<E5M2, E5M2>(a, stream);
 }
 
 hipError_t launch_gemm(const GemmJob& j, hipStream_t stream)
