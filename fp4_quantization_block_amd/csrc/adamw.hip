@@ -23,6 +23,8 @@ namespace mx {
 namespace {
 
 constexpr int CHUNK = 4096;             // elements of a workgroup's chunk: 256 threads x 16
+constexpr int SMALL_CHUNK = 1024;       // of the step with fp32 moments where there are few: x 4
+constexpr int SMALL_STEP = 1 << 22;      // elements of a launch below which it takes small chunks
 constexpr int MOST_CHUNKS = 1 << 23;    // of a launch (a launch counts its threads with 32 bits)
 
 // ---------------------------------------------------------------------------
@@ -52,6 +54,7 @@ __host__ __device__ inline AdamScalars adam_scalars(const AdamHyper& h, double l
     s.b1 = (float)h.beta1; s.c1 = (float)(1.0 - h.beta1);
     s.b2 = (float)h.beta2; s.c2 = (float)(1.0 - h.beta2);
     s.eps = (float)h.eps;
+    if (h.eps > 0.0 && s.eps < 0x1p-126f) s.eps = 0x1p-126f;     // (second_moment takes its reciprocal)
     s.decay = (float)(lr * h.weight_decay);
     s.rate = (float)(lr / (1.0 - int_pow(h.beta1, t)));
     s.root = (float)(1.0 / sqrt(1.0 - int_pow(h.beta2, t)));
@@ -73,17 +76,43 @@ __device__ __forceinline__ AdamScalars scalars_of(const AdamCommon& c)
     return adam_scalars(c.h, lr, t < 1 ? 1 : t);
 }
 
-// One element:
+// N elements:
 //   m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,
 //   p' = p - lr wd p - lr/(1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
-// each line's sums fused, in this order.
-__device__ __forceinline__ void adam_element(const AdamScalars& s, float g, float& p, float& m, float& v)
+// each line's sums fused, in this order; the second moment and the quotient's
+// reciprocal first, then the first moment and the parameter.  Root and
+// reciprocal are the hardware's, each within 1 ulp (correctly rounded ones take
+// 20 more instructions an element, of about 110 with FP8 moments).  The root
+// flushes subnormals: those are scaled, an even power of two, which is exact.
+template <int N>
+__device__ __forceinline__ void second_moment(const AdamScalars& s, const float* g, float* v, float* reciprocal)
 {
 #pragma clang fp contract(off)
-    m = __builtin_fmaf(s.b1, m, s.c1 * g);
-    v = __builtin_fmaf(s.b2, v, s.c2 * g * g);
-    const float d = __builtin_fmaf(__builtin_sqrtf(v), s.root, s.eps);
-    p = __builtin_fmaf(-s.rate, m / d, __builtin_fmaf(-s.decay, p, p));
+    uint32_t least = ~0u;               // over bits - 1: below 2^23 - 1 for a subnormal, large for 0
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        v[i] = __builtin_fmaf(s.b2, v[i], s.c2 * g[i] * g[i]);
+        least = min(least, __float_as_uint(v[i]) - 1u);
+        reciprocal[i] = __builtin_amdgcn_sqrtf(v[i]);
+    }
+    if (least < 0x007FFFFFu) {
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (v[i] < 0x1p-126f) reciprocal[i] = __builtin_amdgcn_sqrtf(v[i] * 0x1p64f) * 0x1p-32f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) reciprocal[i] = __builtin_amdgcn_rcpf(__builtin_fmaf(reciprocal[i], s.root, s.eps));
+}
+
+template <int N>
+__device__ __forceinline__ void first_moment(const AdamScalars& s, const float* g, const float* reciprocal, float* p, float* m)
+{
+#pragma clang fp contract(off)
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        m[i] = __builtin_fmaf(s.b1, m[i], s.c1 * g[i]);
+        p[i] = __builtin_fmaf(-s.rate, m[i] * reciprocal[i], __builtin_fmaf(-s.decay, p[i], p[i]));
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -118,15 +147,15 @@ typedef Table<Adam8, 26> Table8;
 static_assert(sizeof(Table32) + sizeof(AdamCommon) <= 4096 && sizeof(Table8) + sizeof(AdamCommon) <= 4096,
               "a kernel's arguments are at most 4 KiB");
 
-// the tensor that chunk `c` belongs to
+// the tensor that chunk `c` belongs to: each lane looks at one tensor (a search
+// would read the arguments several times, one after the other)
 template <typename T>
 __device__ __forceinline__ int tensor_of(const T& table, int c)
 {
-    int t = 0;
-#pragma unroll
-    for (int step = 32; step > 0; step >>= 1)
-        if (t + step < table.count && table.first[t + step] <= c) t += step;
-    return __builtin_amdgcn_readfirstlane(t);
+    static_assert(T::most <= 64, "a lane each");
+    const int lane = threadIdx.x & 63;
+    const bool before = lane < table.count && table.first[min(lane, T::most - 1)] <= c;
+    return __builtin_popcountll(__ballot(before)) - 1;
 }
 
 // four consecutive elements, or those of them before n
@@ -146,7 +175,7 @@ __device__ __forceinline__ void load4(const void* base, int64_t at, int64_t n, f
 template <int SRC>
 __device__ __forceinline__ void store4(void* base, int64_t at, int64_t n, const float (&v)[4])
 {
-    if (at + 4 <= n) {
+    if (at <= n - 4) {
         Chunk<SRC, 4> c;
         if constexpr (SRC == SRC_F32) {
 #pragma unroll
@@ -178,30 +207,34 @@ __device__ __forceinline__ void store4(int src, void* base, int64_t at, int64_t 
 // ---------------------------------------------------------------------------
 // moments in fp32
 // ---------------------------------------------------------------------------
-template <int PS, int GS>
+template <int PS, int GS, int U>
 __global__ __launch_bounds__(256) void k_adamw32(const Table32 table, const AdamCommon c)
 {
     const int ti = tensor_of(table, (int)blockIdx.x);
     const Adam32& t = table.t[ti];
-    const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - table.first[ti]) * CHUNK + 4 * threadIdx.x;
+    const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - table.first[ti]) * (1024 * U) + 4 * threadIdx.x;
     const float scale = c.scale ? *c.scale : 1.0f;
-    const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
-    const AdamScalars s = scalars_of(c);
-    float p[4][4], g[4][4], m[4][4], v[4][4];
+    float p[U][4], g[U][4], m[U][4], v[U][4];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
+    for (int u = 0; u < U; u++) {
         const int64_t at = base + 1024 * u;
         load4<PS>(t.p, at, n, p[u]);
         load4<GS>(t.g, at, n, g[u]);
         load4<SRC_F32>(t.m, at, n, m[u]);
         load4<SRC_F32>(t.v, at, n, v[u]);
     }
+    const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
+    const AdamScalars s = scalars_of(c);
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
+    for (int u = 0; u < U; u++) {
         const int64_t at = base + 1024 * u;
-        if (!skip)
+        if (!skip) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) adam_element(s, g[u][i] * scale, p[u][i], m[u][i], v[u][i]);
+            for (int i = 0; i < 4; i++) g[u][i] *= scale;
+            float r[4];
+            second_moment<4>(s, g[u], v[u], r);
+            first_moment<4>(s, g[u], r, p[u], m[u]);
+        }
         store4<PS>(t.po, at, n, p[u]);
         store4<SRC_F32>(t.mo, at, n, m[u]);
         store4<SRC_F32>(t.vo, at, n, v[u]);
@@ -217,7 +250,7 @@ __global__ __launch_bounds__(256) void k_adamw32(const Table32 table, const Adam
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t load_codes(const uint8_t* q, int64_t at, int64_t n)
 {
-    if (at + 4 <= n) return *(const uint32_t*)(q + at);
+    if (at <= n - 4) return *(const uint32_t*)(q + at);
     uint32_t w = 0;
     for (int i = 0; i < 4; i++)
         if (at + i < n) w |= (uint32_t)q[at + i] << (8 * i);
@@ -226,7 +259,7 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* q, int64_t at, int
 
 __device__ __forceinline__ void store_codes(uint8_t* q, int64_t at, int64_t n, uint32_t w)
 {
-    if (at + 4 <= n) {
+    if (at <= n - 4) {
         *(uint32_t*)(q + at) = w;
         return;
     }
@@ -234,60 +267,134 @@ __device__ __forceinline__ void store_codes(uint8_t* q, int64_t at, int64_t n, u
         if (at + i < n) q[at + i] = (uint8_t)(w >> (8 * i));
 }
 
-template <int FMT, int G>
-__global__ __launch_bounds__(256) void k_adamw8(const Table8 table, const AdamCommon c, int psrc, int gsrc)
+// four elements as they lie in memory, so that a load does not wait for the
+// conversion of the one before
+struct Raw4 { uint32_t w[4]; };
+
+template <bool WHOLE>
+__device__ __forceinline__ void load_raw(int src, const uint8_t* base, int64_t at, int64_t n, Raw4 (&r)[4], int stride)
 {
-    constexpr int T = G / 16;
+    if (src == SRC_F32) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float* x = (const float*)base + at + i * stride;
+            if (WHOLE || at + i * stride + 4 <= n) __builtin_memcpy(r[i].w, x, 16);
+            else
+#pragma unroll
+                for (int e = 0; e < 4; e++) r[i].w[e] = at + i * stride + e < n ? __float_as_uint(x[e]) : 0u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint16_t* x = (const uint16_t*)base + at + i * stride;
+            if (WHOLE || at + i * stride + 4 <= n) __builtin_memcpy(r[i].w, x, 8);
+            else
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    r[i].w[e] = (at + i * stride + 2 * e < n ? (uint32_t)x[2 * e] : 0u) |
+                                (at + i * stride + 2 * e + 1 < n ? (uint32_t)x[2 * e + 1] << 16 : 0u);
+        }
+    }
+}
+
+__device__ __forceinline__ void raw_values(int src, const Raw4 (&r)[4], float (&v)[16])
+{
+    if (src == SRC_F32) {
+#pragma unroll
+        for (int e = 0; e < 16; e++) v[e] = __uint_as_float(r[e / 4].w[e % 4]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+            const uint32_t w = r[e / 4].w[e % 4 / 2];
+            v[e] = e % 2 ? bf16_hi(w) : bf16_lo(w);
+        }
+    }
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void store_values(int src, uint8_t* base, int64_t at, int64_t n, const float (&v)[16], int stride)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float x[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        store4(src, base, at + i * stride, WHOLE ? INT64_MAX : n, x);
+    }
+}
+
+// one chunk of a workgroup; WHOLE: all of it lies inside the tensor
+template <int FMT, int G, bool WHOLE>
+__device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c, const float (&lg)[128], int64_t chunk, int psrc,
+                                             int gsrc)
+{
+    constexpr int T = G / 16, STRIDE = 4 * T;
+    const int64_t n = t.n, group = chunk / G + threadIdx.x / T;
+    const int j = threadIdx.x % T;
+    const bool live = WHOLE || group * G < n;    // lanes of groups past the end run along with zeros
+    const int64_t at = group * G + 4 * j;        // the lane's words lie STRIDE elements apart
+    Raw4 rp[4], rg[4];
+    uint32_t qm[4], qv[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        qm[i] = load_codes(t.m, at + i * STRIDE, WHOLE ? INT64_MAX : n);
+        qv[i] = load_codes(t.v, at + i * STRIDE, WHOLE ? INT64_MAX : n);
+    }
+    float ma = 1.0f, mk = 1.0f, va = 1.0f, vk = 1.0f;
+    if (live) ma = t.ma[group], mk = t.mk[group], va = t.va[group], vk = t.vk[group];
+    load_raw<WHOLE>(gsrc, t.g, at, n, rg, STRIDE);
+    load_raw<WHOLE>(psrc, t.p, at, n, rp, STRIDE);
+    const float scale = c.scale ? *c.scale : 1.0f;
+    const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
+    float p[16];
+    if (!skip) {
+        const AdamScalars s = scalars_of(c);
+        // what lies past the end must not reach a group's extrema
+        auto cut = [&](float (&x)[16]) __attribute__((always_inline)) {
+            if (!WHOLE && at + 3 * STRIDE + 4 > n)
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    if (at + i / 4 * STRIDE + i % 4 >= n) x[i] = 0.0f;
+        };
+        float g[16], x[16], r[16];
+        raw_values(gsrc, rg, g);
+#pragma unroll
+        for (int i = 0; i < 16; i++) g[i] *= scale;
+        decode_state<FMT, 16>(qv, lg, va, vk, x);
+        second_moment<16>(s, g, x, r);
+        cut(x);
+        encode_state<FMT, T, 16>(x, qv, va, vk);
+        decode_state<FMT, 16>(qm, lg, ma, mk, x);
+        raw_values(psrc, rp, p);
+        first_moment<16>(s, g, r, p, x);
+        cut(x);
+        encode_state<FMT, T, 16>(x, qm, ma, mk);
+    } else {
+        raw_values(psrc, rp, p);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        store_codes(t.mo, at + i * STRIDE, WHOLE ? INT64_MAX : n, qm[i]);
+        store_codes(t.vo, at + i * STRIDE, WHOLE ? INT64_MAX : n, qv[i]);
+    }
+    store_values<WHOLE>(psrc, t.po, at, n, p, STRIDE);
+    if (t.copy) store_values<WHOLE>(SRC_BF16, (uint8_t*)t.copy, at, n, p, STRIDE);
+    if (live && j == 0) {
+        t.mao[group] = ma; t.mko[group] = mk;
+        t.vao[group] = va; t.vko[group] = vk;
+    }
+}
+
+template <int FMT, int G>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3)))
+void k_adamw8(const Table8 table, const AdamCommon c, int psrc, int gsrc)
+{
     __shared__ float lg[128];
     fill_log_table<FMT>(lg);
     __syncthreads();
     const int ti = tensor_of(table, (int)blockIdx.x);
     const Adam8& t = table.t[ti];
-    const int64_t n = t.n, chunk = (int64_t)((int)blockIdx.x - table.first[ti]) * CHUNK;
-    const int64_t group = chunk / G + threadIdx.x / T;
-    const int j = threadIdx.x % T;
-    const bool live = group * G < n;    // lanes of groups past the end run along with zeros
-    auto at = [&](int i) { return group * G + 4 * (j + i * T); };
-
-    const float scale = c.scale ? *c.scale : 1.0f;
-    const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
-    uint32_t qm[4], qv[4];
-    float p[4][4], g[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        qm[i] = load_codes(t.m, at(i), n);
-        qv[i] = load_codes(t.v, at(i), n);
-        load4(psrc, t.p, at(i), n, p[i]);
-        load4(gsrc, t.g, at(i), n, g[i]);
-    }
-    float ma = 1.0f, mk = 1.0f, va = 1.0f, vk = 1.0f;
-    if (live) ma = t.ma[group], mk = t.mk[group], va = t.va[group], vk = t.vk[group];
-    if (!skip) {
-        const AdamScalars s = scalars_of(c);
-        float m[16], v[16];
-        decode_state<FMT, 16>(qm, lg, ma, mk, m);
-        decode_state<FMT, 16>(qv, lg, va, vk, v);
-#pragma unroll
-        for (int i = 0; i < 16; i++) adam_element(s, g[i / 4][i % 4] * scale, p[i / 4][i % 4], m[i], v[i]);
-        // what lies past the end must not reach the group's extrema
-        if (at(3) + 4 > n)
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                if (at(i / 4) + i % 4 >= n) m[i] = v[i] = 0.0f;
-        encode_state<FMT, T, 16>(m, qm, ma, mk);
-        encode_state<FMT, T, 16>(v, qv, va, vk);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        store_codes(t.mo, at(i), n, qm[i]);
-        store_codes(t.vo, at(i), n, qv[i]);
-        store4(psrc, t.po, at(i), n, p[i]);
-        if (t.copy) store4<SRC_BF16>(t.copy, at(i), n, p[i]);
-    }
-    if (live && j == 0) {
-        t.mao[group] = ma; t.mko[group] = mk;
-        t.vao[group] = va; t.vko[group] = vk;
-    }
+    const int64_t chunk = (int64_t)((int)blockIdx.x - table.first[ti]) * CHUNK;
+    if (chunk + CHUNK <= t.n) adamw8_chunk<FMT, G, true>(t, c, lg, chunk, psrc, gsrc);
+    else adamw8_chunk<FMT, G, false>(t, c, lg, chunk, psrc, gsrc);
 }
 
 // ---------------------------------------------------------------------------
@@ -438,13 +545,23 @@ void put8(Adam8& e, const mx_adamw_tensor& t)
     e.n = t.n;
 }
 
+template <int PS, int GS, int U>
+hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
+{
+    return walk<Table32>(j.tensors, j.count, 1024 * U, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
+        k_adamw32<PS, GS, U><<<chunks, 256, 0, s>>>(t, c);
+        return hipGetLastError();
+    });
+}
+
 template <int PS, int GS>
 hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
-    return walk<Table32>(j.tensors, j.count, CHUNK, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
-        k_adamw32<PS, GS><<<chunks, 256, 0, s>>>(t, c);
-        return hipGetLastError();
-    });
+    // few elements to a launch: more workgroups, each with less to wait for
+    int64_t n = 0;
+    for (int i = 0; i < j.count; i++) n += j.tensors[i].n;
+    const int64_t launches = (j.count + Table32::most - 1) / Table32::most;
+    return n < launches * (int64_t)SMALL_STEP ? run32<PS, GS, SMALL_CHUNK / 1024>(j, c, s) : run32<PS, GS, CHUNK / 1024>(j, c, s);
 }
 
 template <int FMT, int G>

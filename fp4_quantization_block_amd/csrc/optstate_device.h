@@ -127,6 +127,14 @@ __device__ __forceinline__ void fill_log_table(float (&lg)[128])
                        : is_nan8<FMT>((uint32_t)c) ? 0.0f : log2_fixed(fabsf(decode8<FMT>((uint32_t)c)) / Fmt<FMT>::fmax);
 }
 
+// whether a word of four codes holds one that is not a finite number
+template <int FMT>
+__device__ __forceinline__ bool any_nonfinite8(uint32_t w)
+{
+    constexpr uint32_t up = FMT == E4M3 ? 0x01010101u : 0x04040404u;   // 0x80 less the first such magnitude
+    return (((w & 0x7F7F7F7Fu) + up) & 0x80808080u) != 0;
+}
+
 // E = 4 NV values of one group from their code words
 template <int FMT, int E>
 __device__ __forceinline__ void decode_state(const uint32_t (&c4)[E / 4], const float (&lg)[128], float amax, float k,
@@ -135,28 +143,33 @@ __device__ __forceinline__ void decode_state(const uint32_t (&c4)[E / 4], const 
 #pragma clang fp contract(off)
     const float kinv = 1.0f / k;
     const bool nan_group = amax != amax || k != k;
-    // the table reads first, then arithmetic without branches; a NaN
-    // output comes from adding NaN (others add -0, which changes nothing)
+    // the table reads first, then arithmetic without branches
     float l[E];
 #pragma unroll
     for (int e = 0; e < E; e++) l[e] = lg[(c4[e / 4] >> (8 * (e % 4))) & 0x7Fu];
-    auto run = [&](auto SIMPLE) __attribute__((always_inline)) {
-#pragma clang fp contract(off)
+    bool plain = kinv > 0.0f && kinv < __builtin_inff() && !nan_group;
+#pragma unroll
+    for (int i = 0; i < E / 4; i++) plain = plain && !any_nonfinite8<FMT>(c4[i]);
+    if (plain) {
+        // Every lg <= 0, so y <= 0 and not NaN.  The zero below y = -150 of the
+        // general form needs no select: 2^y of y < -150 is at most 2^-150,
+        // which rounds to zero (a tie, to even), as does 2^-151 for code 0.
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const float m = amax * exp2_core(fmaxf(kinv * l[e], -151.0f));
+            const uint32_t sign = (c4[e / 4] << (24 - 8 * (e % 4))) & 0x80000000u;
+            o[e] = __uint_as_float(__float_as_uint(m) ^ sign);
+        }
+    } else {
+        // a NaN output comes from adding NaN (others add -0, which changes nothing)
 #pragma unroll
         for (int e = 0; e < E; e++) {
             const uint32_t c = (c4[e / 4] >> (8 * (e % 4))) & 0xFFu, c7 = c & 0x7Fu;
-            const float y = kinv * l[e];
-            float p;
-            if constexpr (decltype(SIMPLE)::value) p = exp2_nonpos(y);    // 0 for code 0 (y = -Inf)
-            else p = c7 == 0 ? 0.0f : exp2_fixed(y);
+            const float p = c7 == 0 ? 0.0f : exp2_fixed(kinv * l[e]);
             const float m = amax * p + (is_nan8<FMT>(c7) || nan_group ? __builtin_nanf("") : -0.0f);
             o[e] = (c & 0x80u) ? -m : m;
         }
-    };
-    // E4M3 has no Inf code, so every non-NaN code has lg <= 0; with
-    // 0 < kinv < Inf every y is then at most 0 and not NaN
-    if (FMT == E4M3 && kinv > 0.0f && kinv < __builtin_inff()) run(std::true_type{});
-    else run(std::false_type{});
+    }
 }
 
 // Code words of E = 4 NV values of a group that T neighbouring lanes hold, and
@@ -219,33 +232,68 @@ __device__ __forceinline__ void encode_state(const float (&xs)[E], uint32_t (&co
         const float k = r > 1.0f ? Range<FMT>::log2r / log2_normal(r) : 1.0f;
         // k is finite and positive, and every quotient u = |x|/amax lies in
         // [0, 1], so y = k log2 u is finite and at most 0 for u > 0
-        float y[E];
         const TensorDiv d = make_div(amax);
         if (d.fast && ((kmin + 1u) << 1) - 1u >= d.lo_key) {
-            // every nonzero |x| of the group is at least amin, at or above the
+            // Every nonzero |x| of the group is at least amin, at or above the
             // division's threshold: the fast form gives the IEEE quotient
             // (+0 for x = 0, a normal number otherwise), and log2 needs no
-            // subnormal step.  Two steps of the general form are left out
+            // subnormal step.
+            auto quotient = [&](int e) __attribute__((always_inline)) {
+                const float q0 = a[e] * d.r;
+                return __builtin_fmaf(__builtin_fmaf(-q0, d.s, a[e]), d.r, q0);
+            };
+            // The fixed sequence.  Two steps of the general form are left out
             // because they cannot change a code: 2^y is at most 1 for y <= 0,
             // so |x|'s value stays within Fmax without the clamp; and below
             // y = -150, where the general form returns 0, the power is at most
             // 2^-149 and its product with Fmax far below the format's smallest
             // subnormal, so it rounds to a zero code (of x's sign) just as 0
             // does.
-#pragma unroll
-            for (int e = 0; e < E; e++) {
-                const float q0 = a[e] * d.r;
-                const float u = __builtin_fmaf(__builtin_fmaf(-q0, d.s, a[e]), d.r, q0);
+            auto fixed = [&](int e) __attribute__((always_inline)) {
+#pragma clang fp contract(off)
+                const float u = quotient(e);
                 const float p = exp2_core(fmaxf(k * log2_normal(u), -151.0f));
-                y[e] = __builtin_copysignf((u == 0.0f ? 0.0f : p) * Fmt<FMT>::fmax, xs[e]);
+                return __builtin_copysignf((u == 0.0f ? 0.0f : p) * Fmt<FMT>::fmax, xs[e]);
+            };
+            // Its codes without it, nearly always: the hardware's log2 and exp2
+            // give the power within a known factor 1 +- EPS of the fixed
+            // sequence's, and where both ends of that interval round to the
+            // same code, rounding being monotone, so does what lies between.
+            // Against the fixed sequences the hardware's log2 is off by at most
+            // 4 units of 2^-24 of the result for arguments from 2^-125 to 1,
+            // its exp2 by 2 from -40 to 0 (every argument compared).  Two more
+            // units of y = k log2 u are its roundings, so y differs by 6 2^-24
+            // |y| with |y| < 17.9 (E4M3) or 31.9 (E5M2), 2^y by ln 2 times that
+            // plus 2 units, and the products with Fmax by 2: 79 units, 137.
+            // (13 issue slots an element instead of 32; one word of four codes
+            // in about 1400 has a value that near a border and takes the fixed
+            // sequence.  117M elements: XX us.)
+            constexpr float EPS = FMT == E4M3 ? 0x1p-17f : 0x1p-16f;       // 128 and 256 units
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                float lo[4], hi[4];
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const int e = 4 * i + c;
+                    // (0 for u = 0: 2^-Inf)
+                    const float p = __builtin_copysignf(__builtin_amdgcn_exp2f(k * __builtin_amdgcn_logf(quotient(e))), xs[e]);
+                    lo[c] = p * (Fmt<FMT>::fmax * (1.0f - EPS));
+                    hi[c] = p * (Fmt<FMT>::fmax * (1.0f + EPS));
+                }
+                codes[i] = cvt4_fp8<FMT>(lo[0], lo[1], lo[2], lo[3]);
+                if (codes[i] != cvt4_fp8<FMT>(hi[0], hi[1], hi[2], hi[3]))
+                    codes[i] = cvt4_fp8<FMT>(fixed(4 * i), fixed(4 * i + 1), fixed(4 * i + 2), fixed(4 * i + 3));
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < E; e++)
-                y[e] = clamp_fmax<FMT>(__builtin_copysignf(pow_fixed(a[e] / amax, k) * Fmt<FMT>::fmax, xs[e]));
-        }
+            for (int i = 0; i < NV; i++) {
+                float y[4];
 #pragma unroll
-        for (int i = 0; i < NV; i++) codes[i] = cvt4_fp8<FMT>(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                for (int c = 0; c < 4; c++)
+                    y[c] = clamp_fmax<FMT>(__builtin_copysignf(pow_fixed(a[4 * i + c] / amax, k) * Fmt<FMT>::fmax, xs[4 * i + c]));
+                codes[i] = cvt4_fp8<FMT>(y[0], y[1], y[2], y[3]);
+            }
+        }
         gamax = amax; gk = k;
     }
 }

@@ -50,10 +50,10 @@ def _exact(p, g, m, v, lr, step, betas, eps, weight_decay, scale=1.0):
     # m: beta1 and 1 - beta1 rounded, g scale, its product, the fused sum.  v: the same with g twice
     em = U * ((b1 * m).abs() + 3 * ((1 - b1) * g).abs() + m1.abs()) + TINY
     ev = U * (b2 * v + 6 * (1 - b2) * g * g + v1) + 4 * TINY
-    # sqrt: half of v's, and its own; root, eps and the fused sum: at most 6 U of d altogether where v is normal
-    ed = ev / (2 * v1.clamp(min=1e-300).sqrt()) / math.sqrt(1 - b2 ** step) + 3 * U * d
-    # the quotient, lr / (1 - b1^t), lr wd, the two fused sums
-    ep = U * (p.abs() * (1 + 2 * lr * weight_decay) + p1.abs()) + rate * (em / d + q.abs() * (ed / d + 3 * U)) + 2 * TINY
+    # sqrt: half of v's, and its own ulp (2 U); 1 / sqrt(1 - b2^t), eps and the fused sum: one U each
+    ed = ev / (2 * v1.clamp(min=1e-300).sqrt()) / math.sqrt(1 - b2 ** step) + 4 * U * d
+    # the reciprocal's ulp (2 U) and its product with m, lr / (1 - b1^t), lr wd, the two fused sums
+    ep = U * (p.abs() * (1 + 2 * lr * weight_decay) + p1.abs()) + rate * (em / d + q.abs() * (ed / d + 4 * U)) + 2 * TINY
     return p1, m1, v1, 1.01 * ep, 1.01 * em, 1.01 * ev
 
 
@@ -102,6 +102,22 @@ def test_hyperparameters(hyper):
     before = _clone(t)
     _run(*t, **hyper)
     _check(before, (t[0], t[2], t[3]), **hyper)
+
+
+def test_subnormal_and_huge_second_moments():
+    """Without eps the root of a subnormal second moment counts; one beyond fp32 stops the parameter."""
+    p, g, m, v = (torch.zeros(64, device=DEV) for _ in range(4))
+    p += 0.5
+    g[:32] = torch.logspace(-21, -17, 32)
+    m[:32] = 1e-20
+    g[40:] = 1e30
+    t = ([p], [g], [m], [v])
+    before = _clone(t)
+    _run(*t, eps=0.0, lr=1e-2)
+    assert torch.all(v[:24] < 2.0 ** -126) and torch.all(v[:32] > 0)
+    _check([[x[0][:32]] for x in before], [[x[0][:32]] for x in (t[0], t[2], t[3])], eps=0.0, lr=1e-2)
+    assert torch.all(torch.isnan(p[32:40]))                          # 0 / 0
+    assert torch.all(torch.isinf(v[40:])) and torch.all(p[40:] == float(torch.tensor(0.5, dtype=torch.float64) * (1 - 1e-3)))
 
 
 def test_first_step_from_zero_moments():
