@@ -630,73 +630,143 @@ __device__ __forceinline__ void store_nt16(void* p, uint4 v)
 // Output kinds of k_gemm_w4 beside fp32 (0), bf16 (1) and MX codes (2 E4M3, 3 E5M2)
 constexpr int GLU = 4;
 
-// OUT == GLU: the gated activation of a 32 x 64 slab of a wave's part, gate
-// and up staged as fp32 in the wave's LDS (rows of GLU_PITCH floats).  Eight
-// lanes take a row, eight consecutive elements each, so that the four lanes of
-// a 1x32 block are neighbours (encode_row_chunk) and a row's 64 elements leave
-// as one run.
-constexpr int GLU_PITCH = 68;
+// OUT == GLU: what becomes of one 32 x 32 tile of gate and up.  The weights are
+// the first operand of the matrix instruction there, so that a lane's 16
+// accumulators are 16 columns of one row, 8 (r / 4) + 4 h + r % 4, and the lane
+// 32 further on has the other 16 of the same 1x32 block: block maxima take one
+// exchange between the halves, and two more (of codes; by pairs of registers)
+// give each lane 16 consecutive columns to store.  No LDS is used.  (Staged
+// there as fp32 and read back along rows: XX us instead of XX at 8192 x 14336
+// with checkpoints.)
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b)
+{
+    auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);     // the high half of a with the low half of b
+    a = p[0];
+    b = p[1];
+}
+
+// 16 registers of four columns each to 16 consecutive columns: w dwords a group of four
+template <int W>
+__device__ __forceinline__ void to_run(uint32_t (&d)[4 * W])
+{
+#pragma unroll
+    for (int c = 0; c < W; c++) {
+        swap_halves(d[c], d[2 * W + c]);
+        swap_halves(d[W + c], d[3 * W + c]);
+    }
+    // groups 0, 2, 1, 3 are now consecutive
+#pragma unroll
+    for (int c = 0; c < W; c++) {
+        const uint32_t t = d[W + c];
+        d[W + c] = d[2 * W + c];
+        d[2 * W + c] = t;
+    }
+}
+
+// where a lane stores: row, first of its 16 columns, how many of them are there (0 for a row past the end)
+struct RunAt { int64_t m, f; int n; };
+
+__device__ __forceinline__ void store_run(bool f32, void* base, int64_t ld, const RunAt& r, const float (&v)[16])
+{
+    const int64_t at = r.m * ld + r.f;
+    if (f32) {
+        uint32_t d[16];
+#pragma unroll
+        for (int k = 0; k < 16; k++) d[k] = __float_as_uint(v[k]);
+        to_run<4>(d);
+        float* p = (float*)base + at;
+        if (r.n == 16) {
+            __builtin_memcpy(p, d, 64);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; k++)
+                if (k < r.n) p[k] = __uint_as_float(d[k]);
+        }
+    } else {
+        uint32_t d[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) d[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+        to_run<2>(d);
+        uint16_t* p = (uint16_t*)base + at;
+        if (r.n == 16) {
+            __builtin_memcpy(p, d, 32);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; k++)
+                if (k < r.n) p[k] = (uint16_t)(d[k / 2] >> (16 * (k % 2)));
+        }
+    }
+}
+
+// one block of a row copy (mx_quantize's encoding) from the two lanes that hold
+// it; the converters saturate (saturate_converters)
+__device__ __forceinline__ void store_block(int fmt, uint8_t* q, uint8_t* s, int64_t ld, const RunAt& r, int h, const float (&v)[16])
+{
+    uint32_t key = chunk_key<16>(v), other = key;
+    swap_halves(key, other);
+    key = max(key, other);
+    uint32_t d[4], byte;
+    if (fmt == E4M3) {
+        const BlockScale<E4M3> b(key);
+#pragma unroll
+        for (int k = 0; k < 4; k++) d[k] = encode4<E4M3, true>(b, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        byte = b.byte;
+    } else {
+        const BlockScale<E5M2> b(key);
+#pragma unroll
+        for (int k = 0; k < 4; k++) d[k] = encode4<E5M2, true>(b, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        byte = b.byte;
+    }
+    if (key >= NONFINITE) {
+        d[0] = d[1] = d[2] = d[3] = 0x7F7F7F7Fu;
+        byte = 0xFFu;
+    }
+    to_run<1>(d);
+    if (r.n > 0) {                                   // (all 16: F is a multiple of 32 here)
+        const int64_t at = r.m * ld + r.f;
+        *(uint4*)(q + at) = make_uint4(d[0], d[1], d[2], d[3]);
+        if (h == 0) s[at >> 5] = (uint8_t)byte;
+    }
+}
 
 template <int ACT>
-__device__ __forceinline__ void glu8(const float (&g)[8], const float (&u)[8], float (&h)[8])
+__device__ __forceinline__ void glu_tile(const GluArgs& a, const f16v& ga, const f16v& ua, float ag, float au, const RunAt& r, int h)
 {
+    float g[16], u[16], y[16];
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-        float a, d;
-        gate<ACT, false>(g[e], a, d);
-        h[e] = a * u[e];
+    for (int k = 0; k < 16; k++) {
+        g[k] = ga[k] * ag;
+        u[k] = ua[k] * au;
+        float d;
+        gate<ACT, false>(g[k], y[k], d);
+        y[k] *= u[k];
+    }
+    if (a.h) store_run(a.out_f32, a.h, a.ld_h, r, y);
+    if (a.gate) {
+        store_run(a.out_f32, a.gate, a.ld_gate, r, g);
+        store_run(a.out_f32, a.up, a.ld_up, r, u);
+    }
+    if (a.qh) store_block(a.h_fmt, a.qh, a.sh, a.N, r, h, y);
+    if (a.qgc) {
+        store_block(a.ckpt_fmt, a.qgc, a.sgc, a.N, r, h, g);
+        store_block(a.ckpt_fmt, a.quc, a.suc, a.N, r, h, u);
     }
 }
 
-__device__ __forceinline__ void store8(bool f32, void* base, int64_t at, int n, const float (&v)[8])
+// a wave's 128 rows x 64 columns from m0, f0 on
+template <int ACT>
+__device__ __forceinline__ void glu_part(const GluArgs& a, const f16v (&acc)[4][4], float ag, float au, int64_t m0, int64_t f0, int h, int l32)
 {
-    if (n >= 8) {
-        if (f32) store_chunk<SRC_F32>(base, at, make_chunk<SRC_F32>(v));
-        else store_chunk<SRC_BF16>(base, at, make_chunk<SRC_BF16>(v));
-    } else {
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-            if (e < n) {
-                if (f32) store_elem<SRC_F32>(base, at + e, v[e]);
-                else store_elem<SRC_BF16>(base, at + e, v[e]);
-            }
-    }
-}
-
-__device__ __forceinline__ void glu_slab(const GluArgs& a, const float* fg, const float* fu, int64_t m0, int64_t f0, int lane)
-{
-    const int64_t f = f0 + 8 * (lane & 7);
-    const int n = (int)min((int64_t)8, a.N - f);             // elements of the row that are there (none: <= 0)
-#pragma unroll 1
-    for (int it = 0; it < 4; it++) {
-        const int row = 8 * it + (lane >> 3);
-        const int64_t m = m0 + row;
-        const int at = row * GLU_PITCH + 8 * (lane & 7);
-        float g[8], u[8], h[8];
+    for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-            const float4 x = *(const float4*)(fg + at + k), y = *(const float4*)(fu + at + k);
-            g[k] = x.x; g[k + 1] = x.y; g[k + 2] = x.z; g[k + 3] = x.w;
-            u[k] = y.x; u[k + 1] = y.y; u[k + 2] = y.z; u[k + 3] = y.w;
+        for (int j = 0; j < 2; j++) {
+            RunAt r;
+            r.m = m0 + 32 * i + l32;
+            r.f = f0 + 32 * j + 16 * h;
+            r.n = r.m < a.M ? (int)min(max(a.N - r.f, (int64_t)0), (int64_t)16) : 0;
+            glu_tile<ACT>(a, acc[i][j], acc[i][j + 2], ag, au, r, h);
         }
-        if (a.act == ACT_SILU) glu8<ACT_SILU>(g, u, h);
-        else if (a.act == ACT_GELU) glu8<ACT_GELU>(g, u, h);
-        else glu8<ACT_GELU_TANH>(g, u, h);
-        const bool valid = m < a.M && n > 0;
-        if (valid) {
-            if (a.h) store8(a.out_f32, a.h, m * a.ld_h + f, n, h);
-            if (a.gate) {
-                store8(a.out_f32, a.gate, m * a.ld_gate + f, n, g);
-                store8(a.out_f32, a.up, m * a.ld_up + f, n, u);
-            }
-        }
-        // (F is then a multiple of 32: the four lanes of a block are valid or not together)
-        if (a.qh) encode_row_chunk(a.h_fmt, h, valid, m * a.N + f, a.qh, a.sh);
-        if (a.qgc) {
-            encode_row_chunk(a.ckpt_fmt, g, valid, m * a.N + f, a.qgc, a.sgc);
-            encode_row_chunk(a.ckpt_fmt, u, valid, m * a.N + f, a.quc, a.suc);
-        }
-    }
 }
 
 // NB: tile columns (256, or 128 for the half tiles of a last partial round:
@@ -867,7 +937,14 @@ void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
 
     auto mma = [&](const Frag& f, int ks, int m) __attribute__((always_inline)) {
         const int i = m / JT, j = m % JT;
-        if ((ks & 1) == 0)
+        if constexpr (OUT == GLU) {                  // the weights first: see glu_tile
+            if ((ks & 1) == 0)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mfma_src<FP4>(f.b[j]), mfma_src<FP4>(f.a[i]), acc[i][j],
+                                                                            MfmaFmt<FB>::code, MfmaFmt<FA>::code, 0, (int)f.sb[j], 0, (int)f.sa[i]);
+            else
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mfma_src<FP4>(f.b[j]), mfma_src<FP4>(f.a[i]), acc[i][j],
+                                                                            MfmaFmt<FB>::code, MfmaFmt<FA>::code, 2, (int)f.sb[j], 2, (int)f.sa[i]);
+        } else if ((ks & 1) == 0)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mfma_src<FP4>(f.a[i]), mfma_src<FP4>(f.b[j]), acc[i][j],
                                                                         MfmaFmt<FA>::code, MfmaFmt<FB>::code, 0, (int)f.sa[i], 0, (int)f.sb[j]);
         else
@@ -1048,33 +1125,11 @@ void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
         if (g.tb) ag = ag * *g.tb;
         if (g.tu) au = au * *g.tu;
         if (g.hadamard_k) ag = ag * 0.03125f, au = au * 0.03125f;
-        uint8_t* buf = wave == 0 ? lA0 : wave == 1 ? lA1 : wave == 2 ? lB0 : lB1;
-        float* fg = (float*)buf;
-        float* fu = fg + 32 * GLU_PITCH;
-        auto put = [&](auto IC) __attribute__((always_inline)) {
-            constexpr int i = decltype(IC)::value;
-#pragma unroll
-            for (int j = 0; j < 2; j++)
-#pragma unroll
-                for (int r = 0; r < 16; r++) {
-                    const int at = (8 * (r / 4) + 4 * h + (r % 4)) * GLU_PITCH + j * 32 + l32;
-                    fg[at] = acc[i][j][r] * ag;
-                    fu[at] = acc[i][j + 2][r] * au;
-                }
-        };
-        // one copy of the slab's code, run four times: the code is fetched cold
-#pragma unroll 1
-        for (int i = 0; i < 4; i++) {
-            if (i == 0) put(std::integral_constant<int, 0>{});
-            else if (i == 1) put(std::integral_constant<int, 1>{});
-            else if (i == 2) put(std::integral_constant<int, 2>{});
-            else put(std::integral_constant<int, 3>{});
-            __builtin_amdgcn_s_waitcnt(0);
-            __builtin_amdgcn_wave_barrier();
-            glu_slab(g, fg, fu, m0 + wm * 128 + i * 32, n0 + wn * 64, lane);
-            __builtin_amdgcn_s_waitcnt(0);
-            __builtin_amdgcn_wave_barrier();
-        }
+        saturate_converters();
+        const int64_t mw = m0 + wm * 128, fw = n0 + wn * 64;
+        if (g.act == ACT_SILU) glu_part<ACT_SILU>(g, acc, ag, au, mw, fw, h, l32);
+        else if (g.act == ACT_GELU) glu_part<ACT_GELU>(g, acc, ag, au, mw, fw, h, l32);
+        else glu_part<ACT_GELU_TANH>(g, acc, ag, au, mw, fw, h, l32);
     } else if constexpr (OUT >= 2) {
         // MX-quantized output (OUT 2: E4M3, 3: E5M2), 1x32 blocks along the
         // rows of C.  Each wave stages a 32-row slab of its quarter as fp32
