@@ -151,10 +151,16 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
         for (int p = 0; p < 4; p++)
             x.q[p] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, at + p * run, u * UNIT, 0));
     };
-    auto load = [&](Stage& s, int u) __attribute__((always_inline)) {
-        load_codes(s.g, rg, voff, u);
-        load_codes(s.u, ru, voff, u);
-        load_codes(s.t, rt, voff, u);
+    constexpr uint32_t OUTSIDE = 0xF0000000u;       // past every tile's rows, whatever run is added
+    const int n = (units - wave + WAVES - 1) / WAVES;                 // units wave, wave + WAVES, ... of this wave
+    // unit i of the wave; one behind its last is not fetched (and not used), so
+    // that no load is conditional
+    auto load = [&](Stage& s, int i) __attribute__((always_inline)) {
+        const int u = wave + min(i, n - 1) * WAVES;
+        const uint32_t off = i < n ? voff : OUTSIDE;
+        load_codes(s.g, rg, off, u);
+        load_codes(s.u, ru, off, u);
+        load_codes(s.t, rt, off, u);
         const int64_t at = (int64_t)u * UBLOCKS;
         __builtin_memcpy(s.g.s, sg + at, sizeof s.g.s);              // (at any address)
         __builtin_memcpy(s.u.s, su + at, sizeof s.u.s);
@@ -190,34 +196,31 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
         put(s.t, mine + 2 * TILE);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
-    // one unit: to LDS, its registers free for unit u, its products
-    auto step = [&](Stage& s, int u) __attribute__((always_inline)) {
+    // one unit: to LDS, its registers free for unit i, its products
+    auto step = [&](Stage& s, int i) __attribute__((always_inline)) {
         put_all(s);
         Stage scales;
         __builtin_memcpy(scales.g.s, s.g.s, sizeof s.g.s);
         __builtin_memcpy(scales.u.s, s.u.s, sizeof s.u.s);
         __builtin_memcpy(scales.t.s, s.t.s, sizeof s.t.s);
-        load(s, u);
+        load(s, i);
         multiply(scales);
     };
-    const int n = (units - wave + WAVES - 1) / WAVES;                 // units wave, wave + WAVES, ...
-    auto unit = [&](int i) __attribute__((always_inline)) { return wave + min(i, n - 1) * WAVES; };
-    // two units in flight; behind the last one it is loaded again, without use,
-    // so that no load is conditional
+    // two units in flight
     Stage a, b;
     if (n > 0) {
-        load(a, unit(0));
-        load(b, unit(1));
+        load(a, 0);
+        load(b, 1);
 #pragma unroll 1
         for (int i = 0; i < n; i += 2) {
-            step(a, unit(i + 2));
-            if (i + 1 < n) step(b, unit(i + 3));
+            step(a, i + 2);
+            if (i + 1 < n) step(b, i + 3);
         }
     }
     // what is left of K behind the whole units: chunks past its end are fetched
     // from past every row's end, which gives zeros, with the scale 1
     if (rest != 0 && wave == units % WAVES) {
-        const uint32_t at = (lane & 7) * 16 < rest ? voff : 0xFFFFFFF0u - 4 * run;
+        const uint32_t at = (lane & 7) * 16 < rest ? voff : OUTSIDE;
         load_codes(a.g, rg, at, units);
         load_codes(a.u, ru, at, units);
         load_codes(a.t, rt, at, units);
