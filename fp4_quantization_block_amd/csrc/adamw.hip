@@ -24,7 +24,13 @@ namespace {
 
 constexpr int CHUNK = 4096;             // elements of a workgroup's chunk: 256 threads x 16
 constexpr int SMALL_CHUNK = 1024;       // of the step with fp32 moments where there are few: x 4
-constexpr int SMALL_STEP = 1 << 22;      // elements of a launch below which it takes small chunks
+constexpr int64_t SMALL_STEP = 1 << 22;  // elements of a launch below which it takes small chunks
+// With FP8 moments, the kernel for whole chunks alone holds 119 registers (four
+// waves a SIMD), the one that also takes a tensor's last, cut chunk 140 (three):
+// 564 against 600 us for 176M elements.  From so many elements on the cut chunks
+// go to a launch of their own (2^25 + 5 in one tensor: 121 against 128 us; 2^24 +
+// 5: 65 against 59, the second launch).
+constexpr int64_t SPLIT_STEP = 1 << 25;
 constexpr int MOST_CHUNKS = 1 << 23;    // of a launch (a launch counts its threads with 32 bits)
 
 // ---------------------------------------------------------------------------
@@ -88,14 +94,14 @@ template <int N>
 __device__ __forceinline__ void second_moment(const AdamScalars& s, const float* g, float* v, float* reciprocal)
 {
 #pragma clang fp contract(off)
-    uint32_t least = ~0u;               // over bits - 1: below 2^23 - 1 for a subnormal, large for 0
+    uint32_t least = ~0u;               // of the bits: below 2^23 for a subnormal, and for 0
 #pragma unroll
     for (int i = 0; i < N; i++) {
         v[i] = __builtin_fmaf(s.b2, v[i], s.c2 * g[i] * g[i]);
-        least = min(least, __float_as_uint(v[i]) - 1u);
+        least = min(least, __float_as_uint(v[i]));
         reciprocal[i] = __builtin_amdgcn_sqrtf(v[i]);
     }
-    if (least < 0x007FFFFFu) {
+    if (least < 0x00800000u) {
 #pragma unroll
         for (int i = 0; i < N; i++)
             if (v[i] < 0x1p-126f) reciprocal[i] = __builtin_amdgcn_sqrtf(v[i] * 0x1p64f) * 0x1p-32f;
@@ -248,51 +254,45 @@ __global__ __launch_bounds__(256) void k_adamw32(const Table32 table, const Adam
 // the tensor's end cuts short is completed with zeros, which change neither
 // its largest nor its smallest nonzero magnitude; their codes are not written.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* q, int64_t at, int64_t n)
+// In what follows `at` counts from the chunk's first element, `here` how many of
+// its elements there are; the pointers are the chunk's (uniform), so that a
+// lane's addresses are 32-bit offsets.
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* q, int at, int here)
 {
-    if (at <= n - 4) return *(const uint32_t*)(q + at);
+    if (at + 4 <= here) return *(const uint32_t*)(q + (uint32_t)at);
     uint32_t w = 0;
     for (int i = 0; i < 4; i++)
-        if (at + i < n) w |= (uint32_t)q[at + i] << (8 * i);
+        if (at + i < here) w |= (uint32_t)q[(uint32_t)(at + i)] << (8 * i);
     return w;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* q, int64_t at, int64_t n, uint32_t w)
+__device__ __forceinline__ void store_codes(uint8_t* q, int at, int here, uint32_t w)
 {
-    if (at <= n - 4) {
-        *(uint32_t*)(q + at) = w;
+    if (at + 4 <= here) {
+        *(uint32_t*)(q + (uint32_t)at) = w;
         return;
     }
     for (int i = 0; i < 4; i++)
-        if (at + i < n) q[at + i] = (uint8_t)(w >> (8 * i));
+        if (at + i < here) q[(uint32_t)(at + i)] = (uint8_t)(w >> (8 * i));
 }
 
 // four elements as they lie in memory, so that a load does not wait for the
 // conversion of the one before
 struct Raw4 { uint32_t w[4]; };
 
-template <bool WHOLE>
-__device__ __forceinline__ void load_raw(int src, const uint8_t* base, int64_t at, int64_t n, Raw4 (&r)[4], int stride)
+template <typename E>
+__device__ __forceinline__ void load_raw(const E* x, int at, int here, int stride, Raw4 (&r)[4])
 {
-    if (src == SRC_F32) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float* x = (const float*)base + at + i * stride;
-            if (WHOLE || at + i * stride + 4 <= n) __builtin_memcpy(r[i].w, x, 16);
-            else
+    for (int i = 0; i < 4; i++) {
+        const int k = at + i * stride;
+        if (k + 4 <= here) {
+            __builtin_memcpy(r[i].w, x + (uint32_t)k, 4 * sizeof(E));
+        } else {
+            E e[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++) r[i].w[e] = at + i * stride + e < n ? __float_as_uint(x[e]) : 0u;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint16_t* x = (const uint16_t*)base + at + i * stride;
-            if (WHOLE || at + i * stride + 4 <= n) __builtin_memcpy(r[i].w, x, 8);
-            else
-#pragma unroll
-                for (int e = 0; e < 2; e++)
-                    r[i].w[e] = (at + i * stride + 2 * e < n ? (uint32_t)x[2 * e] : 0u) |
-                                (at + i * stride + 2 * e + 1 < n ? (uint32_t)x[2 * e + 1] << 16 : 0u);
+            for (int j = 0; j < 4; j++) e[j] = k + j < here ? x[(uint32_t)(k + j)] : E{};
+            __builtin_memcpy(r[i].w, e, sizeof e);
         }
     }
 }
@@ -311,37 +311,34 @@ __device__ __forceinline__ void raw_values(int src, const Raw4 (&r)[4], float (&
     }
 }
 
-template <bool WHOLE>
-__device__ __forceinline__ void store_values(int src, uint8_t* base, int64_t at, int64_t n, const float (&v)[16], int stride)
-{
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float x[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-        store4(src, base, at + i * stride, WHOLE ? INT64_MAX : n, x);
-    }
-}
-
-// one chunk of a workgroup; WHOLE: all of it lies inside the tensor
+// One chunk of a workgroup; WHOLE: all of it lies inside the tensor.  The second
+// moment is done with before the first is begun, which holds fewer registers.
 template <int FMT, int G, bool WHOLE>
-__device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c, const float (&lg)[128], int64_t chunk, int psrc,
+__device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c, const float (&lg)[256], int64_t chunk, int psrc,
                                              int gsrc)
 {
-    constexpr int T = G / 16, STRIDE = 4 * T;
-    const int64_t n = t.n, group = chunk / G + threadIdx.x / T;
-    const int j = threadIdx.x % T;
-    const bool live = WHOLE || group * G < n;    // lanes of groups past the end run along with zeros
-    const int64_t at = group * G + 4 * j;        // the lane's words lie STRIDE elements apart
+    constexpr int T = G / 16, STRIDE = 4 * T;    // the lane's words lie STRIDE elements apart
+    const int here = WHOLE ? CHUNK : (int)(t.n - chunk);
+    const uint32_t group = threadIdx.x / T;
+    const int j = threadIdx.x % T, at = (int)group * G + 4 * j;
+    const bool live = WHOLE || (int)group * G < here;     // lanes of groups past the end run along with zeros
+    const int64_t groups = chunk / G;
     Raw4 rp[4], rg[4];
     uint32_t qm[4], qv[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        qm[i] = load_codes(t.m, at + i * STRIDE, WHOLE ? INT64_MAX : n);
-        qv[i] = load_codes(t.v, at + i * STRIDE, WHOLE ? INT64_MAX : n);
+        qm[i] = load_codes(t.m + chunk, at + i * STRIDE, here);
+        qv[i] = load_codes(t.v + chunk, at + i * STRIDE, here);
     }
     float ma = 1.0f, mk = 1.0f, va = 1.0f, vk = 1.0f;
-    if (live) ma = t.ma[group], mk = t.mk[group], va = t.va[group], vk = t.vk[group];
-    load_raw<WHOLE>(gsrc, t.g, at, n, rg, STRIDE);
-    load_raw<WHOLE>(psrc, t.p, at, n, rp, STRIDE);
+    if (live) {
+        ma = (t.ma + groups)[group]; mk = (t.mk + groups)[group];
+        va = (t.va + groups)[group]; vk = (t.vk + groups)[group];
+    }
+    if (gsrc == SRC_F32) load_raw((const float*)t.g + chunk, at, here, STRIDE, rg);
+    else load_raw((const uint16_t*)t.g + chunk, at, here, STRIDE, rg);
+    if (psrc == SRC_F32) load_raw((const float*)t.p + chunk, at, here, STRIDE, rp);
+    else load_raw((const uint16_t*)t.p + chunk, at, here, STRIDE, rp);
     const float scale = c.scale ? *c.scale : 1.0f;
     const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
     float p[16];
@@ -349,19 +346,19 @@ __device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c
         const AdamScalars s = scalars_of(c);
         // what lies past the end must not reach a group's extrema
         auto cut = [&](float (&x)[16]) __attribute__((always_inline)) {
-            if (!WHOLE && at + 3 * STRIDE + 4 > n)
+            if (!WHOLE)
 #pragma unroll
                 for (int i = 0; i < 16; i++)
-                    if (at + i / 4 * STRIDE + i % 4 >= n) x[i] = 0.0f;
+                    if (at + i / 4 * STRIDE + i % 4 >= here) x[i] = 0.0f;
         };
         float g[16], x[16], r[16];
         raw_values(gsrc, rg, g);
 #pragma unroll
         for (int i = 0; i < 16; i++) g[i] *= scale;
-        decode_state<FMT, 16>(qv, lg, va, vk, x);
+        decode_state<FMT, 16, false>(qv, lg, va, vk, x);
         second_moment<16>(s, g, x, r);
         cut(x);
-        encode_state<FMT, T, 16>(x, qv, va, vk);
+        encode_state<FMT, T, 16, false>(x, qv, va, vk);
         decode_state<FMT, 16>(qm, lg, ma, mk, x);
         raw_values(psrc, rp, p);
         first_moment<16>(s, g, r, p, x);
@@ -370,30 +367,39 @@ __device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c
     } else {
         raw_values(psrc, rp, p);
     }
+    auto store = [&](int src, uint8_t* to) __attribute__((always_inline)) {
+        to += chunk * (src == SRC_F32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float x[4] = {p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]};
+            store4(src, to, (uint32_t)(at + i * STRIDE), here, x);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        store_codes(t.mo, at + i * STRIDE, WHOLE ? INT64_MAX : n, qm[i]);
-        store_codes(t.vo, at + i * STRIDE, WHOLE ? INT64_MAX : n, qv[i]);
+        store_codes(t.mo + chunk, at + i * STRIDE, here, qm[i]);
+        store_codes(t.vo + chunk, at + i * STRIDE, here, qv[i]);
     }
-    store_values<WHOLE>(psrc, t.po, at, n, p, STRIDE);
-    if (t.copy) store_values<WHOLE>(SRC_BF16, (uint8_t*)t.copy, at, n, p, STRIDE);
+    store(psrc, t.po);
+    if (t.copy) store(SRC_BF16, (uint8_t*)t.copy);
     if (live && j == 0) {
-        t.mao[group] = ma; t.mko[group] = mk;
-        t.vao[group] = va; t.vko[group] = vk;
+        (t.mao + groups)[group] = ma; (t.mko + groups)[group] = mk;
+        (t.vao + groups)[group] = va; (t.vko + groups)[group] = vk;
     }
 }
 
-template <int FMT, int G>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3)))
+template <int FMT, int G, bool WHOLE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WHOLE ? 4 : 3, WHOLE ? 4 : 3)))
 void k_adamw8(const Table8 table, const AdamCommon c, int psrc, int gsrc)
 {
-    __shared__ float lg[128];
+    __shared__ float lg[256];
     fill_log_table<FMT>(lg);
     __syncthreads();
     const int ti = tensor_of(table, (int)blockIdx.x);
     const Adam8& t = table.t[ti];
     const int64_t chunk = (int64_t)((int)blockIdx.x - table.first[ti]) * CHUNK;
-    if (chunk + CHUNK <= t.n) adamw8_chunk<FMT, G, true>(t, c, lg, chunk, psrc, gsrc);
+    if constexpr (WHOLE) adamw8_chunk<FMT, G, true>(t, c, lg, chunk, psrc, gsrc);
+    else if (chunk + CHUNK <= t.n) adamw8_chunk<FMT, G, true>(t, c, lg, chunk, psrc, gsrc);
     else adamw8_chunk<FMT, G, false>(t, c, lg, chunk, psrc, gsrc);
 }
 
@@ -504,25 +510,28 @@ __global__ __launch_bounds__(256) void k_grad_norm_join(const double* partial, i
 }
 
 // ---------------------------------------------------------------------------
-// Walks the tensors of a call, filling tables: put(slot, tensor) fills one
-// slot, in chunks of so many elements; flush(table, chunks) launches a full table.  Empty tensors are passed over.
+// Walks the tensors of a call, filling tables: piece(i) is what tensor i has in
+// this walk, put(slot, piece) fills a table's slot, in chunks of so many
+// elements, flush(table, chunks) launches a full table.  Empty pieces are passed
+// over.
 // ---------------------------------------------------------------------------
-template <typename T, typename Entry, typename Put, typename Flush>
-hipError_t walk(const Entry* tensors, int count, int elements, int most_chunks, Put put, Flush flush)
+template <typename T, typename Piece, typename Put, typename Flush>
+hipError_t walk(int count, Piece piece, int elements, int most_chunks, Put put, Flush flush)
 {
     T table;
     int chunks = 0;
     table.count = 0;
     for (int i = 0; i < count; i++) {
-        if (tensors[i].n == 0) continue;
-        const int more = (int)((tensors[i].n + elements - 1) / elements);
+        const auto e = piece(i);
+        if (e.n == 0) continue;
+        const int more = (int)((e.n + elements - 1) / elements);
         if (table.count > 0 && (table.count == T::most || chunks > most_chunks - more)) {
-            const hipError_t e = flush(table, chunks);
-            if (e != hipSuccess) return e;
+            const hipError_t r = flush(table, chunks);
+            if (r != hipSuccess) return r;
             chunks = table.count = 0;
         }
         table.first[table.count] = chunks;
-        put(table.t[table.count++], tensors[i]);
+        put(table.t[table.count++], e);
         chunks += more;
     }
     return table.count > 0 ? flush(table, chunks) : hipSuccess;
@@ -545,32 +554,72 @@ void put8(Adam8& e, const mx_adamw_tensor& t)
     e.n = t.n;
 }
 
+// elements [from, from + n) of a tensor with FP8 moments; from is a multiple of
+// the group
+mx_adamw_tensor part_of(const mx_adamw_tensor& t, const AdamJob& j, int64_t from, int64_t n)
+{
+    mx_adamw_tensor e = t;
+    e.n = n;
+    if (n == 0 || from == 0) return e;
+    const int64_t pb = from * (j.psrc == SRC_F32 ? 4 : 2), gb = from * (j.gsrc == SRC_F32 ? 4 : 2), groups = from / j.group;
+    e.p = (const uint8_t*)t.p + pb;
+    e.p_out = (uint8_t*)t.p_out + pb;
+    e.g = (const uint8_t*)t.g + gb;
+    if (t.copy) e.copy = (uint8_t*)t.copy + 2 * from;
+    e.m = (const uint8_t*)t.m + from;
+    e.v = (const uint8_t*)t.v + from;
+    e.m_out = (uint8_t*)t.m_out + from;
+    e.v_out = (uint8_t*)t.v_out + from;
+    e.m_amax += groups; e.m_kexp += groups; e.v_amax += groups; e.v_kexp += groups;
+    e.m_amax_out += groups; e.m_kexp_out += groups; e.v_amax_out += groups; e.v_kexp_out += groups;
+    return e;
+}
+
 template <int PS, int GS, int U>
 hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
-    return walk<Table32>(j.tensors, j.count, 1024 * U, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
+    return walk<Table32>(j.count, [&](int i) { return j.tensors[i]; }, 1024 * U, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
         k_adamw32<PS, GS, U><<<chunks, 256, 0, s>>>(t, c);
         return hipGetLastError();
     });
+}
+
+int64_t elements_of(const AdamJob& j)
+{
+    int64_t n = 0;
+    for (int i = 0; i < j.count; i++) n += j.tensors[i].n;
+    return n;
 }
 
 template <int PS, int GS>
 hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
     // few elements to a launch: more workgroups, each with less to wait for
-    int64_t n = 0;
-    for (int i = 0; i < j.count; i++) n += j.tensors[i].n;
     const int64_t launches = (j.count + Table32::most - 1) / Table32::most;
-    return n < launches * (int64_t)SMALL_STEP ? run32<PS, GS, SMALL_CHUNK / 1024>(j, c, s) : run32<PS, GS, CHUNK / 1024>(j, c, s);
+    return elements_of(j) < launches * SMALL_STEP ? run32<PS, GS, SMALL_CHUNK / 1024>(j, c, s) : run32<PS, GS, CHUNK / 1024>(j, c, s);
+}
+
+template <int FMT, int G, bool WHOLE, typename Piece>
+hipError_t run8(const AdamJob& j, const AdamCommon& c, Piece piece, hipStream_t s)
+{
+    return walk<Table8>(j.count, piece, CHUNK, MOST_CHUNKS, put8, [&](const Table8& t, int chunks) {
+        k_adamw8<FMT, G, WHOLE><<<chunks, 256, 0, s>>>(t, c, j.psrc, j.gsrc);
+        return hipGetLastError();
+    });
 }
 
 template <int FMT, int G>
 hipError_t run8(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
-    return walk<Table8>(j.tensors, j.count, CHUNK, MOST_CHUNKS, put8, [&](const Table8& t, int chunks) {
-        k_adamw8<FMT, G><<<chunks, 256, 0, s>>>(t, c, j.psrc, j.gsrc);
-        return hipGetLastError();
-    });
+    bool cut = false;
+    for (int i = 0; i < j.count; i++) cut = cut || j.tensors[i].n % CHUNK != 0;
+    if (cut && elements_of(j) < SPLIT_STEP) return run8<FMT, G, false>(j, c, [&](int i) { return j.tensors[i]; }, s);
+    const hipError_t e = run8<FMT, G, true>(j, c, [&](int i) { return part_of(j.tensors[i], j, 0, j.tensors[i].n / CHUNK * CHUNK); }, s);
+    if (e != hipSuccess) return e;
+    return run8<FMT, G, false>(j, c, [&](int i) {
+        const int64_t whole = j.tensors[i].n / CHUNK * CHUNK;
+        return part_of(j.tensors[i], j, whole, j.tensors[i].n - whole);
+    }, s);
 }
 
 template <int FMT>
@@ -607,7 +656,7 @@ template <int SRC>
 hipError_t run_norm(const GradNormJob& j, int& partials, hipStream_t s)
 {
     return walk<NormTable>(
-        j.tensors, j.count, NormChunk<SRC>::elements, 1 << 30,
+        j.count, [&](int i) { return j.tensors[i]; }, NormChunk<SRC>::elements, 1 << 30,
         [](NormEntry& e, const mx_tensor& t) { e.x = (const uint8_t*)t.x; e.n = t.n; },
         [&](const NormTable& t, int chunks) {
             const int wgs = chunks < NORM_WGS ? chunks : NORM_WGS;

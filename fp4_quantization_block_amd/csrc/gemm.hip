@@ -636,8 +636,9 @@ constexpr int GLU = 4;
 // 32 further on has the other 16 of the same 1x32 block: block maxima take one
 // exchange between the halves, and two more (of codes; by pairs of registers)
 // give each lane 16 consecutive columns to store.  No LDS is used.  (Staged
-// there as fp32 and read back along rows: XX us instead of XX at 8192 x 14336
-// with checkpoints.)
+// there as fp32 and read back along rows: 959 us instead of 911 at 8192 x 4096 x
+// 14336 E4M3 with checkpoints, 876 instead of 842 without; mx_gemm of the same
+// products with bf16 output takes 863, and mx_glu_forward 146 or 103 more.)
 __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b)
 {
     auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);     // the high half of a with the low half of b

@@ -38,7 +38,8 @@ template <> struct MfmaFmt<E2M1> { static constexpr int code = 4; };
 // -> the lanes that multiply it.  A load instruction covers eight whole 128-byte
 // lines, eight lanes to a row.  (Loaded straight into the lane layout of the
 // matrix instruction, 16 bytes of 32 rows at a time, a line is asked for four
-// times: 37 us instead of XX for one token at 4096 x 14336 E4M3.)
+// times: 37 us instead of 31 for one token at 4096 x 14336 E4M3, 63 instead of
+// 34 for 32 tokens.)
 template <bool FP4>
 struct Unit {
     static constexpr int DWORDS = FP4 ? 2 : 1;       // scale dwords of a row

@@ -27,9 +27,13 @@
 // powers, far below an FP8 step.
 //
 // 4 bytes read and 1 written per element, 8 bytes of parameters per group;
-// the exact fp32 sequence makes the kernels bound by VALU work, so both
-// kernels are written to spend as few instructions per element as the
-// arithmetic allows while computing the same bits:
+// the exact fp32 sequence is much VALU work, so both kernels are written to
+// spend as few instructions per element as the arithmetic allows while
+// computing the same bits (the codes in optstate_device.h, which the AdamW step
+// shares):
+//  - the quantizer takes the powers from the hardware's log2 and exp2 where
+//    their error cannot change a code, which it checks, and evaluates the
+//    sequence only elsewhere;
 //  - log2 splits x into m and e with one integer subtraction of the bits of
 //    sqrt(1/2) (the exponent field drops by one exactly when the mantissa
 //    lies above sqrt(2)), and exp2 takes its special cases as selects, so
@@ -93,7 +97,7 @@ __global__ __launch_bounds__(256) void k_optstate_dequant(const uint32_t* __rest
 {
     constexpr int T = G / (4 * NV);
     static_assert(T >= 1 && (T & (T - 1)) == 0, "threads per group");
-    __shared__ float lg[128];
+    __shared__ float lg[256];
     fill_log_table<FMT>(lg);
     __syncthreads();
     const int64_t nthreads = ngroups * T;

@@ -113,18 +113,21 @@ __device__ __forceinline__ float decode8(uint32_t c)
 template <int FMT>
 __device__ __forceinline__ bool is_nan8(uint32_t c7) { return FMT == E4M3 ? c7 == 0x7Fu : c7 > 0x7Cu; }
 
-// log2(|decode(c)| / Fmax) for the 128 magnitudes, in the same fixed
-// sequence the per-element form evaluates; -Inf for code 0 (so that its
-// power is 0 whenever the exponent 1/k is positive) and 0 for the NaN
-// codes, whose output is NaN whatever the power.  Filled by a workgroup of
-// 256 threads, which then meets a barrier before it reads.
+// log2(|decode(c)| / Fmax) for the 256 codes (both signs, so that a code is
+// its own index), in the same fixed sequence the per-element form evaluates; 0
+// for the NaN codes, whose output is NaN whatever the power, and for the zeros
+// NO_POWER, whose power is 0 for every exponent that decode_state takes it at.
+// Filled by a workgroup of 256 threads, which then meets a barrier before it
+// reads.
+constexpr float NO_POWER = -4096.0f;
+
 template <int FMT>
-__device__ __forceinline__ void fill_log_table(float (&lg)[128])
+__device__ __forceinline__ void fill_log_table(float (&lg)[256])
 {
 #pragma clang fp contract(off)
-    for (int c = threadIdx.x; c < 128; c += 256)
-        lg[c] = c == 0 ? -__builtin_inff()
-                       : is_nan8<FMT>((uint32_t)c) ? 0.0f : log2_fixed(fabsf(decode8<FMT>((uint32_t)c)) / Fmt<FMT>::fmax);
+    const uint32_t c = threadIdx.x, c7 = c & 0x7Fu;
+    if (c < 256)
+        lg[c] = c7 == 0 ? NO_POWER : is_nan8<FMT>(c7) ? 0.0f : log2_fixed(fabsf(decode8<FMT>(c7)) / Fmt<FMT>::fmax);
 }
 
 // whether a word of four codes holds one that is not a finite number
@@ -135,9 +138,10 @@ __device__ __forceinline__ bool any_nonfinite8(uint32_t w)
     return (((w & 0x7F7F7F7Fu) + up) & 0x80808080u) != 0;
 }
 
-// E = 4 NV values of one group from their code words
-template <int FMT, int E>
-__device__ __forceinline__ void decode_state(const uint32_t (&c4)[E / 4], const float (&lg)[128], float amax, float k,
+// E = 4 NV values of one group from their code words.  SIGNED false: nearly
+// all values are positive (second moments); others are right, but slower.
+template <int FMT, int E, bool SIGNED = true>
+__device__ __forceinline__ void decode_state(const uint32_t (&c4)[E / 4], const float (&lg)[256], float amax, float k,
                                              float (&o)[E])
 {
 #pragma clang fp contract(off)
@@ -146,18 +150,23 @@ __device__ __forceinline__ void decode_state(const uint32_t (&c4)[E / 4], const 
     // the table reads first, then arithmetic without branches
     float l[E];
 #pragma unroll
-    for (int e = 0; e < E; e++) l[e] = lg[(c4[e / 4] >> (8 * (e % 4))) & 0x7Fu];
-    bool plain = kinv > 0.0f && kinv < __builtin_inff() && !nan_group;
+    for (int e = 0; e < E; e++) l[e] = lg[(c4[e / 4] >> (8 * (e % 4))) & 0xFFu];
+    // (2^-4 4096 = 256: the power of NO_POWER is 0)
+    bool plain = kinv >= 0x1p-4f && kinv < 0x1p16f && !nan_group;
 #pragma unroll
-    for (int i = 0; i < E / 4; i++) plain = plain && !any_nonfinite8<FMT>(c4[i]);
+    for (int i = 0; i < E / 4; i++) {
+        plain = plain && !any_nonfinite8<FMT>(c4[i]);
+        if constexpr (!SIGNED) plain = plain && (c4[i] & 0x80808080u) == 0;
+    }
     if (plain) {
-        // Every lg <= 0, so y <= 0 and not NaN.  The zero below y = -150 of the
-        // general form needs no select: 2^y of y < -150 is at most 2^-150,
-        // which rounds to zero (a tie, to even), as does 2^-151 for code 0.
+        // Every lg <= 0, so y <= 0 and not NaN, at least -2^28.  The zero below
+        // y = -150 of the general form needs no select, nor its bound at -151:
+        // 2^y of y < -150 is at most 2^-150, which rounds to zero (a tie, to
+        // even).
 #pragma unroll
         for (int e = 0; e < E; e++) {
-            const float m = amax * exp2_core(fmaxf(kinv * l[e], -151.0f));
-            const uint32_t sign = (c4[e / 4] << (24 - 8 * (e % 4))) & 0x80000000u;
+            const float m = amax * exp2_core(kinv * l[e]);
+            const uint32_t sign = SIGNED ? (c4[e / 4] << (24 - 8 * (e % 4))) & 0x80000000u : 0u;
             o[e] = __uint_as_float(__float_as_uint(m) ^ sign);
         }
     } else {
@@ -175,27 +184,45 @@ __device__ __forceinline__ void decode_state(const uint32_t (&c4)[E / 4], const 
 // Code words of E = 4 NV values of a group that T neighbouring lanes hold, and
 // the group's largest magnitude and exponent (in every lane).  All lanes of the
 // wave take part.  Zeros change neither extremum: lanes past the end of a
-// group that is not full pass zeros.
-template <int FMT, int T, int E>
+// group that is not full pass zeros.  SIGNED false: as in decode_state.
+template <int FMT, int T, int E, bool SIGNED = true>
 __device__ __forceinline__ void encode_state(const float (&xs)[E], uint32_t (&codes)[E / 4], float& gamax, float& gk)
 {
 #pragma clang fp contract(off)
     static_assert(T >= 1 && T <= 64 && (T & (T - 1)) == 0, "a group's threads lie inside one wave");
     constexpr int NV = E / 4;
-    float a[E];
     // group maximum and smallest nonzero magnitude as integer extrema of
     // |x|'s bits (their order is the values' for finite magnitudes; Inf
     // and NaN bits lie above every finite one, so they flag the group by
-    // themselves).  The minimum runs over bits - 1, which sends zeros to
-    // the top of the unsigned range.
-    uint32_t kmax = 0, kmin = ~0u;
+    // themselves, and so do signs that are not expected).  The minimum runs
+    // over bits - 1, which sends zeros to the top of the unsigned range; a
+    // thread that has none takes it over the bits.
+    uint32_t kmax, kmin;
+    if constexpr (SIGNED) {                      // (the sign goes as an operand's modifier; a NaN stays one)
+        float hi = __builtin_fabsf(xs[0]), lo = hi;
 #pragma unroll
-    for (int e = 0; e < E; e++) {
-        const uint32_t b = __float_as_uint(xs[e]) & 0x7FFFFFFFu;
-        a[e] = __uint_as_float(b);
-        kmax = max(kmax, b);
-        kmin = min(kmin, b - 1u);
+        for (int e = 1; e < E; e++) {
+            hi = __builtin_elementwise_maximum(hi, __builtin_fabsf(xs[e]));
+            lo = __builtin_elementwise_minimum(lo, __builtin_fabsf(xs[e]));
+        }
+        kmax = __float_as_uint(hi);
+        kmin = __float_as_uint(lo);
+    } else {
+        kmax = kmin = __float_as_uint(xs[0]);
+#pragma unroll
+        for (int e = 1; e < E; e++) {
+            kmax = max(kmax, __float_as_uint(xs[e]));
+            kmin = min(kmin, __float_as_uint(xs[e]));
+        }
     }
+    if (kmin == 0) {
+        kmin = ~0u;
+#pragma unroll
+        for (int e = 0; e < E; e++) kmin = min(kmin, (__float_as_uint(xs[e]) & 0x7FFFFFFFu) - 1u);
+    } else {
+        kmin--;
+    }
+    auto a = [&](int e) __attribute__((always_inline)) { return SIGNED ? __builtin_fabsf(xs[e]) : xs[e]; };
     // butterflies inside 32-lane halves by swizzle (xor mask in bits 14:10,
     // and mask 0x1F), across halves by a permute
     auto step = [&](auto OFFC) __attribute__((always_inline)) {
@@ -217,7 +244,9 @@ __device__ __forceinline__ void encode_state(const float (&xs)[E], uint32_t (&co
     const float amin = __uint_as_float(kmin + 1u);  // used only when some |x| > 0
     const bool bad = kmax >= 0x7F800000u;
     const float amax = __uint_as_float(kmax);
-    if (bad) {                                   // a NaN or Inf: the NaN code everywhere
+    if (!SIGNED && kmax > 0x80000000u) {         // (a group's lanes take this together)
+        encode_state<FMT, T, E, true>(xs, codes, gamax, gk);
+    } else if (bad) {                            // a NaN or Inf: the NaN code everywhere
 #pragma unroll
         for (int i = 0; i < NV; i++) codes[i] = 0x7F7F7F7Fu;
         gamax = __builtin_nanf(""); gk = __builtin_nanf("");
@@ -239,8 +268,8 @@ __device__ __forceinline__ void encode_state(const float (&xs)[E], uint32_t (&co
             // (+0 for x = 0, a normal number otherwise), and log2 needs no
             // subnormal step.
             auto quotient = [&](int e) __attribute__((always_inline)) {
-                const float q0 = a[e] * d.r;
-                return __builtin_fmaf(__builtin_fmaf(-q0, d.s, a[e]), d.r, q0);
+                const float q0 = a(e) * d.r;
+                return __builtin_fmaf(__builtin_fmaf(-q0, d.s, a(e)), d.r, q0);
             };
             // The fixed sequence.  Two steps of the general form are left out
             // because they cannot change a code: 2^y is at most 1 for y <= 0,
@@ -261,24 +290,26 @@ __device__ __forceinline__ void encode_state(const float (&xs)[E], uint32_t (&co
             // same code, rounding being monotone, so does what lies between.
             // Against the fixed sequences the hardware's log2 is off by at most
             // 4 units of 2^-24 of the result for arguments from 2^-125 to 1,
-            // its exp2 by 2 from -40 to 0 (every argument compared).  Two more
-            // units of y = k log2 u are its roundings, so y differs by 6 2^-24
-            // |y| with |y| < 17.9 (E4M3) or 31.9 (E5M2), 2^y by ln 2 times that
-            // plus 2 units, and the products with Fmax by 2: 79 units, 137.
-            // (13 issue slots an element instead of 32; one word of four codes
-            // in about 1400 has a value that near a border and takes the fixed
-            // sequence.  117M elements: XX us.)
+            // its exp2 by 2 from -40 to 0 (every argument compared).  With y =
+            // k log2 u, |y| < 17.9 (E4M3) or 31.9 (E5M2), the exponent y +
+            // log2 Fmax differs by 4 |y| units for the logarithm, |y| for the
+            // fixed sequence's product, and one half ulp of the sum and one of
+            // the constant, 8 units each (16 for E5M2): 105 or 191 units.  The
+            // power differs by ln 2 times that and 3 units: 76, 136.  (14 issue
+            // slots an element instead of 32; one word of four codes in about
+            // 1400 has a value that near a border and takes the fixed sequence.)
             constexpr float EPS = FMT == E4M3 ? 0x1p-17f : 0x1p-16f;       // 128 and 256 units
+            constexpr float LOG2E = 1.44269504f, LOW = (FMT == E4M3 ? 8.80735492f : 15.80735492f) - EPS * LOG2E;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 float lo[4], hi[4];
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                     const int e = 4 * i + c;
-                    // (0 for u = 0: 2^-Inf)
-                    const float p = __builtin_copysignf(__builtin_amdgcn_exp2f(k * __builtin_amdgcn_logf(quotient(e))), xs[e]);
-                    lo[c] = p * (Fmt<FMT>::fmax * (1.0f - EPS));
-                    hi[c] = p * (Fmt<FMT>::fmax * (1.0f + EPS));
+                    // the interval's lower end (0 for u = 0: 2^-Inf), and its upper one
+                    lo[c] = __builtin_amdgcn_exp2f(__builtin_fmaf(k, __builtin_amdgcn_logf(quotient(e)), LOW));
+                    if constexpr (SIGNED) lo[c] = __builtin_copysignf(lo[c], xs[e]);
+                    hi[c] = lo[c] * (1.0f + 2.0f * EPS);
                 }
                 codes[i] = cvt4_fp8<FMT>(lo[0], lo[1], lo[2], lo[3]);
                 if (codes[i] != cvt4_fp8<FMT>(hi[0], hi[1], hi[2], hi[3]))
@@ -290,7 +321,7 @@ __device__ __forceinline__ void encode_state(const float (&xs)[E], uint32_t (&co
                 float y[4];
 #pragma unroll
                 for (int c = 0; c < 4; c++)
-                    y[c] = clamp_fmax<FMT>(__builtin_copysignf(pow_fixed(a[4 * i + c] / amax, k) * Fmt<FMT>::fmax, xs[4 * i + c]));
+                    y[c] = clamp_fmax<FMT>(__builtin_copysignf(pow_fixed(a(4 * i + c) / amax, k) * Fmt<FMT>::fmax, xs[4 * i + c]));
                 codes[i] = cvt4_fp8<FMT>(y[0], y[1], y[2], y[3]);
             }
         }
