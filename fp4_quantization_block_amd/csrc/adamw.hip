@@ -126,9 +126,11 @@ __device__ __forceinline__ void first_moment(const AdamScalars& s, const float* 
 // ---------------------------------------------------------------------------
 struct Adam32 {
     const uint8_t* p; const uint8_t* g; const float* m; const float* v;
-    uint8_t* po; float* mo; float* vo; uint16_t* copy;
+    uint8_t* po; float* mo; float* vo;
     int64_t n;
 };
+
+struct Adam32Copy : Adam32 { uint16_t* copy; };
 
 struct Adam8 {
     const uint8_t* p; const uint8_t* g;
@@ -148,10 +150,11 @@ struct Table {
     int32_t count;
 };
 
-typedef Table<Adam32, 48> Table32;
-typedef Table<Adam8, 26> Table8;
-static_assert(sizeof(Table32) + sizeof(AdamCommon) <= 4096 && sizeof(Table8) + sizeof(AdamCommon) <= 4096,
-              "a kernel's arguments are at most 4 KiB");
+typedef Table<Adam32, 58> Table32;
+typedef Table<Adam32Copy, 52> Table32Copy;
+typedef Table<Adam8, 28> Table8;
+static_assert(sizeof(Table32) + sizeof(AdamCommon) <= 4096 && sizeof(Table32Copy) + sizeof(AdamCommon) <= 4096 &&
+              sizeof(Table8) + sizeof(AdamCommon) + 8 <= 4096, "a kernel's arguments are at most 4 KiB");
 
 // the tensor that chunk `c` belongs to: each lane looks at one tensor (a search
 // would read the arguments several times, one after the other)
@@ -213,11 +216,11 @@ __device__ __forceinline__ void store4(int src, void* base, int64_t at, int64_t 
 // ---------------------------------------------------------------------------
 // moments in fp32
 // ---------------------------------------------------------------------------
-template <int PS, int GS, int U>
-__global__ __launch_bounds__(256) void k_adamw32(const Table32 table, const AdamCommon c)
+template <int PS, int GS, int U, typename Tab>
+__global__ __launch_bounds__(256) void k_adamw32(const Tab table, const AdamCommon c)
 {
     const int ti = tensor_of(table, (int)blockIdx.x);
-    const Adam32& t = table.t[ti];
+    const auto& t = table.t[ti];
     const int64_t n = t.n, base = (int64_t)((int)blockIdx.x - table.first[ti]) * (1024 * U) + 4 * threadIdx.x;
     const float scale = c.scale ? *c.scale : 1.0f;
     float p[U][4], g[U][4], m[U][4], v[U][4];
@@ -244,7 +247,8 @@ __global__ __launch_bounds__(256) void k_adamw32(const Table32 table, const Adam
         store4<PS>(t.po, at, n, p[u]);
         store4<SRC_F32>(t.mo, at, n, m[u]);
         store4<SRC_F32>(t.vo, at, n, v[u]);
-        if (t.copy) store4<SRC_BF16>(t.copy, at, n, p[u]);
+        if constexpr (std::is_same<Tab, Table32Copy>::value)
+            if (t.copy) store4<SRC_BF16>(t.copy, at, n, p[u]);
     }
 }
 
@@ -540,8 +544,14 @@ hipError_t walk(int count, Piece piece, int elements, int most_chunks, Put put, 
 void put32(Adam32& e, const mx_adamw_tensor& t)
 {
     e.p = (const uint8_t*)t.p; e.g = (const uint8_t*)t.g; e.m = (const float*)t.m; e.v = (const float*)t.v;
-    e.po = (uint8_t*)t.p_out; e.mo = (float*)t.m_out; e.vo = (float*)t.v_out; e.copy = (uint16_t*)t.copy;
+    e.po = (uint8_t*)t.p_out; e.mo = (float*)t.m_out; e.vo = (float*)t.v_out;
     e.n = t.n;
+}
+
+void put32(Adam32Copy& e, const mx_adamw_tensor& t)
+{
+    put32(static_cast<Adam32&>(e), t);
+    e.copy = (uint16_t*)t.copy;
 }
 
 void put8(Adam8& e, const mx_adamw_tensor& t)
@@ -575,13 +585,23 @@ mx_adamw_tensor part_of(const mx_adamw_tensor& t, const AdamJob& j, int64_t from
     return e;
 }
 
+template <int PS, int GS, int U, typename Tab>
+hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
+{
+    return walk<Tab>(
+        j.count, [&](int i) { return j.tensors[i]; }, 1024 * U, MOST_CHUNKS, [](auto& e, const mx_adamw_tensor& t) { put32(e, t); },
+        [&](const Tab& t, int chunks) {
+            k_adamw32<PS, GS, U, Tab><<<chunks, 256, 0, s>>>(t, c);
+            return hipGetLastError();
+        });
+}
+
 template <int PS, int GS, int U>
 hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
-    return walk<Table32>(j.count, [&](int i) { return j.tensors[i]; }, 1024 * U, MOST_CHUNKS, put32, [&](const Table32& t, int chunks) {
-        k_adamw32<PS, GS, U><<<chunks, 256, 0, s>>>(t, c);
-        return hipGetLastError();
-    });
+    bool copy = false;
+    for (int i = 0; i < j.count; i++) copy = copy || j.tensors[i].copy;
+    return copy ? run32<PS, GS, U, Table32Copy>(j, c, s) : run32<PS, GS, U, Table32>(j, c, s);
 }
 
 int64_t elements_of(const AdamJob& j)

@@ -5,6 +5,7 @@ the GEMM runs in the HIP kernels of libmx.so.  PyTorch supplies device
 memory and the current HIP stream.  If the library is not built, calls raise
 immediately; there is no fallback implementation.
 """
+import bisect
 import ctypes
 import os
 from typing import NamedTuple, Optional, Tuple
@@ -940,7 +941,24 @@ class AdamWPlan:
         for i in range(n):
             self._one(self.array[i], i, params[i], self.grads.tensors[i], ms[i], vs[i], [x[i] for x in outs],
                       copies[i], params[0].dtype, spans)
-        _check_apart(spans)
+        self._written = _check_apart(spans)
+
+    def set_grads(self, grads) -> None:
+        """Other gradients of the same parameters, for a program whose gradients are new tensors each step."""
+        grads = TensorList(grads)
+        if len(grads) != self.count or (self.count and (grads.at != self.at)):
+            raise ValueError("one gradient for each parameter, on their device")
+        for i, t in enumerate(grads.tensors):
+            n = t.numel()
+            if n != self.array[i].n:
+                raise ValueError(f"gradient {i} must have {self.array[i].n} elements")
+            start, stop = t.data_ptr(), t.data_ptr() + n * t.element_size()
+            k = bisect.bisect_left(self._written, (stop,)) - 1       # the last written span that begins before its end
+            if n and k >= 0 and self._written[k][1] > start:
+                raise ValueError(f"gradient {i} overlaps a tensor that the step writes")
+        for a, t in zip(self.array, grads.tensors):
+            a.g = t.data_ptr()
+        self.grads = grads
 
     def _one(self, a, i, p, g, m, v, outs, copy, dtype, spans):
         a.n = n = p.numel()
@@ -974,7 +992,7 @@ class AdamWPlan:
 
 
 def _check_apart(spans):
-    """No output over another tensor than the input that it updates in place."""
+    """No output over another tensor than the input that it updates in place; returns the written spans in order."""
     inputs = {(s[3], s[0], s[1]) for s in spans if not s[2]}
     places = {(s[3], s[0], s[1]) for s in spans if s[2]} & inputs
     end = write_end = 0                          # where the spans so far end, and those that are written
@@ -986,6 +1004,7 @@ def _check_apart(spans):
         end = max(end, stop)
         if out:
             write_end = max(write_end, stop)
+    return sorted((start, stop) for start, stop, out, _ in spans if out)
 
 
 def adamw_plan(params, grads, exp_avg, exp_avg_sq, fmt=None, group: int = 128, copies=None, out=None) -> AdamWPlan:

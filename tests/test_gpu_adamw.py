@@ -143,6 +143,16 @@ def test_scale_copy_and_out_of_place():
     assert all(torch.equal(a, b) for x, y in zip(out, (t[0], t[2], t[3])) for a, b in zip(x, y))
 
 
+def test_new_gradients_of_a_plan():
+    t = _make([5000, 33], seed=8)
+    plan = mx.adamw_plan(*t)
+    other = _make([5000, 33], g="bf16", seed=9)[1]
+    before = _clone((t[0], other, t[2], t[3]))
+    plan.set_grads(other)
+    mx.mx_adamw_step(plan, 1e-3, 3, **HYPER)
+    _check(before, (t[0], t[2], t[3]))
+
+
 def test_rows_behind_the_tensors_stay():
     """Elements between and behind the tensors of one buffer are left as they were."""
     for fmt in (None, "e4m3"):

@@ -150,6 +150,26 @@ def test_plan_refuses_partial_overlap():
         mx.adamw_plan(p, [flat[50:150], g[1]], m, v, out=([flat[:100], torch.zeros(101)], m, v))
 
 
+def test_set_grads():
+    p, g, m, v = _tensors()
+    plan = mx.adamw_plan(p, g, m, v)
+    new = [torch.zeros(100, dtype=torch.bfloat16), torch.zeros(101, dtype=torch.bfloat16)]
+    plan.set_grads(new)
+    assert [plan.array[i].g for i in (0, 1)] == [t.data_ptr() for t in new] and plan.grads.src == mx.MX_SRC_BF16
+    for bad, error in (([new[0]], ValueError), ([new[1], new[0]], ValueError), ([new[0], torch.zeros(101)], TypeError),
+                       ([p[0], torch.zeros(101)], ValueError), ([m[0], torch.zeros(101)], ValueError)):
+        with pytest.raises(error):
+            plan.set_grads(bad)
+    assert plan.grads.tensors == tuple(new)
+    flat = torch.zeros(400)
+    plan = mx.adamw_plan([flat[100:200]], [torch.zeros(100)], [torch.zeros(100)], [torch.zeros(100)])
+    plan.set_grads([flat[:100]])
+    plan.set_grads([flat[200:300]])
+    for at in (1, 50, 100, 199):
+        with pytest.raises(ValueError):
+            plan.set_grads([flat[at:at + 100]])
+
+
 def test_fp8_plan_refuses():
     p, g, m, v = _tensors(group=64)
     q, amax, k = m[0]
