@@ -715,9 +715,9 @@ mx_status mx_gemm_glu(const void* qa, const uint8_t* sa, const float* ta, int32_
     g_msg[0] = '\0';
     mx_status s = check_gemm_operands(qa, sa, ta, fa, qg, sg, tg, fb, M, F, K, hadamard_k);
     if (s != MX_OK || (s = check_gemm_operands(qa, sa, ta, fa, qu, su, tu, fb, M, F, K, hadamard_k)) != MX_OK) return s;
-    // tiles of 32 elements of F, in eights, by tiles of at least 32 rows, and 512 threads each
-    if ((F + 255) / 256 * 8 * ((M + 31) / 32) >= (int64_t)1 << 22)
-        return fail(MX_ERR_INVALID_ARG, "M x F must be fewer than 2^22 tiles of 32 x 32");
+    // (a launch counts its threads with 32 bits: at most 512 to a tile, or 256 to 32 x 32 of it, six at most)
+    if (((M + 255) / 256) * ((F + 127) / 128) >= (int64_t)1 << 21)
+        return fail(MX_ERR_INVALID_ARG, "M x F must be fewer than 2^21 output tiles of 256 x 128");
     if ((s = check_act(act)) != MX_OK) return s;
     if (!h && !qh) return fail(MX_ERR_INVALID_ARG, "one of h and qh is needed");
     if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return fail(MX_ERR_INVALID_ARG, "unknown output dtype");

@@ -109,6 +109,166 @@ __device__ __forceinline__ int swz(int row, int chunk) { return row * BKB + ((ch
 // kernel's fixed cost).
 __device__ __forceinline__ uint32_t f32x2_to_bf16x2_rne(float a, float b) { return pack_bf16(a, b); }
 
+// Output kind of both kernels beside fp32 (0), bf16 (1) and, of k_gemm_w4, MX codes
+// (2 E4M3, 3 E5M2)
+constexpr int GLU = 4;
+
+// OUT == GLU: what becomes of one 32 x 32 tile of gate and up.  The weights are
+// the first operand of the matrix instruction there, so that a lane's 16
+// accumulators are 16 columns of one row, 8 (r / 4) + 4 h + r % 4, and the lane
+// 32 further on has the other 16 of the same 1x32 block: block maxima take one
+// exchange between the halves, and two more (of codes; by pairs of registers)
+// give each lane 16 consecutive columns to store.  No LDS is used.  (Staged
+// there as fp32 and read back along rows: 959 us instead of 911 at 8192 x 4096 x
+// 14336 E4M3 with checkpoints, 876 instead of 842 without; mx_gemm of the same
+// products with bf16 output takes 863, and mx_glu_forward 146 or 103 more.)
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b)
+{
+    auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);     // the high half of a with the low half of b
+    a = p[0];
+    b = p[1];
+}
+
+// 16 registers of four columns each to 16 consecutive columns: w dwords a group of four
+template <int W>
+__device__ __forceinline__ void to_run(uint32_t (&d)[4 * W])
+{
+#pragma unroll
+    for (int c = 0; c < W; c++) {
+        swap_halves(d[c], d[2 * W + c]);
+        swap_halves(d[W + c], d[3 * W + c]);
+    }
+    // groups 0, 2, 1, 3 are now consecutive
+#pragma unroll
+    for (int c = 0; c < W; c++) {
+        const uint32_t t = d[W + c];
+        d[W + c] = d[2 * W + c];
+        d[2 * W + c] = t;
+    }
+}
+
+// where a lane stores: row, first of its 16 columns, how many of them are there (0 for a row past the end)
+struct RunAt { int64_t m, f; int n; };
+
+__device__ __forceinline__ void store_run(bool f32, void* base, int64_t ld, const RunAt& r, const float (&v)[16])
+{
+    const int64_t at = r.m * ld + r.f;
+    if (f32) {
+        uint32_t d[16];
+#pragma unroll
+        for (int k = 0; k < 16; k++) d[k] = __float_as_uint(v[k]);
+        to_run<4>(d);
+        float* p = (float*)base + at;
+        if (r.n == 16) {
+            __builtin_memcpy(p, d, 64);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; k++)
+                if (k < r.n) p[k] = __uint_as_float(d[k]);
+        }
+    } else {
+        uint32_t d[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) d[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+        to_run<2>(d);
+        uint16_t* p = (uint16_t*)base + at;
+        if (r.n == 16) {
+            __builtin_memcpy(p, d, 32);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; k++)
+                if (k < r.n) p[k] = (uint16_t)(d[k / 2] >> (16 * (k % 2)));
+        }
+    }
+}
+
+// one block of a row copy (mx_quantize's encoding) from the two lanes that hold
+// it; the converters saturate (saturate_converters)
+__device__ __forceinline__ void store_block(int fmt, uint8_t* q, uint8_t* s, int64_t ld, const RunAt& r, int h, const float (&v)[16])
+{
+    uint32_t key = chunk_key<16>(v), other = key;
+    swap_halves(key, other);
+    key = max(key, other);
+    uint32_t d[4], byte;
+    if (fmt == E4M3) {
+        const BlockScale<E4M3> b(key);
+#pragma unroll
+        for (int k = 0; k < 4; k++) d[k] = encode4<E4M3, true>(b, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        byte = b.byte;
+    } else {
+        const BlockScale<E5M2> b(key);
+#pragma unroll
+        for (int k = 0; k < 4; k++) d[k] = encode4<E5M2, true>(b, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        byte = b.byte;
+    }
+    if (key >= NONFINITE) {
+        d[0] = d[1] = d[2] = d[3] = 0x7F7F7F7Fu;
+        byte = 0xFFu;
+    }
+    to_run<1>(d);
+    if (r.n > 0) {                                   // (all 16: F is a multiple of 32 here)
+        const int64_t at = r.m * ld + r.f;
+        *(uint4*)(q + at) = make_uint4(d[0], d[1], d[2], d[3]);
+        if (h == 0) s[at >> 5] = (uint8_t)byte;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void glu_tile(const GluArgs& a, const f16v& ga, const f16v& ua, float ag, float au, const RunAt& r, int h)
+{
+    float g[16], u[16], y[16];
+#pragma unroll
+    for (int k = 0; k < 16; k++) {
+        g[k] = ga[k] * ag;
+        u[k] = ua[k] * au;
+        float d;
+        gate<ACT, false>(g[k], y[k], d);
+        y[k] *= u[k];
+    }
+    if (a.h) store_run(a.out_f32, a.h, a.ld_h, r, y);
+    if (a.gate) {
+        store_run(a.out_f32, a.gate, a.ld_gate, r, g);
+        store_run(a.out_f32, a.up, a.ld_up, r, u);
+    }
+    if (a.qh) store_block(a.h_fmt, a.qh, a.sh, a.N, r, h, y);
+    if (a.qgc) {
+        store_block(a.ckpt_fmt, a.qgc, a.sgc, a.N, r, h, g);
+        store_block(a.ckpt_fmt, a.quc, a.suc, a.N, r, h, u);
+    }
+}
+
+// a wave's 128 rows x 16 JT columns from m0, f0 on: tiles 0 .. JT/2 - 1 of gate, then those of up
+template <int ACT, int JT>
+__device__ __forceinline__ void glu_part(const GluArgs& a, const f16v (&acc)[4][JT], float ag, float au, int64_t m0, int64_t f0, int h, int l32)
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < JT / 2; j++) {
+            RunAt r;
+            r.m = m0 + 32 * i + l32;
+            r.f = f0 + 32 * j + 16 * h;
+            r.n = r.m < a.M ? (int)min(max(a.N - r.f, (int64_t)0), (int64_t)16) : 0;
+            glu_tile<ACT>(a, acc[i][j], acc[i][j + JT / 2], ag, au, r, h);
+            __builtin_amdgcn_sched_barrier(0);       // one tile's values in registers at a time
+        }
+}
+
+template <int JT>
+__device__ __forceinline__ void glu_epilogue(const GluArgs& g, const f16v (&acc)[4][JT], int64_t m0, int64_t f0, int h, int l32)
+{
+    float ag = g.alpha, au;
+    if (g.ta) ag = ag * *g.ta;
+    au = ag;
+    if (g.tb) ag = ag * *g.tb;
+    if (g.tu) au = au * *g.tu;
+    if (g.hadamard_k) ag = ag * 0.03125f, au = au * 0.03125f;
+    saturate_converters();
+    if (g.act == ACT_SILU) glu_part<ACT_SILU, JT>(g, acc, ag, au, m0, f0, h, l32);
+    else if (g.act == ACT_GELU) glu_part<ACT_GELU, JT>(g, acc, ag, au, m0, f0, h, l32);
+    else glu_part<ACT_GELU_TANH, JT>(g, acc, ag, au, m0, f0, h, l32);
+}
+
 // tile index of this workgroup: XCD-aware, then grouped row-major order
 __device__ __forceinline__ void tile_of(int wg, int tiles_m, int tiles_n, int& tm, int& tn)
 {
@@ -171,7 +331,8 @@ struct LaneOffs {
     uint32_t sa, sb;      // scale-plane index of the lane's first A / B row
 };
 
-template <bool FP4>
+// BROWS: tile rows between the wave's two tiles of B (GLU: a tile of Wg, one of Wu)
+template <bool FP4, int BROWS>
 __device__ __forceinline__ void read_kstep(KFrag<FP4>& f, const uint8_t* sA, const uint8_t* sB,
                                            const uint32_t* sSA, const uint32_t* sSB, int ks, LaneOffs o,
                                            int h)
@@ -182,25 +343,25 @@ __device__ __forceinline__ void read_kstep(KFrag<FP4>& f, const uint8_t* sA, con
     // chunk (c ^ key) of the lane's rows, for c = cbase + h: rows 32 apart
     // share the key, so one offset serves all row tiles of the operand
     auto cofs = [&](int cbase) { return ((uint32_t)cbase << 4) ^ o.hk; };
-    auto frag = [&](const uint8_t* base, uint32_t lane_off, int t) {
+    auto frag = [&](const uint8_t* base, uint32_t lane_off, int row) {
         if constexpr (!FP4) {
-            const uint4 c0 = *(const uint4*)(base + lane_off + cofs(ks * 4) + t * 32 * BKB);
-            const uint4 c1 = *(const uint4*)(base + lane_off + cofs(ks * 4 + 2) + t * 32 * BKB);
+            const uint4 c0 = *(const uint4*)(base + lane_off + cofs(ks * 4) + row * BKB);
+            const uint4 c1 = *(const uint4*)(base + lane_off + cofs(ks * 4 + 2) + row * BKB);
             return int8v{(int)c0.x, (int)c0.y, (int)c0.z, (int)c0.w, (int)c1.x, (int)c1.y, (int)c1.z, (int)c1.w};
         } else {
-            const uint4 c0 = *(const uint4*)(base + lane_off + cofs(ks * 2) + t * 32 * BKB);
+            const uint4 c0 = *(const uint4*)(base + lane_off + cofs(ks * 2) + row * BKB);
             return int4v{(int)c0.x, (int)c0.y, (int)c0.z, (int)c0.w};
         }
     };
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        f.a[i] = frag(sA, o.a, i);
+        f.a[i] = frag(sA, o.a, 32 * i);
         f.sa[i] = sSA[(ks / 2) * BM + o.sa + i * 32] >> (8 * h);
     }
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-        f.b[j] = frag(sB, o.b, j);
-        f.sb[j] = sSB[(ks / 2) * BM + o.sb + j * 32] >> (8 * h);
+        f.b[j] = frag(sB, o.b, BROWS * j);
+        f.sb[j] = sSB[(ks / 2) * BM + o.sb + j * BROWS] >> (8 * h);
     }
 }
 
@@ -216,44 +377,49 @@ __device__ __forceinline__ void hold(KFrag<FP4>& f)
 #endif
 }
 
+// one MFMA of a k-step; GLU: the weights first (see glu_tile)
+template <int FA, int FB, bool GLU_ORDER>
+__device__ __forceinline__ f16v mma_one(const typename KFrag<FA == E2M1>::V& a, const typename KFrag<FA == E2M1>::V& b, f16v acc, int ks,
+                                        uint32_t sa, uint32_t sb)
+{
+    constexpr bool FP4 = FA == E2M1;
+    if constexpr (GLU_ORDER) {
+        if ((ks & 1) == 0)
+            return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mfma_src<FP4>(b), mfma_src<FP4>(a), acc, MfmaFmt<FB>::code, MfmaFmt<FA>::code, 0,
+                                                                   (int)sb, 0, (int)sa);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mfma_src<FP4>(b), mfma_src<FP4>(a), acc, MfmaFmt<FB>::code, MfmaFmt<FA>::code, 2, (int)sb,
+                                                               2, (int)sa);
+    } else {
+        if ((ks & 1) == 0)
+            return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mfma_src<FP4>(a), mfma_src<FP4>(b), acc, MfmaFmt<FA>::code, MfmaFmt<FB>::code, 0,
+                                                                   (int)sa, 0, (int)sb);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mfma_src<FP4>(a), mfma_src<FP4>(b), acc, MfmaFmt<FA>::code, MfmaFmt<FB>::code, 2, (int)sa,
+                                                               2, (int)sb);
+    }
+}
+
 // One k-step of MFMAs; after MFMA m (0..7) calls between(m), in program order.
-template <int FA, int FB, typename Between>
+template <int FA, int FB, bool GLU_ORDER, typename Between>
 __device__ __forceinline__ void mma_kstep_with(f16v (&acc)[4][2], const KFrag<FA == E2M1>& f, int ks, Between between)
 {
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-            if ((ks & 1) == 0)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    mfma_src<FA == E2M1>(f.a[i]), mfma_src<FA == E2M1>(f.b[j]), acc[i][j], MfmaFmt<FA>::code, MfmaFmt<FB>::code, 0, (int)f.sa[i], 0,
-                    (int)f.sb[j]);
-            else
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    mfma_src<FA == E2M1>(f.a[i]), mfma_src<FA == E2M1>(f.b[j]), acc[i][j], MfmaFmt<FA>::code, MfmaFmt<FB>::code, 2, (int)f.sa[i], 2,
-                    (int)f.sb[j]);
+            acc[i][j] = mma_one<FA, FB, GLU_ORDER>(f.a[i], f.b[j], acc[i][j], ks, f.sa[i], f.sb[j]);
             __builtin_amdgcn_sched_barrier(0);
             between(2 * i + j);
             __builtin_amdgcn_sched_barrier(0);
         }
 }
 
-template <int FA, int FB>
+template <int FA, int FB, bool GLU_ORDER>
 __device__ __forceinline__ void mma_kstep(f16v (&acc)[4][2], const KFrag<FA == E2M1>& f, int ks)
 {
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            if ((ks & 1) == 0)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    mfma_src<FA == E2M1>(f.a[i]), mfma_src<FA == E2M1>(f.b[j]), acc[i][j], MfmaFmt<FA>::code, MfmaFmt<FB>::code, 0, (int)f.sa[i], 0,
-                    (int)f.sb[j]);
-            else
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    mfma_src<FA == E2M1>(f.a[i]), mfma_src<FA == E2M1>(f.b[j]), acc[i][j], MfmaFmt<FA>::code, MfmaFmt<FB>::code, 2, (int)f.sa[i], 2,
-                    (int)f.sb[j]);
-        }
+        for (int j = 0; j < 2; j++) acc[i][j] = mma_one<FA, FB, GLU_ORDER>(f.a[i], f.b[j], acc[i][j], ks, f.sa[i], f.sb[j]);
 }
 
 // Workgroup barrier between the phases of the two-group schedule: this wave's LDS reads complete, no
@@ -266,7 +432,7 @@ __device__ __forceinline__ void half_barrier()
 
 template <int FA, int FB, int OUT>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void k_gemm(GArgs g)
+void k_gemm(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)      // the host pass only needs the launch stub
     constexpr bool FP4 = (FA == E2M1);
@@ -289,7 +455,8 @@ void k_gemm(GArgs g)
 
     int tm, tn;
     tile_of(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    constexpr int NT = OUT == GLU ? BN / 2 : BN;     // columns of N that the tile covers
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * NT;
 
     const int64_t kbytes = g.K / EPB;                // bytes per operand row
     const int64_t kblocks = g.K / 32;
@@ -312,23 +479,34 @@ void k_gemm(GArgs g)
     // lane offset, so rows past the matrix still fall outside the range.
     auto rsrc = [&](const uint8_t* base, int64_t first_row, int64_t rows, int64_t row_bytes) __attribute__((always_inline)) {
         int64_t n = (rows - first_row) * row_bytes;
+        if constexpr (OUT == GLU) n = min(n, BM * row_bytes);     // the tile's rows, at most 2^31 bytes: see load_tail
         n = n < 0 ? 0 : n > 0xFFFFFFFFll ? 0xFFFFFFFFll : n;
         return __builtin_amdgcn_make_buffer_rsrc((void*)(base + first_row * row_bytes), (short)0,
                                                  (int)(uint32_t)n, 0x00020000);
     };
     const auto ra = rsrc(g.qa, m0, g.M, kbytes), rb = rsrc(g.qb, n0, g.N, kbytes);
-    const auto rsa = rsrc(g.sa, m0, g.M, kblocks), rsb = rsrc(g.sb, n0, g.N, kblocks);
+    const auto rsa = rsrc(g.sa, m0, g.M, kblocks);
+    auto rsb = rsrc(g.sb, n0, g.N, kblocks);
+    // GLU: tile rows 0-127 of B are rows of Wg, 128-255 the same rows of Wu
+    auto rb2 = rb;
+    uint32_t soff_brow = soff_row;
+    if constexpr (OUT == GLU) {
+        rb2 = rsrc(g.qu, n0, g.N, kbytes);
+        if (wave & 2) rsb = rsrc(g.su, n0, g.N, kblocks);
+        soff_brow = (uint32_t)((64 * (wave & 1) + lane) * kblocks);
+    }
     // Operand load instruction q (0..15) of stage s: run p = q / 2 of A (q
     // even) or B (q odd); then the scale loads.
-    auto dma_op = [&](int s, int q, uint8_t* sA, uint8_t* sB) __attribute__((always_inline)) {
+    auto dma_op = [&](int s, int q, uint8_t* sA, uint8_t* sB, bool fetch = true) __attribute__((always_inline)) {
         const int p = q >> 1;
         uint32_t v = voff;
 #if defined(__HIP_DEVICE_COMPILE__)
         asm volatile("" : "+v"(v));
 #endif
-        const uint32_t off = v + (uint32_t)(s * BKB) + (uint32_t)(32 * p * kbytes);
+        uint32_t off = v + (uint32_t)(s * BKB) + (uint32_t)(32 * (OUT == GLU && (q & 1) ? p & 3 : p) * kbytes);
+        if (!fetch) off = 0xFFFFFFF0u;
         if (q & 1)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(sB + (32 * p + 8 * wave) * BKB), 16, off, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(OUT == GLU && p >= 4 ? rb2 : rb, (lds_void*)(sB + (32 * p + 8 * wave) * BKB), 16, off, 0, 0, 0);
         else
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(sA + (32 * p + 8 * wave) * BKB), 16, off, 0, 0, 0);
     };
@@ -336,9 +514,9 @@ void k_gemm(GArgs g)
     auto dma_scales = [&](int s, uint32_t* sSA, uint32_t* sSB) __attribute__((always_inline)) {
 #pragma unroll
         for (int w = 0; w < SB / 4; w++) {
-            const uint32_t off = soff_row + (uint32_t)(s * SB + 4 * w);
+            const uint32_t off = soff_row + (uint32_t)(s * SB + 4 * w), offb = soff_brow + (uint32_t)(s * SB + 4 * w);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void*)(sSA + w * BM + 64 * wave), 4, off, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void*)(sSB + w * BM + 64 * wave), 4, off, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void*)(sSB + w * BM + 64 * wave), 4, offb, 0, 0, 0);
         }
     };
     auto load_direct = [&](int s, uint8_t* sA, uint8_t* sB, uint32_t* sSA, uint32_t* sSB) __attribute__((always_inline)) {
@@ -346,9 +524,16 @@ void k_gemm(GArgs g)
         for (int q = 0; q < 16; q++) dma_op(s, q, sA, sB);
         dma_scales(s, sSA, sSB);
     };
-    // register path with zero fill for a ragged last stage
+    // register path with zero fill for a ragged last stage (GLU, which has no
+    // registers left for it: direct loads, with chunks past a row's end taken
+    // from past the tile, which gives zeros)
     auto load_tail = [&](int s, uint8_t* sA, uint8_t* sB, uint32_t* sSA, uint32_t* sSB) __attribute__((always_inline)) {
         const int64_t kb0 = (int64_t)s * BKB;
+        if constexpr (OUT == GLU) {
+            const bool fetch = kb0 + (((lane & 7) ^ swz_key(lrow)) << 4) < kbytes;
+#pragma unroll
+            for (int q = 0; q < 16; q++) dma_op(s, q, sA, sB, fetch);
+        } else
 #pragma unroll
         for (int p = 0; p < 8; p++) {
             const int id = p * 256 + tid;
@@ -363,7 +548,11 @@ void k_gemm(GArgs g)
             *(uint4*)(sA + swz(row, chunk)) = va;
             *(uint4*)(sB + swz(row, chunk)) = vb;
         }
-        const int64_t ar = min(m0 + tid, g.M - 1), br = min(n0 + tid, g.N - 1);
+        const uint8_t* sb = g.sb;
+        int64_t brow = n0 + tid;
+        if constexpr (OUT == GLU)
+            if (wave & 2) sb = g.su, brow -= 128;
+        const int64_t ar = min(m0 + tid, g.M - 1), br = min(brow, g.N - 1);
 #pragma unroll
         for (int w = 0; w < SB / 4; w++) {
             uint32_t va = 0, vb = 0;
@@ -371,7 +560,7 @@ void k_gemm(GArgs g)
             for (int b = 0; b < 4; b++) {
                 const int64_t blk = (int64_t)s * SB + 4 * w + b;
                 const uint32_t xa = blk < kblocks ? g.sa[ar * kblocks + blk] : 127u;
-                const uint32_t xb = blk < kblocks ? g.sb[br * kblocks + blk] : 127u;
+                const uint32_t xb = blk < kblocks ? sb[br * kblocks + blk] : 127u;
                 va |= xa << (8 * b);
                 vb |= xb << (8 * b);
             }
@@ -407,10 +596,11 @@ void k_gemm(GArgs g)
     // barrier without a memory fence; both groups pass 2T+2 of them.
     LaneOffs lo;
     lo.a = (uint32_t)((wm * 128 + l32) * BKB);
-    lo.b = (uint32_t)((wn * 64 + l32) * BKB);
+    constexpr int BROWS = OUT == GLU ? 128 : 32;     // between the wave's two tiles of B
+    lo.b = (uint32_t)((wn * (OUT == GLU ? 32 : 64) + l32) * BKB);
     lo.hk = (uint32_t)((h ^ swz_key(l32)) << 4);
     lo.sa = (uint32_t)(wm * 128 + l32);
-    lo.sb = (uint32_t)(wn * 64 + l32);
+    lo.sb = (uint32_t)(wn * (OUT == GLU ? 32 : 64) + l32);
     KFrag<FP4> f;
     // FAST: every load is direct (no register path, no ragged stage); the
     // other case keeps its loads out of the MFMA phases.
@@ -425,7 +615,7 @@ void k_gemm(GArgs g)
         const bool next = s + 1 < nstages;
 #pragma unroll
         for (int ks = 0; ks < KSTEPS; ks++) {
-            read_kstep<FP4>(f, xA, xB, xSA, xSB, ks, lo, h);
+            read_kstep<FP4, BROWS>(f, xA, xB, xSA, xSB, ks, lo, h);
             if (ks == 0 && next) {
                 if constexpr (FAST) {
                     dma_scales(s + 1, ySA, ySB);
@@ -438,9 +628,9 @@ void k_gemm(GArgs g)
             half_barrier();
             hold(f);
             if (FAST && ks == 0 && next)
-                mma_kstep_with<FA, FB>(acc, f, ks, [&](int m) __attribute__((always_inline)) { dma_op(s + 1, 8 + m, yA, yB); });
+                mma_kstep_with<FA, FB, OUT == GLU>(acc, f, ks, [&](int m) __attribute__((always_inline)) { dma_op(s + 1, 8 + m, yA, yB); });
             else
-                mma_kstep<FA, FB>(acc, f, ks);
+                mma_kstep<FA, FB, OUT == GLU>(acc, f, ks);
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
             if (ks == KSTEPS - 1) __builtin_amdgcn_s_waitcnt(0);
@@ -463,17 +653,18 @@ void k_gemm(GArgs g)
     auto g1_stage = [&](const uint8_t* xA, const uint8_t* xB, const uint32_t* xSA, const uint32_t* xSB) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < KSTEPS; ks++) {
-            read_kstep<FP4>(f, xA, xB, xSA, xSB, ks, lo, h);
+            read_kstep<FP4, BROWS>(f, xA, xB, xSA, xSB, ks, lo, h);
             half_barrier();
             hold(f);
-            mma_kstep<FA, FB>(acc, f, ks);
+            mma_kstep<FA, FB, OUT == GLU>(acc, f, ks);
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
             half_barrier();
         }
     };
     if (wave < 4) {
-        if (g.reg_path || ragged) g0_run(std::false_type{});
+        // (GLU comes here only with a ragged K or unaligned scale arrays)
+        if (OUT == GLU || g.reg_path || ragged) g0_run(std::false_type{});
         else g0_run(std::true_type{});
     } else {
         half_barrier();                                        // stage 0 landed
@@ -484,6 +675,11 @@ void k_gemm(GArgs g)
             g1_stage(lA1, lB1, lSA1, lSB1);
         }
         if (s < nstages) g1_stage(lA0, lB0, lSA0, lSB0);
+    }
+
+    if constexpr (OUT == GLU) {
+        glu_epilogue<2>(g, acc, m0 + wm * 128, n0 + wn * 32, h, l32);
+        return;
     }
 
     // ---- epilogue: per-tensor scales once ----
@@ -625,149 +821,6 @@ __device__ __forceinline__ void store_nt16(void* p, uint4 v)
 {
     typedef unsigned int u32x4v __attribute__((ext_vector_type(4)));
     __builtin_nontemporal_store(u32x4v{v.x, v.y, v.z, v.w}, (u32x4v*)p);
-}
-
-// Output kinds of k_gemm_w4 beside fp32 (0), bf16 (1) and MX codes (2 E4M3, 3 E5M2)
-constexpr int GLU = 4;
-
-// OUT == GLU: what becomes of one 32 x 32 tile of gate and up.  The weights are
-// the first operand of the matrix instruction there, so that a lane's 16
-// accumulators are 16 columns of one row, 8 (r / 4) + 4 h + r % 4, and the lane
-// 32 further on has the other 16 of the same 1x32 block: block maxima take one
-// exchange between the halves, and two more (of codes; by pairs of registers)
-// give each lane 16 consecutive columns to store.  No LDS is used.  (Staged
-// there as fp32 and read back along rows: 959 us instead of 911 at 8192 x 4096 x
-// 14336 E4M3 with checkpoints, 876 instead of 842 without; mx_gemm of the same
-// products with bf16 output takes 863, and mx_glu_forward 146 or 103 more.)
-__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b)
-{
-    auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);     // the high half of a with the low half of b
-    a = p[0];
-    b = p[1];
-}
-
-// 16 registers of four columns each to 16 consecutive columns: w dwords a group of four
-template <int W>
-__device__ __forceinline__ void to_run(uint32_t (&d)[4 * W])
-{
-#pragma unroll
-    for (int c = 0; c < W; c++) {
-        swap_halves(d[c], d[2 * W + c]);
-        swap_halves(d[W + c], d[3 * W + c]);
-    }
-    // groups 0, 2, 1, 3 are now consecutive
-#pragma unroll
-    for (int c = 0; c < W; c++) {
-        const uint32_t t = d[W + c];
-        d[W + c] = d[2 * W + c];
-        d[2 * W + c] = t;
-    }
-}
-
-// where a lane stores: row, first of its 16 columns, how many of them are there (0 for a row past the end)
-struct RunAt { int64_t m, f; int n; };
-
-__device__ __forceinline__ void store_run(bool f32, void* base, int64_t ld, const RunAt& r, const float (&v)[16])
-{
-    const int64_t at = r.m * ld + r.f;
-    if (f32) {
-        uint32_t d[16];
-#pragma unroll
-        for (int k = 0; k < 16; k++) d[k] = __float_as_uint(v[k]);
-        to_run<4>(d);
-        float* p = (float*)base + at;
-        if (r.n == 16) {
-            __builtin_memcpy(p, d, 64);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; k++)
-                if (k < r.n) p[k] = __uint_as_float(d[k]);
-        }
-    } else {
-        uint32_t d[8];
-#pragma unroll
-        for (int k = 0; k < 8; k++) d[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
-        to_run<2>(d);
-        uint16_t* p = (uint16_t*)base + at;
-        if (r.n == 16) {
-            __builtin_memcpy(p, d, 32);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; k++)
-                if (k < r.n) p[k] = (uint16_t)(d[k / 2] >> (16 * (k % 2)));
-        }
-    }
-}
-
-// one block of a row copy (mx_quantize's encoding) from the two lanes that hold
-// it; the converters saturate (saturate_converters)
-__device__ __forceinline__ void store_block(int fmt, uint8_t* q, uint8_t* s, int64_t ld, const RunAt& r, int h, const float (&v)[16])
-{
-    uint32_t key = chunk_key<16>(v), other = key;
-    swap_halves(key, other);
-    key = max(key, other);
-    uint32_t d[4], byte;
-    if (fmt == E4M3) {
-        const BlockScale<E4M3> b(key);
-#pragma unroll
-        for (int k = 0; k < 4; k++) d[k] = encode4<E4M3, true>(b, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        byte = b.byte;
-    } else {
-        const BlockScale<E5M2> b(key);
-#pragma unroll
-        for (int k = 0; k < 4; k++) d[k] = encode4<E5M2, true>(b, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        byte = b.byte;
-    }
-    if (key >= NONFINITE) {
-        d[0] = d[1] = d[2] = d[3] = 0x7F7F7F7Fu;
-        byte = 0xFFu;
-    }
-    to_run<1>(d);
-    if (r.n > 0) {                                   // (all 16: F is a multiple of 32 here)
-        const int64_t at = r.m * ld + r.f;
-        *(uint4*)(q + at) = make_uint4(d[0], d[1], d[2], d[3]);
-        if (h == 0) s[at >> 5] = (uint8_t)byte;
-    }
-}
-
-template <int ACT>
-__device__ __forceinline__ void glu_tile(const GluArgs& a, const f16v& ga, const f16v& ua, float ag, float au, const RunAt& r, int h)
-{
-    float g[16], u[16], y[16];
-#pragma unroll
-    for (int k = 0; k < 16; k++) {
-        g[k] = ga[k] * ag;
-        u[k] = ua[k] * au;
-        float d;
-        gate<ACT, false>(g[k], y[k], d);
-        y[k] *= u[k];
-    }
-    if (a.h) store_run(a.out_f32, a.h, a.ld_h, r, y);
-    if (a.gate) {
-        store_run(a.out_f32, a.gate, a.ld_gate, r, g);
-        store_run(a.out_f32, a.up, a.ld_up, r, u);
-    }
-    if (a.qh) store_block(a.h_fmt, a.qh, a.sh, a.N, r, h, y);
-    if (a.qgc) {
-        store_block(a.ckpt_fmt, a.qgc, a.sgc, a.N, r, h, g);
-        store_block(a.ckpt_fmt, a.quc, a.suc, a.N, r, h, u);
-    }
-}
-
-// a wave's 128 rows x 64 columns from m0, f0 on
-template <int ACT>
-__device__ __forceinline__ void glu_part(const GluArgs& a, const f16v (&acc)[4][4], float ag, float au, int64_t m0, int64_t f0, int h, int l32)
-{
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            RunAt r;
-            r.m = m0 + 32 * i + l32;
-            r.f = f0 + 32 * j + 16 * h;
-            r.n = r.m < a.M ? (int)min(max(a.N - r.f, (int64_t)0), (int64_t)16) : 0;
-            glu_tile<ACT>(a, acc[i][j], acc[i][j + 2], ag, au, r, h);
-        }
 }
 
 // NB: tile columns (256, or 128 for the half tiles of a last partial round:
@@ -1120,17 +1173,7 @@ void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
             }
         }
     } else if constexpr (OUT == GLU) {
-        float ag = g.alpha, au;
-        if (g.ta) ag = ag * *g.ta;
-        au = ag;
-        if (g.tb) ag = ag * *g.tb;
-        if (g.tu) au = au * *g.tu;
-        if (g.hadamard_k) ag = ag * 0.03125f, au = au * 0.03125f;
-        saturate_converters();
-        const int64_t mw = m0 + wm * 128, fw = n0 + wn * 64;
-        if (g.act == ACT_SILU) glu_part<ACT_SILU>(g, acc, ag, au, mw, fw, h, l32);
-        else if (g.act == ACT_GELU) glu_part<ACT_GELU>(g, acc, ag, au, mw, fw, h, l32);
-        else glu_part<ACT_GELU_TANH>(g, acc, ag, au, mw, fw, h, l32);
+        glu_epilogue<JT>(g, acc, m0 + wm * 128, n0 + wn * 64, h, l32);
     } else if constexpr (OUT >= 2) {
         // MX-quantized output (OUT 2: E4M3, 3: E5M2), 1x32 blocks along the
         // rows of C.  Each wave stages a 32-row slab of its quarter as fp32
@@ -1253,7 +1296,10 @@ hipError_t launch2(const GArgs& a, int out, hipStream_t s)
 template <int FA, int FB>
 hipError_t launch_glu(const GluArgs& a, hipStream_t s)
 {
-    k_gemm_w4<FA, FB, GLU, 256><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, s>>>(a);
+    constexpr int EPB = FA == E2M1 ? 2 : 1;
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n));
+    if (!a.reg_path && (a.K / EPB) % BKB == 0) k_gemm_w4<FA, FB, GLU, 256><<<grid, dim3(256), 0, s>>>(a);
+    else k_gemm<FA, FB, GLU><<<grid, dim3(512), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -1265,13 +1311,7 @@ bool gemm_w4_eligible(const GemmJob& j)
     return kbytes % BKB == 0 && (((uintptr_t)j.sa | (uintptr_t)j.sb) & 3u) == 0;
 }
 
-bool gemm_glu_w4_eligible(const GemmGluJob& j)
-{
-    const int64_t kbytes = j.fa == E2M1 ? j.K / 2 : j.K;
-    return kbytes % BKB == 0 && (((uintptr_t)j.sa | (uintptr_t)j.sg | (uintptr_t)j.su) & 3u) == 0;
-}
-
-hipError_t launch_gemm_glu_w4(const GemmGluJob& j, hipStream_t stream)
+hipError_t launch_gemm_glu_tiles(const GemmGluJob& j, hipStream_t stream)
 {
     GluArgs a{};
     a.qa = j.qa; a.sa = j.sa; a.ta = j.ta;
@@ -1285,6 +1325,7 @@ hipError_t launch_gemm_glu_w4(const GemmGluJob& j, hipStream_t stream)
     a.ckpt_fmt = j.ckpt_fmt; a.qgc = j.qgc; a.sgc = j.sgc; a.quc = j.quc; a.suc = j.suc;
     a.tiles_m = (int)((j.M + BM - 1) / BM);
     a.tiles_n = (int)((j.F + BN / 2 - 1) / (BN / 2));
+    a.reg_path = (((uintptr_t)j.sa | (uintptr_t)j.sg | (uintptr_t)j.su) & 3u) != 0;
     if (j.fa == E2M1) return launch_glu<E2M1, E2M1>(a, stream);
     if (j.fa == E4M3 && j.fb == E4M3) return launch_glu<E4M3, E4M3>(a, stream);
     if (j.fa == E5M2 && j.fb == E4M3) return launch_glu<E5M2, E4M3>(a, stream);

@@ -6,9 +6,8 @@
 // here h as the down projection's operand and the 8-bit checkpoints of gate
 // and up, [COAT, "FP8啟用"].)
 //
-// Many rows run on k_gemm_w4 (gemm.hip).  k_glu_rows below takes few rows, and
-// everything whose K or scale arrays that kernel does not take.  For few rows
-// the time goes to reading the weights once.  The matrix instruction gets 32
+// Many rows run on the GEMM kernels (gemm.hip), k_glu_rows below takes few:
+// their time goes to reading the weights once.  The matrix instruction gets 32
 // rows of Wg, then of Wu, as its first operand and up to 32 tokens as its
 // second, so that a lane holds gate and up of the same elements.  A workgroup
 // covers 32 elements of F (one block of a row copy); its waves split K and meet
@@ -307,13 +306,14 @@ hipError_t launch_rows(const GemmGluJob& j, hipStream_t s)
 hipError_t launch_gemm_glu(const GemmGluJob& j, hipStream_t s)
 {
     // k_glu_rows takes a time in proportion to its workgroups (32 rows x 32
-    // elements; at 14336 x 4096 E4M3 127 us for 3584 of them, 49 for 896),
-    // k_gemm_w4 one in proportion to its rounds of a 256 x 128 tile on each CU
-    // (65-76 us a round there), both in proportion to K: even at seven
-    // workgroups a CU and round (M = 128: 73 us by rows, 70 by tiles).
+    // elements), the GEMM kernels one in proportion to their rounds of a 256 x
+    // 128 tile on each CU, both in proportion to K.  At F = 14336, K = 4096, by
+    // rows and by tiles: M = 64 (896 workgroups) E4M3 37-48 and 51-65 us, E2M1
+    // 24 and 36; M = 96 (1344) 64 and 66, 32 and 38; M = 128 (1792) 58-73 and
+    // 51-70, 37 and 36; M = 256 127 and 51-76, 65 and 36.
     const int64_t wgs = ((j.M + ROWS - 1) / ROWS) * ((j.F + ROWS - 1) / ROWS);
     const int64_t rounds = (((j.M + 255) / 256) * ((j.F + 127) / 128) + 255) / 256;
-    if (wgs > 7 * 256 * rounds && gemm_glu_w4_eligible(j)) return launch_gemm_glu_w4(j, s);
+    if (wgs > 6 * 256 * rounds) return launch_gemm_glu_tiles(j, s);
     if (j.fa == E2M1) return launch_rows<E2M1, E2M1>(j, s);
     if (j.fa == E4M3) return j.fb == E4M3 ? launch_rows<E4M3, E4M3>(j, s) : launch_rows<E4M3, E5M2>(j, s);
     return j.fb == E4M3 ? launch_rows<E5M2, E4M3>(j, s) : launch_rows<E5M2, E5M2>(j, s);

@@ -138,10 +138,8 @@ struct GemmGluJob {
 
 hipError_t launch_gemm_glu(const GemmGluJob& j, hipStream_t stream);
 
-// the form for many rows (gemm.hip), and whether it takes the operands: rows of
-// K holding a multiple of 128 bytes of codes, 4-byte aligned scale arrays
-bool gemm_glu_w4_eligible(const GemmGluJob& j);
-hipError_t launch_gemm_glu_w4(const GemmGluJob& j, hipStream_t stream);
+// the form for many rows (gemm.hip): tiles of 256 rows x 128 elements of F
+hipError_t launch_gemm_glu_tiles(const GemmGluJob& j, hipStream_t stream);
 
 // norm forward: s = x (+ residual, rounded; written to sum), its statistics,
 // y and / or the row copy of y, and the checkpoint (row copy) of s

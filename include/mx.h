@@ -536,8 +536,9 @@ mx_status mx_glu_backward_dual_layout(const void* dh, int64_t ld_dh, int32_t src
  * gate, up: [M][F] of `out_dtype` for a backward call from tensors; both or
  *        neither.
  * qgc, sgc, quc, suc: checkpoints of gate and up in ckpt_fmt; all four or none.
- * Formats and M, F, K as mx_gemm (for N: F), F % 32 == 0 where a row copy or
- * checkpoint is written; any K that mx_gemm takes, any alignment of the scales.
+ * Formats and M, F, K as mx_gemm (for N: F), but fewer than 2^21 output tiles of
+ * 256 x 128; F % 32 == 0 where a row copy or checkpoint is written; any K that
+ * mx_gemm takes, any alignment of the scales.
  * Codes 16-byte aligned.  Outputs must not overlap inputs or each other.
  * Errors: MX_ERR_INVALID_ARG, MX_ERR_UNSUPPORTED, MX_ERR_ALIGNMENT, MX_ERR_HIP.
  */

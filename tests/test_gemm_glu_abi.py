@@ -33,7 +33,8 @@ def _call(lib, fa=0, fb=0, M=4, F=64, K=64, alpha=1.0, had=0, act=0, ld_h=64, ou
     *[({k: None}, INV) for k in AT if k not in ("ta", "tg", "tu", "h")],
     (dict(h=None, qh=None, sh=None), INV), (dict(fa=3), INV), (dict(fb=-1), INV), (dict(fa=2), UNS), (dict(fb=2), UNS),
     (dict(M=0), INV), (dict(F=0), INV), (dict(K=0), INV), (dict(M=-1), INV), (dict(K=48), INV),
-    (dict(K=(1 << 23) + 32), INV), (dict(M=1 << 31), INV), (dict(F=1 << 31), INV), (dict(had=2), INV),
+    (dict(K=(1 << 23) + 32), INV), (dict(M=1 << 31), INV), (dict(F=1 << 31), INV),
+    (dict(M=1 << 20, F=1 << 19, ld_h=1 << 19, ld_g=1 << 19, ld_u=1 << 19), INV), (dict(had=2), INV),
     (dict(act=3), INV), (dict(act=-1), INV), (dict(out=2), INV), (dict(ld_h=63), INV), (dict(ld_g=63), INV),
     (dict(ld_u=0), INV), (dict(hf=2), UNS), (dict(hf=3), INV), (dict(cf=2), UNS), (dict(cf=9), INV),
     (dict(F=40), INV), *[({k: P * AT[k] + 8}, ALI) for k in ("qa", "qg", "qu", "qh", "qgc", "quc")],
