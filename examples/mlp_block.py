@@ -5,9 +5,9 @@ with its activations kept in 8 bits.
 
     s   = x + residual                  mx_norm_forward: s, its RMS norm, and
     xn  = rmsnorm(s) * w                    the E4M3 checkpoint of s
-    gu  = xn . W_gu                     mx_quantize_dual_layout, mx_gemm
-    h   = silu(gate) * up               mx_glu_forward: h as the next GEMM's
-                                            operand, checkpoints of gate and up
+    h   = silu(xn . W_g) * (xn . W_u)   mx_quantize_dual_layout, mx_gemm_glu: h as
+                                            the next GEMM's operand, checkpoints
+                                            of gate and up
     out = s + h . W_d                   mx_gemm
 
 The backward needs s, gate and up again (from their checkpoints), xn (its
@@ -15,6 +15,10 @@ column copy, which is the wgrad GEMM's operand) and h, which it recomputes:
 2 bytes an element in bf16 become 1.03, and h is not kept at all.  mx_glu_backward_dual_layout
 writes the gradients of gate and up, and h, as the operands of the backward
 GEMMs; mx_norm_backward adds the gradient that goes round the block.
+
+The optimizer keeps 32-bit weights and FP8 moments: mx_grad_norm gives the
+factor that clips the gradients, mx_adamw_step reads it on the device and writes
+the 16-bit weights, which are quantized again in both layouts.
 
 Data and weights are random.  The step's gradients are compared with torch's
 autograd in fp32 for up to 1024 tokens, and the step is timed.
@@ -84,8 +88,9 @@ def forward(x: torch.Tensor, residual: torch.Tensor, w: Weights):
     ffn = w.w_d.shape[0]
     n = mx.mx_norm_forward(x, w.norm, eps=EPS, kind="rms", residual=residual, ckpt_fmt=ACT_FMT)
     xq, xs, xqc, xsc, _ = mx.mx_quantize_dual_layout(n.y, ACT)
-    gu = _gemm((xq, xs), ACT_FMT, w.gu_col, ACT_FMT)
-    g = mx.mx_glu_forward(gu[:, :ffn], gu[:, ffn:], "silu", write_h=False, h_fmt=ACT_FMT, ckpt_fmt=ACT_FMT)
+    q, sc = w.gu_col
+    g = mx.mx_gemm_glu(xq, xs, None, ACT_FMT, q[:ffn], sc[:ffn], None, q[ffn:], sc[ffn:], None, ACT_FMT, xq.shape[0], ffn,
+                       xq.shape[1], act="silu", write_h=False, h_fmt=ACT_FMT, ckpt_fmt=ACT_FMT)
     out = n.sum + _gemm((g.qh, g.sh), ACT_FMT, w.d_col, ACT_FMT)
     return out, Saved(mx.checkpoint(ACT_FMT, n.qx, n.sx), n.rstd, (xqc, xsc),
                       mx.checkpoint(ACT_FMT, g.qg, g.sg), mx.checkpoint(ACT_FMT, g.qu, g.su))
@@ -102,6 +107,37 @@ def backward(dout: torch.Tensor, saved: Saved, w: Weights):
     dw_gu = _gemm(saved.xn_col, ACT_FMT, (d.q_col, d.s_col), GRAD_FMT)
     n = mx.mx_norm_backward(dxn, saved.rstd, ckpt=saved.s, weight=w.norm, kind="rms", dsum=dout)
     return n.dx, n.dweight, dw_gu, dw_d
+
+
+class Optimizer:
+    """AdamW on a block's weights: 32-bit weights, FP8 moments, gradients clipped to a global norm."""
+
+    def __init__(self, w: Weights, lr: float = 3e-4, max_norm: float = 1.0):
+        self.w, self.lr, self.max_norm = w, lr, max_norm
+        self.copies = [w.norm, w.w_gu, w.w_d]
+        self.params = [t.float() for t in self.copies]
+        self.moments = [[mx.adamw_state(t, ACT_FMT) for t in self.params] for _ in range(2)]
+        grads = [torch.empty_like(t) for t in self.copies]            # each step brings its own
+        self.plan = mx.adamw_plan(self.params, grads, *self.moments, fmt=ACT_FMT, copies=self.copies)
+        self.step_count = torch.zeros(1, dtype=torch.int64, device=w.norm.device)
+
+    def step(self, dnorm, dw_gu, dw_d) -> torch.Tensor:
+        """One step from the gradients; returns their norm and the factor that clipped it."""
+        self.step_count += 1
+        self.plan.set_grads([dnorm.to(self.copies[0].dtype), dw_gu, dw_d])
+        clip = mx.mx_grad_norm(self.plan.grads, max_norm=self.max_norm)
+        mx.mx_adamw_step(self.plan, self.lr, self.step_count, betas=(0.9, 0.95), weight_decay=0.1, scale=clip[1:])
+        w = self.w
+        for t, row, col in ((w.w_gu, w.gu_row, w.gu_col), (w.w_d, w.d_row, w.d_col)):
+            mx.mx_quantize_dual_layout(t, ACT, *row, *col)
+        return clip
+
+
+def train_step(x, residual, dout, w: Weights, opt: Optimizer):
+    """Forward, backward from the gradient of out, and the optimizer's step; returns out, dx and the clipping."""
+    out, saved = forward(x, residual, w)
+    dx, *grads = backward(dout, saved, w)
+    return out, dx, opt.step(*grads)
 
 
 def reference(x, residual, dout, w: Weights):
@@ -155,6 +191,15 @@ def main():
     ms = (time.perf_counter() - t) / a.steps * 1e3
     flops = 18 * a.tokens * a.hidden * a.ffn
     print(f"forward and backward: {ms:.3f} ms, {flops / ms / 1e9:.0f} TFLOP/s over everything", flush=True)
+    opt = Optimizer(w)
+    for _ in range(3):
+        train_step(x, r, dout, w, opt)
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    for _ in range(a.steps):
+        train_step(x, r, dout, w, opt)
+    torch.cuda.synchronize()
+    print(f"with the optimizer's step: {(time.perf_counter() - t) / a.steps * 1e3:.3f} ms", flush=True)
 
 
 if __name__ == "__main__":

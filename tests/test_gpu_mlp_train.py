@@ -1,0 +1,91 @@
+"""A whole training step of examples/mlp_block.py: the fused projections, the
+backward from their checkpoints, the clipped gradients and the AdamW step with
+FP8 moments, eager and as a captured graph."""
+import math
+import os
+import sys
+
+import pytest
+import torch
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+import mlp_block as B  # noqa: E402
+
+from fp4_quantization_block_amd import mx  # noqa: E402
+from gpu_util import DEV, require_gpu  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+TOKENS, HIDDEN, FFN = 256, 512, 1024
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _block(seed=0):
+    w = B.make_weights(HIDDEN, FFN, DEV, seed)
+    return w, B.Optimizer(w, max_norm=1e-3)
+
+
+def test_step_is_adamw_of_the_clipped_gradients():
+    """The first step from zero moments: sign-like, known in closed form from the gradients."""
+    w, opt = _block()
+    x, r, dout = B.inputs(TOKENS, HIDDEN, DEV)
+    out, saved = B.forward(x, r, w)
+    dx, *grads = B.backward(dout, saved, w)
+    before = [p.clone() for p in opt.params]
+    clip = opt.step(*grads)
+    grads = [grads[0].bfloat16(), *grads[1:]]
+    norm = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    assert abs(float(clip[0]) - norm) <= 2 ** -23 * norm
+    assert abs(float(clip[1]) - min(1.0, 1e-3 / norm)) <= 2 ** -23
+    for p, b, g, c in zip(opt.params, before, grads, opt.copies):
+        g = g.double() * float(clip[1])
+        # m / (1 - b1) = g, sqrt(v / (1 - b2)) = |g|; the update is at most lr, its roundings a few of fp32's
+        want = b.double() * (1 - opt.lr * 0.1) - opt.lr * g / (g.abs() + 1e-8)
+        assert float((p.double() - want).abs().max()) <= 2 ** -23 * float(b.abs().max()) + 32 * 2 ** -24 * opt.lr
+        assert torch.equal(c, p.bfloat16())
+    # the quantized weights are those of the new ones
+    for t, row, col in ((w.w_gu, w.gu_row, w.gu_col), (w.w_d, w.d_row, w.d_col)):
+        again = mx.mx_quantize_dual_layout(t, B.ACT)
+        assert all(torch.equal(a, b) for a, b in zip(again, (*row, *col)))
+
+
+def test_a_gradient_that_is_not_finite_changes_nothing():
+    w, opt = _block()
+    x, r, dout = B.inputs(TOKENS, HIDDEN, DEV)
+    B.train_step(x, r, dout, w, opt)
+    before = [t.clone() for t in (*opt.params, *opt.copies, *(a for s in opt.moments for m in s for a in m), *w.gu_row)]
+    dout[3, 5] = math.inf
+    clip = B.train_step(x, r, dout, w, opt)[2]
+    assert math.isnan(float(clip[1]))
+    after = [*opt.params, *opt.copies, *(a for s in opt.moments for m in s for a in m), *w.gu_row]
+    assert all(torch.equal(a, b) for a, b in zip(before, after))
+
+
+def test_captured_steps():
+    """The whole step in a graph, replayed over other inputs, against eager steps of a twin."""
+    (w, opt), (w2, opt2) = _block(), _block()
+    x, r, dout = B.inputs(TOKENS, HIDDEN, DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):                        # one step ahead of the capture, on both sides
+        B.train_step(x, r, dout, w, opt)
+    torch.cuda.current_stream().wait_stream(side)
+    B.train_step(x, r, dout, w2, opt2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, dx, clip = B.train_step(x, r, dout, w, opt)
+    for k in range(3):
+        new = B.inputs(TOKENS, HIDDEN, DEV, seed=10 + k)
+        for a, b in zip((x, r, dout), new):
+            a.copy_(b)
+        want = B.train_step(*new, w2, opt2)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((out, dx, clip, *opt.params, *opt.copies, *w.gu_col, *w.d_row), (*want, *opt2.params, *opt2.copies, *w2.gu_col, *w2.d_row)):
+            assert torch.equal(a, b), k
+        assert int(opt.step_count) == int(opt2.step_count) == k + 2
