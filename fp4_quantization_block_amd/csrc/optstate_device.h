@@ -244,7 +244,7 @@ __device__ __forceinline__ void encode_state(const float (&xs)[E], uint32_t (&co
     const float amin = __uint_as_float(kmin + 1u);  // used only when some |x| > 0
     const bool bad = kmax >= 0x7F800000u;
     const float amax = __uint_as_float(kmax);
-    if (!SIGNED && kmax > 0x80000000u) {         // (a group's lanes take this together)
+    if (!SIGNED && kmax >= 0x80000000u) {        // (a group's lanes take this together)
         encode_state<FMT, T, E, true>(xs, codes, gamax, gk);
     } else if (bad) {                            // a NaN or Inf: the NaN code everywhere
 #pragma unroll
