@@ -795,12 +795,12 @@ static mx_status check_adamw_apart(const mx_adamw_tensor& t, bool fp8)
 
 int64_t mx_grad_norm_workspace_bytes(int32_t count) { return count < 0 ? 0 : mx::grad_norm_work_bytes(count); }
 
-mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, int32_t src_dtype, double max_norm, void* work,
-                       int64_t work_bytes, float* out, void* stream)
+mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, double max_norm, void* work, int64_t work_bytes,
+                       float* out, void* stream)
 {
     g_msg[0] = '\0';
     mx_status s = check_list(tensors, count);
-    if (s != MX_OK || (s = check_source_dtype(src_dtype)) != MX_OK) return s;
+    if (s != MX_OK) return s;
     if (!(max_norm > 0.0)) return fail(MX_ERR_INVALID_ARG, "max_norm must be > 0");
     if (!work || !out) return fail(MX_ERR_INVALID_ARG, "work and out must not be NULL");
     if (work_bytes < mx_grad_norm_workspace_bytes(count))
@@ -808,16 +808,17 @@ mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, int32_t src_dtyp
     if ((reinterpret_cast<uintptr_t>(work) & 7u) != 0 || off4(out))
         return fail(MX_ERR_ALIGNMENT, "work must be 8-byte and out 4-byte aligned");
     for (int32_t i = 0; i < count; i++) {
-        if ((s = check_length(tensors[i].n)) != MX_OK) return s;
+        if ((s = check_length(tensors[i].n)) != MX_OK || (s = check_source_dtype(tensors[i].dtype)) != MX_OK) return s;
+        if (tensors[i].reserved != 0) return fail(MX_ERR_INVALID_ARG, "reserved field must be 0");
         if (tensors[i].n == 0) continue;
         if (!tensors[i].x) return fail(MX_ERR_INVALID_ARG, "a tensor is NULL");
-        if (reinterpret_cast<uintptr_t>(tensors[i].x) % elem_bytes(src_dtype) != 0)
+        if (reinterpret_cast<uintptr_t>(tensors[i].x) % elem_bytes(tensors[i].dtype) != 0)
             return fail(MX_ERR_ALIGNMENT, "a tensor is not aligned to its element size");
         if (tensors[i].x == work || tensors[i].x == out)
             return fail(MX_ERR_INVALID_ARG, "work and out must not lie over a tensor");
     }
     mx::GradNormJob j{};
-    j.tensors = tensors; j.count = count; j.src = src_dtype; j.max_norm = max_norm;
+    j.tensors = tensors; j.count = count; j.max_norm = max_norm;
     j.work = (double*)work; j.out = out;
     return hip_status(mx::launch_grad_norm(j, (hipStream_t)stream));
 }

@@ -669,15 +669,23 @@ hipError_t launch_adamw(const AdamJob& j, hipStream_t s)
 
 int64_t grad_norm_work_bytes(int count)
 {
-    return ((int64_t)(count < 1 ? 1 : count) + NormTable::most - 1) / NormTable::most * NORM_WGS * (int64_t)sizeof(double);
+    // two walks, one for each type, of at most so many launches together
+    const int64_t launches = count < 1 ? 2 : ((int64_t)count + NormTable::most - 1) / NormTable::most + 1;
+    return launches * NORM_WGS * (int64_t)sizeof(double);
 }
 
+// the partial sums of the tensors of one type
 template <int SRC>
 hipError_t run_norm(const GradNormJob& j, int& partials, hipStream_t s)
 {
     return walk<NormTable>(
-        j.count, [&](int i) { return j.tensors[i]; }, NormChunk<SRC>::elements, 1 << 30,
-        [](NormEntry& e, const mx_tensor& t) { e.x = (const uint8_t*)t.x; e.n = t.n; },
+        j.count,
+        [&](int i) {
+            mx_tensor t = j.tensors[i];
+            if (t.dtype != SRC) t.n = 0;
+            return t;
+        },
+        NormChunk<SRC>::elements, 1 << 30, [](NormEntry& e, const mx_tensor& t) { e.x = (const uint8_t*)t.x; e.n = t.n; },
         [&](const NormTable& t, int chunks) {
             const int wgs = chunks < NORM_WGS ? chunks : NORM_WGS;
             k_grad_norm<SRC><<<wgs, 256, 0, s>>>(t, chunks, j.work + partials);
@@ -689,7 +697,8 @@ hipError_t run_norm(const GradNormJob& j, int& partials, hipStream_t s)
 hipError_t launch_grad_norm(const GradNormJob& j, hipStream_t s)
 {
     int partials = 0;
-    const hipError_t e = j.src == SRC_F32 ? run_norm<SRC_F32>(j, partials, s) : run_norm<SRC_BF16>(j, partials, s);
+    hipError_t e = run_norm<SRC_F32>(j, partials, s);
+    if (e == hipSuccess) e = run_norm<SRC_BF16>(j, partials, s);
     if (e != hipSuccess) return e;
     k_grad_norm_join<<<1, 256, 0, s>>>(j.work, partials, j.out, j.max_norm);
     return hipGetLastError();

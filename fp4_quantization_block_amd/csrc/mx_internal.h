@@ -69,7 +69,7 @@ struct AdamJob {
 hipError_t launch_adamw(const AdamJob& j, hipStream_t stream);
 
 struct GradNormJob {
-    const mx_tensor* tensors; int count; int src;
+    const mx_tensor* tensors; int count;
     double max_norm;
     double* work; float* out;
 };

@@ -56,7 +56,7 @@ class mx_qconfig(ctypes.Structure):
 
 
 class mx_tensor(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("n", ctypes.c_int64)]
+    _fields_ = [("x", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class mx_adamw_tensor(ctypes.Structure):
@@ -136,7 +136,7 @@ def load() -> ctypes.CDLL:
                               ctypes.c_float, _i32, _i32, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i64, _i32,
                               _vp, _vp, _vp, _vp, _vp]
     L.mx_grad_norm.restype = _i32
-    L.mx_grad_norm.argtypes = [_vp, _i32, _i32, ctypes.c_double, _vp, _i64, _vp, _vp]
+    L.mx_grad_norm.argtypes = [_vp, _i32, ctypes.c_double, _vp, _i64, _vp, _vp]
     L.mx_grad_norm_workspace_bytes.restype = _i64
     L.mx_grad_norm_workspace_bytes.argtypes = [_i32]
     L.mx_adamw_step.restype = _i32
@@ -860,17 +860,16 @@ def mx_gemm_glu(qa: torch.Tensor, sa, ta, fa, qg, sg, tg, qu, su, tu, fb, M: int
 # the optimizer's side of a step, over many tensors at once
 # ---------------------------------------------------------------------------
 class TensorList:
-    """The addresses of tensors of one type and device, as mx_grad_norm takes
-    them; keeps the tensors."""
+    """The addresses and types (float32 or bfloat16, each its own) of tensors of
+    one device, as mx_grad_norm takes them; keeps the tensors."""
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
-        self.src, self.at = MX_SRC_F32, -1
-        if self.tensors:
-            self.src, self.at = _src_code(self.tensors[0], "tensor 0"), self.tensors[0].get_device()
-        for i, t in enumerate(self.tensors):
-            _dense(t, t.shape, self.tensors[0].dtype, self.at, f"tensor {i}")
-        self.array = (mx_tensor * max(1, len(self.tensors)))(*((t.data_ptr(), t.numel()) for t in self.tensors))
+        self.at = self.tensors[0].get_device() if self.tensors else -1
+        self.array = (mx_tensor * max(1, len(self.tensors)))(*(
+            (_dense(t, t.shape, t.dtype, self.at, f"tensor {i}"), t.numel(), _src_code(t, f"tensor {i}"), 0)
+            for i, t in enumerate(self.tensors)))
+        self.nbytes = None                       # of mx_grad_norm's workspace
 
     def __len__(self):
         return len(self.tensors)
@@ -906,13 +905,15 @@ def mx_grad_norm(grads, max_norm: float = float("inf"), out: Optional[torch.Tens
         out = torch.empty(2, dtype=torch.float32, device=f"cuda:{at}") if n == 0 or at < 0 else \
             grads.tensors[0].new_empty_strided((2,), (1,), dtype=torch.float32)
     if work is None:
-        nbytes = L.mx_grad_norm_workspace_bytes(n)
+        nbytes = grads.nbytes
+        if nbytes is None:
+            nbytes = grads.nbytes = L.mx_grad_norm_workspace_bytes(n)
         work = out.new_empty_strided((nbytes,), (1,), dtype=torch.uint8)
     elif work.get_device() != at or not work.is_contiguous():
         raise ValueError("work must be contiguous and on the device of the gradients")
     else:
         nbytes = work.numel() * work.element_size()
-    _check(L.mx_grad_norm(grads.array, n, grads.src, max_norm, work.data_ptr(), nbytes,
+    _check(L.mx_grad_norm(grads.array, n, max_norm, work.data_ptr(), nbytes,
                           _dense(out, (2,), torch.float32, at, "out"), _stream_on(stream, at)))
     return out
 
@@ -925,6 +926,7 @@ class AdamWPlan:
         params, ms, vs = list(params), list(exp_avg), list(exp_avg_sq)
         n = len(params)
         self.grads = TensorList(grads)
+        self.grad_src = self._grad_src(self.grads)
         if out is None:
             out = params, ms, vs
         outs = [list(x) for x in out]
@@ -943,11 +945,19 @@ class AdamWPlan:
                       copies[i], params[0].dtype, spans)
         self._written = _check_apart(spans)
 
+    @staticmethod
+    def _grad_src(grads: TensorList) -> int:
+        kinds = {t.dtype for t in grads.tensors}
+        if len(kinds) > 1:
+            raise TypeError("the gradients of a plan must have one type")
+        return MX_SRC_BF16 if kinds == {torch.bfloat16} else MX_SRC_F32
+
     def set_grads(self, grads) -> None:
         """Other gradients of the same parameters, for a program whose gradients are new tensors each step."""
         grads = TensorList(grads)
         if len(grads) != self.count or (self.count and (grads.at != self.at)):
             raise ValueError("one gradient for each parameter, on their device")
+        src = self._grad_src(grads)
         for i, t in enumerate(grads.tensors):
             n = t.numel()
             if n != self.array[i].n:
@@ -958,7 +968,7 @@ class AdamWPlan:
                 raise ValueError(f"gradient {i} overlaps a tensor that the step writes")
         for a, t in zip(self.array, grads.tensors):
             a.g = t.data_ptr()
-        self.grads = grads
+        self.grads, self.grad_src = grads, src
 
     def _one(self, a, i, p, g, m, v, outs, copy, dtype, spans):
         a.n = n = p.numel()
@@ -1045,7 +1055,7 @@ def mx_adamw_step(plan: AdamWPlan, lr, step, betas=(0.9, 0.999), eps: float = 1e
     pscale = None if scale is None else _one_element(scale, torch.float32, at, "scale")
     if plan.count == 0:
         at = _device()
-    _check(load().mx_adamw_step(plan.array, plan.count, plan.src, plan.grads.src, plan.fmt, plan.group,
+    _check(load().mx_adamw_step(plan.array, plan.count, plan.src, plan.grad_src, plan.fmt, plan.group,
                                 ctypes.byref(cfg), pscale, _stream_on(stream, at)))
 
 

@@ -563,6 +563,8 @@ mx_status mx_gemm_glu(const void* qa, const uint8_t* sa, const float* ta, int32_
 typedef struct mx_tensor {
     const void* x;
     int64_t n;
+    int32_t dtype;            /* MX_SRC_F32 / MX_SRC_BF16 */
+    int32_t reserved;         /* must be 0 */
 } mx_tensor;
 
 /*
@@ -574,15 +576,16 @@ typedef struct mx_tensor {
  * sizes fix, with no atomics: the result repeats bit for bit, and no finite
  * gradient's square overflows or vanishes.
  *
- * tensors:  all of `src_dtype`.
+ * tensors:  each with its own type, so that parameters of both types are clipped
+ *        by one norm.
  * max_norm: > 0; Inf does not clip.
  * work:  at least mx_grad_norm_workspace_bytes(count) bytes, 8-byte aligned;
  *        contents undefined afterwards.
  * out:   two fp32 in device memory, 4-byte aligned.
  * Errors: MX_ERR_INVALID_ARG, MX_ERR_ALIGNMENT, MX_ERR_HIP.
  */
-mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, int32_t src_dtype, double max_norm, void* work,
-                       int64_t work_bytes, float* out, void* stream);
+mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, double max_norm, void* work, int64_t work_bytes,
+                       float* out, void* stream);
 
 /* Bytes of workspace mx_grad_norm needs for `count` tensors (0 for a count it refuses). */
 int64_t mx_grad_norm_workspace_bytes(int32_t count);
@@ -622,7 +625,7 @@ enum { MX_STATE_F32 = -1 };
 typedef struct mx_adamw_config {
     double lr;                /* >= 0 */
     double beta1, beta2;      /* in [0, 1) */
-    double eps;               /* >= 0 */
+    double eps;               /* >= 0; below fp32's smallest normal, 2^-126, and not 0, it counts as that */
     double weight_decay;      /* >= 0 */
     int64_t step;             /* t >= 1: 1 at the first step */
     const float* lr_dev;      /* not NULL: lr is read from the device when the step runs */

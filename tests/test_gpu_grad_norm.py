@@ -48,6 +48,13 @@ def test_norm(sizes, dtype, max_norm):
     _check(mx.mx_grad_norm(grads, max_norm=max_norm), grads, max_norm)
 
 
+def test_mixed_types():
+    """Gradients of both types in any order, more than one launch of each."""
+    grads = [g for pair in zip(_make([4097] * 70, torch.float32), _make([1, 9000] * 35, torch.bfloat16, seed=1)) for g in pair]
+    _check(mx.mx_grad_norm(grads, max_norm=1e-3), grads, 1e-3)
+    assert torch.equal(mx.mx_grad_norm(grads), mx.mx_grad_norm(mx.tensor_list(grads)))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_odd_addresses(dtype):
     flat = _make([100000], dtype)[0]

@@ -21,16 +21,15 @@ def lib():
     return mx.load()
 
 
-def _norm(lib, x=P, n=64, count=1, src=0, max_norm=1.0, work=P * 2, nbytes=1 << 20, out=P * 3, array=True):
-    a = (mx.mx_tensor * 2)((P * 5, 64), (x, n))
-    return lib.mx_grad_norm(ctypes.byref(a, ctypes.sizeof(mx.mx_tensor)) if array else None, count, src, max_norm,
-                            work, nbytes, out, None)
+def _norm(lib, x=P, n=64, count=2, src=0, reserved=0, max_norm=1.0, work=P * 2, nbytes=1 << 20, out=P * 3, array=True):
+    a = (mx.mx_tensor * 2)((P * 5, 64, 1, 0), (x, n, src, reserved))
+    return lib.mx_grad_norm(ctypes.byref(a) if array else None, count, max_norm, work, nbytes, out, None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(count=-1), INV), (dict(array=False), INV), (dict(src=2), INV), (dict(max_norm=0.0), INV),
+    (dict(count=-1), INV), (dict(array=False), INV), (dict(src=2), INV), (dict(reserved=1), INV), (dict(max_norm=0.0), INV),
     (dict(max_norm=-1.0), INV), (dict(max_norm=NAN), INV), (dict(work=None), INV), (dict(out=None), INV),
-    (dict(nbytes=8191), INV), (dict(work=P + 4), ALI), (dict(out=P + 2), ALI), (dict(n=-1), INV),
+    (dict(nbytes=16383), INV), (dict(work=P + 4), ALI), (dict(out=P + 2), ALI), (dict(n=-1), INV),
     (dict(n=(1 << 35) + 1), INV), (dict(x=None), INV), (dict(x=P + 2), ALI), (dict(x=P + 1, src=1), ALI),
     (dict(x=P * 2), INV), (dict(x=P * 3), INV),
 ])
@@ -42,7 +41,7 @@ def test_grad_norm_refuses(lib, kw, status):
 def test_grad_norm_workspace_grows_with_the_tensors(lib):
     size = lib.mx_grad_norm_workspace_bytes
     assert size(-1) == 0 and size(0) == size(1) == size(64) > 0
-    assert size(65) == 2 * size(64) and size(1000) == 16 * size(64)
+    assert size(65) == size(64) + size(64) // 2 and size(1000) == 17 * size(64) // 2
 
 
 _IN = dict(p=1, g=2, m=3, v=4, m_amax=5, m_kexp=6, v_amax=7, v_kexp=8)
@@ -150,12 +149,22 @@ def test_plan_refuses_partial_overlap():
         mx.adamw_plan(p, [flat[50:150], g[1]], m, v, out=([flat[:100], torch.zeros(101)], m, v))
 
 
+def test_grads_of_both_types():
+    g = [torch.zeros(5), torch.zeros(7, dtype=torch.bfloat16), torch.zeros(0)]
+    t = mx.tensor_list(g)
+    assert [(t.array[i].x or 0, t.array[i].n, t.array[i].dtype) for i in range(3)] == \
+        [(g[0].data_ptr(), 5, mx.MX_SRC_F32), (g[1].data_ptr(), 7, mx.MX_SRC_BF16), (0, 0, mx.MX_SRC_F32)]
+    p, m, v = ([torch.zeros(n) for n in (5, 7)] for _ in range(3))
+    with pytest.raises(TypeError, match="one type"):
+        mx.adamw_plan(p, g[:2], m, v)
+
+
 def test_set_grads():
     p, g, m, v = _tensors()
     plan = mx.adamw_plan(p, g, m, v)
     new = [torch.zeros(100, dtype=torch.bfloat16), torch.zeros(101, dtype=torch.bfloat16)]
     plan.set_grads(new)
-    assert [plan.array[i].g for i in (0, 1)] == [t.data_ptr() for t in new] and plan.grads.src == mx.MX_SRC_BF16
+    assert [plan.array[i].g for i in (0, 1)] == [t.data_ptr() for t in new] and plan.grad_src == mx.MX_SRC_BF16
     for bad, error in (([new[0]], ValueError), ([new[1], new[0]], ValueError), ([new[0], torch.zeros(101)], TypeError),
                        ([p[0], torch.zeros(101)], ValueError), ([m[0], torch.zeros(101)], ValueError)):
         with pytest.raises(error):
