@@ -19,7 +19,8 @@
 // runs every GEMM whose rows of K hold a multiple of 128 bytes of codes and
 // whose scale arrays are 4-byte aligned, and is the only one with the
 // MX-quantized output.  k_gemm below takes the rest (a ragged last K stage,
-// unaligned scale arrays):
+// unaligned scale arrays).  Both also run mx_gemm_glu for many rows, with a
+// second operand beside B (GLU below).
 //
 // Tiling: 256x256 output tile per 512-thread workgroup (2x4 waves, 128x64
 // per wave = 4x2 MFMA 32x32 tiles, fp32 accumulators in AGPRs).  Two waves
@@ -81,7 +82,7 @@ struct GArgs {
     int reg_path;             // 1: scale arrays not 4-byte aligned -> every stage via registers
 };
 
-// GLU: a second operand beside B, and what the epilogue writes (see glu_slab)
+// GLU: a second operand beside B, and what the epilogue writes (see glu_tile)
 struct GluArgs : GArgs {
     const uint8_t* qu; const uint8_t* su; const float* tu;
     int act;
@@ -827,7 +828,8 @@ __device__ __forceinline__ void store_nt16(void* p, uint4 v)
 // each wave then computes 128 x 64 and the B tile has 128 rows).
 // OUT == GLU: B is Wg, and the tile's 256 "columns" are 128 of gate and the
 // same 128 of up, in runs of 32 rows of Wg, Wg, Wu, Wu for each half: a wave's
-// accumulators j = 0, 1 hold gate and j + 2 up of the same elements.
+// accumulators j = 0, 1 hold gate and j + 2 up of the same elements.  (Half
+// tiles: 64 of each, j = 0 gate and 1 up.)
 template <int FA, int FB, int OUT, int NB>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
@@ -840,7 +842,7 @@ void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
     constexpr int JT = NB / 64;                      // 32-column MFMA tiles per wave (4 or 2)
     constexpr int RB = NB / 32;                      // 32-row load runs of the B tile (8 or 4)
     constexpr int NM = 4 * JT;                       // MFMAs per k-step and wave
-    static_assert(NB == 256 || (NB == 128 && OUT < 2), "half tiles serve the fp32 / bf16 outputs");
+    static_assert(NB == 256 || (NB == 128 && (OUT < 2 || OUT == GLU)), "no half tiles with MX-quantized output");
     constexpr int NT = OUT == GLU ? NB / 2 : NB;     // columns of N that the tile covers
     typedef W4Frag<FP4, JT> Frag;
     __shared__ __align__(16) uint8_t lA0[TILE_BYTES], lA1[TILE_BYTES];
@@ -943,13 +945,16 @@ void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
 
     // fragment reads (same lane layout and swizzle as k_gemm)
     const uint32_t oa = (uint32_t)((wm * 128 + l32) * BKB);
-    const uint32_t ob = (uint32_t)((wn * (NB / 2) + l32) * BKB);
+    // (GLU half tiles: 64 rows of Wg, then of Wu; a wave has 32 of each)
+    constexpr bool GLU_HALF = OUT == GLU && NB == 128;
+    constexpr int WROWS = GLU_HALF ? 32 : NB / 2, BSTEP = GLU_HALF ? 64 : 32;
+    const uint32_t ob = (uint32_t)((wn * WROWS + l32) * BKB);
     const uint32_t hk = (uint32_t)((h ^ swz_key(l32)) << 4);
-    const int rsa = 2 * BM * SBD * h + wm * 128 + l32, rsb = 2 * BM * SBD * h + BM + wn * (NB / 2) + l32;
+    const int rsa = 2 * BM * SBD * h + wm * 128 + l32, rsb = 2 * BM * SBD * h + BM + wn * WROWS + l32;
     // fragment t (0..3: A tile t, 4..7: B tile t-4) of k-step ks: FP8 holds
     // chunks 4ks + h and 4ks + 2 + h of the lane's row, FP4 chunk 2ks + h
     auto rd_frag = [&](Frag& f, const uint8_t* sA, const uint8_t* sB, int ks, int t) __attribute__((always_inline)) {
-        const uint8_t* base = t < 4 ? sA + oa + (t & 3) * 32 * BKB : sB + ob + (t & 3) * 32 * BKB;
+        const uint8_t* base = t < 4 ? sA + oa + (t & 3) * 32 * BKB : sB + ob + (t & 3) * BSTEP * BKB;
         typename KFrag<FP4>::V v;
         if constexpr (FP4) {
             const uint4 v0 = *(const uint4*)(base + ((((uint32_t)(ks * 2)) << 4) ^ hk));
@@ -967,7 +972,7 @@ void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
     auto rd_scale = [&](Frag& f, const uint32_t* sS, int t, int ks) __attribute__((always_inline)) {
         const int d = (ks / 2) * 2 * BM;
         if (t < 4) f.sa[t] = sS[d + rsa + 32 * t];
-        else f.sb[t - 4] = sS[d + rsb + 32 * (t - 4)];
+        else f.sb[t - 4] = sS[d + rsb + BSTEP * (t - 4)];
     };
     auto wr_scales = [&](uint32_t* sS) __attribute__((always_inline)) {
 #pragma unroll
@@ -1173,7 +1178,7 @@ void k_gemm_w4(typename std::conditional<OUT == GLU, GluArgs, GArgs>::type g)
             }
         }
     } else if constexpr (OUT == GLU) {
-        glu_epilogue<JT>(g, acc, m0 + wm * 128, n0 + wn * 64, h, l32);
+        glu_epilogue<JT>(g, acc, m0 + wm * 128, n0 + wn * (NT / 2), h, l32);
     } else if constexpr (OUT >= 2) {
         // MX-quantized output (OUT 2: E4M3, 3: E5M2), 1x32 blocks along the
         // rows of C.  Each wave stages a 32-row slab of its quarter as fp32
@@ -1293,13 +1298,28 @@ hipError_t launch2(const GArgs& a, int out, hipStream_t s)
     }
 }
 
+// mx_gemm_glu's tiles of 256 rows x 64 columns
+int64_t glu_half_tiles(int64_t M, int64_t F) { return ((M + BM - 1) / BM) * ((F + BN / 4 - 1) / (BN / 4)); }
+
 template <int FA, int FB>
 hipError_t launch_glu(const GluArgs& a, hipStream_t s)
 {
     constexpr int EPB = FA == E2M1 ? 2 : 1;
-    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n));
-    if (!a.reg_path && (a.K / EPB) % BKB == 0) k_gemm_w4<FA, FB, GLU, 256><<<grid, dim3(256), 0, s>>>(a);
-    else k_gemm<FA, FB, GLU><<<grid, dim3(512), 0, s>>>(a);
+    if (a.reg_path || (a.K / EPB) % BKB != 0) {
+        k_gemm<FA, FB, GLU><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(512), 0, s>>>(a);
+        return hipGetLastError();
+    }
+    // Half tiles where all of them run at once.  (A last partial round of them
+    // behind whole tiles, in a launch of its own, gains nothing: 3.5 rounds at
+    // 2047 x 4096 x 14336 E2M1 took 159 us, and 158 as four.)
+    const int64_t half = glu_half_tiles(a.M, a.N);
+    if (half <= cu_count()) {
+        GluArgs b = a;
+        b.tiles_n = (int)(half / a.tiles_m);
+        k_gemm_w4<FA, FB, GLU, 128><<<dim3((unsigned)half), dim3(256), 0, s>>>(b);
+    } else {
+        k_gemm_w4<FA, FB, GLU, 256><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
@@ -1309,6 +1329,15 @@ bool gemm_w4_eligible(const GemmJob& j)
 {
     const int64_t kbytes = j.fa == E2M1 ? j.K / 2 : j.K;
     return kbytes % BKB == 0 && (((uintptr_t)j.sa | (uintptr_t)j.sb) & 3u) == 0;
+}
+
+int gemm_glu_rounds(const GemmGluJob& j, bool& half)
+{
+    const int64_t kbytes = j.fa == E2M1 ? j.K / 2 : j.K, cus = cu_count();
+    const bool w4 = kbytes % BKB == 0 && (((uintptr_t)j.sa | (uintptr_t)j.sg | (uintptr_t)j.su) & 3u) == 0;
+    half = w4 && glu_half_tiles(j.M, j.F) <= cus;
+    const int64_t tiles = ((j.M + BM - 1) / BM) * ((j.F + BN / 2 - 1) / (BN / 2));
+    return (int)((tiles + cus - 1) / cus);
 }
 
 hipError_t launch_gemm_glu_tiles(const GemmGluJob& j, hipStream_t stream)

@@ -8,10 +8,10 @@
 //
 // Many rows run on the GEMM kernels (gemm.hip), k_glu_rows below takes few:
 // their time goes to reading the weights once.  The matrix instruction gets 32
-// rows of Wg, then of Wu, as its first operand and up to 32 tokens as its
-// second, so that a lane holds gate and up of the same elements.  A workgroup
-// covers 32 elements of F (one block of a row copy); its waves split K and meet
-// in LDS.
+// rows of Wg, then of Wu, as its first operand and 32 tokens as its second, so
+// that a lane holds gate and up of the same elements.  A workgroup covers 32
+// elements of F (one block of a row copy) and TM tiles of 32 tokens; its waves
+// split K and meet in LDS.
 #include "act_device.h"
 #include "mx_internal.h"
 
@@ -24,7 +24,7 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int WAVES = 4;            // of a workgroup, which split K
 constexpr int UNIT = 128;           // bytes of K a row that a wave takes at a time
-constexpr int ROWS = 32;            // elements of F of a workgroup, and tokens of a tile
+constexpr int ROWS = 32;            // elements of F of a workgroup, tokens of a tile
 constexpr int TILE = ROWS * UNIT;   // bytes of a unit of one operand
 constexpr int PITCH = 33;           // of the joined sums: rows of 32 tokens, one float between
 
@@ -107,7 +107,7 @@ __device__ __forceinline__ float gate_value(int act, float x)
     return a;
 }
 
-template <int FA, int FB>
+template <int FA, int FB, int TM>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
 {
@@ -116,7 +116,7 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
     constexpr int EPB = FP4 ? 2 : 1, UBLOCKS = UNIT * EPB / 32;      // blocks of a unit
     constexpr int STEPS = UNIT * EPB / 64;                           // MFMA steps of a unit
     typedef Unit<FP4> U;
-    __shared__ __align__(16) uint8_t lds[WAVES][3 * TILE];
+    __shared__ __align__(16) uint8_t lds[WAVES][(2 + TM) * TILE];
     static_assert(sizeof lds >= WAVES * 2 * ROWS * PITCH * sizeof(float), "the joined sums take the place of the units");
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -124,28 +124,36 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
     // the tiles of tokens of one set of weights run one after the other on one XCD
     const int wg = blockIdx.x, tf = wg / (8 * tiles_m) * 8 + wg % 8, tm = wg / 8 % tiles_m;
     if (tf >= tiles_f) return;
-    const int64_t f0 = (int64_t)tf * ROWS, m0 = (int64_t)tm * ROWS;
+    const int64_t f0 = (int64_t)tf * ROWS, m0 = (int64_t)tm * (TM * ROWS);
     const int64_t kbytes = g.K / EPB, kblocks = g.K / 32;
     const int units = (int)(kbytes / UNIT), rest = (int)(kbytes % UNIT);   // whole ones, bytes of the last
 
     // codes: buffer loads over the tile's rows (at most 2^28 bytes), so that
     // rows past the end are zero and not fetched; their scales are the last row's
     auto rsrc = [&](const uint8_t* base, int64_t first, int64_t rows) __attribute__((always_inline)) {
-        const int64_t n = min(rows - first, (int64_t)ROWS) * kbytes;
+        const int64_t n = max(min(rows - first, (int64_t)ROWS), (int64_t)0) * kbytes;
         return __builtin_amdgcn_make_buffer_rsrc((void*)(base + first * kbytes), (short)0, (int)(uint32_t)n, 0x00020000);
     };
-    const auto rg = rsrc(g.qg, f0, g.F), ru = rsrc(g.qu, f0, g.F), rt = rsrc(g.qa, m0, g.M);
-    const int64_t wrow = min(f0 + l32, g.F - 1), trow = min(m0 + l32, g.M - 1);
-    const uint8_t *sg = g.sg + wrow * kblocks, *su = g.su + wrow * kblocks, *st = g.sa + trow * kblocks;
+    const auto rg = rsrc(g.qg, f0, g.F), ru = rsrc(g.qu, f0, g.F);
+    const int64_t wrow = min(f0 + l32, g.F - 1);
+    const uint8_t *sg = g.sg + wrow * kblocks, *su = g.su + wrow * kblocks, *st[TM];
+    __amdgpu_buffer_rsrc_t rt[TM];
+#pragma unroll
+    for (int i = 0; i < TM; i++) {
+        rt[i] = rsrc(g.qa, m0 + i * ROWS, g.M);
+        st[i] = g.sa + min(m0 + i * ROWS + l32, g.M - 1) * kblocks;
+    }
     const uint32_t voff = (uint32_t)((lane >> 3) * kbytes + (lane & 7) * 16), run = (uint32_t)(8 * kbytes);
 
-    f16v acc[2];
+    f16v acc[TM][2];
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int t = 0; t < TM; t++)
 #pragma unroll
-        for (int r = 0; r < 16; r++) acc[i][r] = 0.0f;
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) acc[t][i][r] = 0.0f;
 
-    struct Stage { U g, u, t; };
+    struct Stage { U g, u, t[TM]; };
     auto load_codes = [&](U& x, __amdgpu_buffer_rsrc_t r, uint32_t at, int u) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < 4; p++)
@@ -160,11 +168,13 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
         const uint32_t off = i < n ? voff : OUTSIDE;
         load_codes(s.g, rg, off, u);
         load_codes(s.u, ru, off, u);
-        load_codes(s.t, rt, off, u);
+#pragma unroll
+        for (int t = 0; t < TM; t++) load_codes(s.t[t], rt[t], off, u);
         const int64_t at = (int64_t)u * UBLOCKS;
         __builtin_memcpy(s.g.s, sg + at, sizeof s.g.s);              // (at any address)
         __builtin_memcpy(s.u.s, su + at, sizeof s.u.s);
-        __builtin_memcpy(s.t.s, st + at, sizeof s.t.s);
+#pragma unroll
+        for (int t = 0; t < TM; t++) __builtin_memcpy(s.t[t].s, st[t] + at, sizeof s.t[t].s);
     };
     uint8_t* const mine = lds[wave];
     const int wat = swz(lane >> 3, lane & 7);                         // (rows 8 apart: the key's other bits below)
@@ -176,14 +186,18 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
 #pragma unroll
         for (int k = 0; k < STEPS; k++) {
             const int8v xg = source<FP4>(mine, k, l32, h), xu = source<FP4>(mine + TILE, k, l32, h);
-            const int8v xt = source<FP4>(mine + 2 * TILE, k, l32, h);
-            const int a = (int)(s.g.s[k / 2] >> (8 * h)), b = (int)(s.u.s[k / 2] >> (8 * h)), c = (int)(s.t.s[k / 2] >> (8 * h));
-            if (k % 2 == 0) {
-                acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xg, xt, acc[0], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 0, a, 0, c);
-                acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xu, xt, acc[1], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 0, b, 0, c);
-            } else {
-                acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xg, xt, acc[0], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 2, a, 2, c);
-                acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xu, xt, acc[1], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 2, b, 2, c);
+            const int a = (int)(s.g.s[k / 2] >> (8 * h)), b = (int)(s.u.s[k / 2] >> (8 * h));
+#pragma unroll
+            for (int t = 0; t < TM; t++) {
+                const int8v xt = source<FP4>(mine + (2 + t) * TILE, k, l32, h);
+                const int c = (int)(s.t[t].s[k / 2] >> (8 * h));
+                if (k % 2 == 0) {
+                    acc[t][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xg, xt, acc[t][0], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 0, a, 0, c);
+                    acc[t][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xu, xt, acc[t][1], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 0, b, 0, c);
+                } else {
+                    acc[t][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xg, xt, acc[t][0], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 2, a, 2, c);
+                    acc[t][1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xu, xt, acc[t][1], MfmaFmt<FB>::code, MfmaFmt<FA>::code, 2, b, 2, c);
+                }
             }
         }
     };
@@ -193,7 +207,8 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         put(s.g, mine);
         put(s.u, mine + TILE);
-        put(s.t, mine + 2 * TILE);
+#pragma unroll
+        for (int t = 0; t < TM; t++) put(s.t[t], mine + (2 + t) * TILE);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
     // one unit: to LDS, its registers free for unit i, its products
@@ -202,7 +217,8 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
         Stage scales;
         __builtin_memcpy(scales.g.s, s.g.s, sizeof s.g.s);
         __builtin_memcpy(scales.u.s, s.u.s, sizeof s.u.s);
-        __builtin_memcpy(scales.t.s, s.t.s, sizeof s.t.s);
+#pragma unroll
+        for (int t = 0; t < TM; t++) __builtin_memcpy(scales.t[t].s, s.t[t].s, sizeof s.t[t].s);
         load(s, i);
         multiply(scales);
     };
@@ -223,31 +239,26 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
         const uint32_t at = (lane & 7) * 16 < rest ? voff : OUTSIDE;
         load_codes(a.g, rg, at, units);
         load_codes(a.u, ru, at, units);
-        load_codes(a.t, rt, at, units);
 #pragma unroll
-        for (int d = 0; d < U::DWORDS; d++) {
-            a.g.s[d] = a.u.s[d] = a.t.s[d] = 0;
+        for (int t = 0; t < TM; t++) load_codes(a.t[t], rt[t], at, units);
+        auto scales = [&](U& x, const uint8_t* from) __attribute__((always_inline)) {
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int64_t block = (int64_t)units * UBLOCKS + 4 * d + k;
-                const bool in = block < kblocks;
-                a.g.s[d] |= (in ? (uint32_t)sg[block] : 127u) << (8 * k);
-                a.u.s[d] |= (in ? (uint32_t)su[block] : 127u) << (8 * k);
-                a.t.s[d] |= (in ? (uint32_t)st[block] : 127u) << (8 * k);
+            for (int d = 0; d < U::DWORDS; d++) {
+                x.s[d] = 0;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int64_t block = (int64_t)units * UBLOCKS + 4 * d + k;
+                    x.s[d] |= (block < kblocks ? (uint32_t)from[block] : 127u) << (8 * k);
+                }
             }
-        }
+        };
+        scales(a.g, sg);
+        scales(a.u, su);
+#pragma unroll
+        for (int t = 0; t < TM; t++) scales(a.t[t], st[t]);
         put_all(a);
         multiply(a);
     }
-
-    // join: [wave][row of the two MFMA tiles][token], in the units' place
-    float* const red = (float*)&lds[0][0];
-    constexpr int PART = 2 * ROWS * PITCH;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int r = 0; r < 16; r++) red[wave * PART + (ROWS * i + 8 * (r / 4) + 4 * h + r % 4) * PITCH + l32] = acc[i][r];
 
     float common = g.alpha;
     if (g.ta) common = common * *g.ta;
@@ -255,68 +266,97 @@ void k_glu_rows(const GemmGluJob g, int tiles_f, int tiles_m)
     if (g.tg) ag = ag * *g.tg;
     if (g.tu) au = au * *g.tu;
     if (g.hadamard_k) ag = ag * 0.03125f, au = au * 0.03125f;
-    __syncthreads();
 
-    // thread t: tokens t / 16 and 16 further on, elements 2 (t % 16) and the next
+    // join, a tile of tokens at a time: [wave][row of the two MFMA tiles][token],
+    // in the units' place
+    float* const red = (float*)&lds[0][0];
+    constexpr int PART = 2 * ROWS * PITCH;
     const int pair = 2 * (threadIdx.x & 15);
 #pragma unroll
-    for (int token = threadIdx.x >> 4; token < ROWS; token += 4 * WAVES) {
-        float gv[2] = {0.0f, 0.0f}, uv[2] = {0.0f, 0.0f}, hv[2];
+    for (int t = 0; t < TM; t++) {
+        if (m0 + t * ROWS >= g.M) break;
+        __syncthreads();
 #pragma unroll
-        for (int w = 0; w < WAVES; w++)
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int r = 0; r < 16; r++)
+                red[wave * PART + (ROWS * i + 8 * (r / 4) + 4 * h + r % 4) * PITCH + l32] = acc[t][i][r];
+        __syncthreads();
+        // thread x: tokens x / 16 and 16 further on, elements 2 (x % 16) and the next
+#pragma unroll
+        for (int token = threadIdx.x >> 4; token < ROWS; token += 4 * WAVES) {
+            float gv[2] = {0.0f, 0.0f}, uv[2] = {0.0f, 0.0f}, hv[2];
+#pragma unroll
+            for (int w = 0; w < WAVES; w++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    gv[e] += red[w * PART + (pair + e) * PITCH + token];
+                    uv[e] += red[w * PART + (ROWS + pair + e) * PITCH + token];
+                }
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                gv[e] += red[w * PART + (pair + e) * PITCH + token];
-                uv[e] += red[w * PART + (ROWS + pair + e) * PITCH + token];
+                gv[e] *= ag;
+                uv[e] *= au;
+                hv[e] = gate_value(g.act, gv[e]) * uv[e];
             }
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            gv[e] *= ag;
-            uv[e] *= au;
-            hv[e] = gate_value(g.act, gv[e]) * uv[e];
-        }
-        const int64_t m = m0 + token, f = f0 + pair;
-        const bool row = m < g.M, first = row && f < g.F, second = row && f + 1 < g.F;
-        if (g.h) emit_pair(g.out_f32, g.h, m * g.ld_h + f, hv[0], hv[1], first, second);
-        if (g.gate) {
-            emit_pair(g.out_f32, g.gate, m * g.ld_gate + f, gv[0], gv[1], first, second);
-            emit_pair(g.out_f32, g.up, m * g.ld_up + f, uv[0], uv[1], first, second);
-        }
-        // (F is then a multiple of 32: a block is there whole or not at all)
-        if (g.qh) emit_codes(g.h_fmt, hv[0], hv[1], first, m * g.F + f, g.qh, g.sh);
-        if (g.qgc) {
-            emit_codes(g.ckpt_fmt, gv[0], gv[1], first, m * g.F + f, g.qgc, g.sgc);
-            emit_codes(g.ckpt_fmt, uv[0], uv[1], first, m * g.F + f, g.quc, g.suc);
+            const int64_t m = m0 + t * ROWS + token, f = f0 + pair;
+            const bool row = m < g.M, first = row && f < g.F, second = row && f + 1 < g.F;
+            if (g.h) emit_pair(g.out_f32, g.h, m * g.ld_h + f, hv[0], hv[1], first, second);
+            if (g.gate) {
+                emit_pair(g.out_f32, g.gate, m * g.ld_gate + f, gv[0], gv[1], first, second);
+                emit_pair(g.out_f32, g.up, m * g.ld_up + f, uv[0], uv[1], first, second);
+            }
+            // (F is then a multiple of 32: a block is there whole or not at all)
+            if (g.qh) emit_codes(g.h_fmt, hv[0], hv[1], first, m * g.F + f, g.qh, g.sh);
+            if (g.qgc) {
+                emit_codes(g.ckpt_fmt, gv[0], gv[1], first, m * g.F + f, g.qgc, g.sgc);
+                emit_codes(g.ckpt_fmt, uv[0], uv[1], first, m * g.F + f, g.quc, g.suc);
+            }
         }
     }
 #endif
 }
 
-template <int FA, int FB>
+template <int FA, int FB, int TM>
 hipError_t launch_rows(const GemmGluJob& j, hipStream_t s)
 {
-    const int tiles_f = (int)((j.F + ROWS - 1) / ROWS), tiles_m = (int)((j.M + ROWS - 1) / ROWS);
+    const int tiles_f = (int)((j.F + ROWS - 1) / ROWS), tiles_m = (int)((j.M + TM * ROWS - 1) / (TM * ROWS));
     const unsigned grid = (unsigned)((tiles_f + 7) / 8 * 8) * (unsigned)tiles_m;
-    k_glu_rows<FA, FB><<<grid, 64 * WAVES, 0, s>>>(j, tiles_f, tiles_m);
+    k_glu_rows<FA, FB, TM><<<grid, 64 * WAVES, 0, s>>>(j, tiles_f, tiles_m);
     return hipGetLastError();
+}
+
+template <int TM>
+hipError_t launch_rows(const GemmGluJob& j, hipStream_t s)
+{
+    if (j.fa == E2M1) return launch_rows<E2M1, E2M1, TM>(j, s);
+    if (j.fa == E4M3) return j.fb == E4M3 ? launch_rows<E4M3, E4M3, TM>(j, s) : launch_rows<E4M3, E5M2, TM>(j, s);
+    return j.fb == E4M3 ? launch_rows<E5M2, E4M3, TM>(j, s) : launch_rows<E5M2, E5M2, TM>(j, s);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_glu(const GemmGluJob& j, hipStream_t s)
 {
-    // k_glu_rows takes a time in proportion to its workgroups (32 rows x 32
-    // elements), the GEMM kernels one in proportion to their rounds of a 256 x
-    // 128 tile on each CU, both in proportion to K.  At F = 14336, K = 4096, by
-    // rows and by tiles: M = 64 (896 workgroups) E4M3 37-48 and 51-65 us, E2M1
-    // 24 and 36; M = 96 (1344) 64 and 66, 32 and 38; M = 128 (1792) 58-73 and
-    // 51-70, 37 and 36; M = 256 127 and 51-76, 65 and 36.
-    const int64_t wgs = ((j.M + ROWS - 1) / ROWS) * ((j.F + ROWS - 1) / ROWS);
-    const int64_t rounds = (((j.M + 255) / 256) * ((j.F + 127) / 128) + 255) / 256;
-    if (wgs > 6 * 256 * rounds) return launch_gemm_glu_tiles(j, s);
-    if (j.fa == E2M1) return launch_rows<E2M1, E2M1>(j, s);
-    if (j.fa == E4M3) return j.fb == E4M3 ? launch_rows<E4M3, E4M3>(j, s) : launch_rows<E4M3, E5M2>(j, s);
-    return j.fb == E4M3 ? launch_rows<E5M2, E4M3>(j, s) : launch_rows<E5M2, E5M2>(j, s);
+    // Workgroups of 32 tokens that all run at once (one on each CU) are left
+    // narrow, more of them take two tiles of tokens (n: how many there are then).
+    // At F = 4096, K = 2048 E4M3, 32 and 64 tokens a workgroup: M = 64 8.1 and
+    // 10.5 us, M = 128 12.7 and 10.8, M = 256 22 and 17; at F = 14336, K = 4096:
+    // M = 64 48 and 41 (E2M1 22.5 and 18.9).  Four tiles were no better: M = 128
+    // 61 us, two 60.
+    const int64_t tiles_f = (j.F + ROWS - 1) / ROWS, n = (j.M + 2 * ROWS - 1) / (2 * ROWS) * tiles_f;
+    const bool narrow = j.M <= ROWS || (j.M + ROWS - 1) / ROWS * tiles_f <= 256;
+    // These take a time in proportion to n, the GEMM kernels one in proportion to
+    // their rounds, all in proportion to K.  Rows and tiles: where one round of
+    // half tiles is enough (F = 2048, K = 4096 E4M3) n = 512 25 and 33 us, n =
+    // 1024 46 and 34 (E2M1 17 and 20, 28 and 21); F = 14336 n = 448 41 and 43, n =
+    // 896 54 and 44; else, a round (F = 28672 and 65536) n = 896 74.5 and 74.7 (E2M1
+    // 41-44 and 44), n = 1024 74-77 and 78 (47 and 56), n = 1792 103 and 77; K not a
+    // multiple of 128 bytes n = 896 69 and 82, n = 1792 100 and 98.
+    bool half;
+    const int64_t rounds = gemm_glu_rounds(j, half);
+    if (n > (half ? 640 : 1024 * rounds)) return launch_gemm_glu_tiles(j, s);
+    return narrow ? launch_rows<1>(j, s) : launch_rows<2>(j, s);
 }
 
 }  // namespace mx

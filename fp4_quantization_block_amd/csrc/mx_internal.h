@@ -140,6 +140,8 @@ hipError_t launch_gemm_glu(const GemmGluJob& j, hipStream_t stream);
 
 // the form for many rows (gemm.hip): tiles of 256 rows x 128 elements of F
 hipError_t launch_gemm_glu_tiles(const GemmGluJob& j, hipStream_t stream);
+// rounds of its tiles over the CUs; half: they are half tiles, in one round
+int gemm_glu_rounds(const GemmGluJob& j, bool& half);
 
 // norm forward: s = x (+ residual, rounded; written to sum), its statistics,
 // y and / or the row copy of y, and the checkpoint (row copy) of s

@@ -87,10 +87,13 @@ def _check(op, act="silu", alpha=1.0, fmts=("e4m3", "e5m2"), what=""):
 
 
 # Rows around the tiles of tokens, F around the tiles of weights, K around the units of 128 bytes and the workgroup's
-# waves, for the kernel for few rows; from over 1536 tiles of 32 x 32 on, the GEMM kernels' 256 x 128 tiles, with K that
-# the faster of the two takes (whole stages) and does not take.
+# waves, for the kernel for few rows, with one tile of tokens to a workgroup (at most 256 of them) and with two; from over
+# 640 workgroups of two on, K in whole stages, the faster GEMM kernel's half tiles of 256 x 64 (at most 256 of them);
+# from over 1024 on, its tiles of 256 x 128, or the other GEMM kernel's for K that it does not take.
+WIDE = [(100, 2528, 256), (70, 2817, 160), (65, 4100, 96), (127, 2560, 1152), (40, 6176, 64)]
+FULL = [(4100, 1056, 256), (4097, 1043, 128), (4356, 1090, 512), (4100, 1056, 96), (4351, 1025, 416)]
 TALL = [(2060, 896, 128), (2049, 1000, 256), (2300, 901, 768), (2060, 960, 96), (2305, 897, 224), (2057, 928, 416)]
-SHAPES = TALL + [(1, 32, 32), (1, 1, 64), (2, 33, 96), (31, 64, 128), (32, 31, 160), (33, 96, 1024), (64, 257, 1056),
+SHAPES = WIDE + FULL + TALL + [(1, 32, 32), (1, 1, 64), (2, 33, 96), (31, 64, 128), (32, 31, 160), (33, 96, 1024), (64, 257, 1056),
           (65, 128, 1152), (7, 320, 2304), (300, 200, 96), (257, 513, 384), (129, 260, 640), (512, 384, 512),
           (255, 160, 256), (520, 130, 224)]
 
@@ -102,30 +105,35 @@ def test_shapes(shape, fa, fb):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
-@pytest.mark.parametrize("shape", [(3, 96, 256), (2060, 896, 256), (2060, 896, 160)], ids=str)
+@pytest.mark.parametrize("shape", [(3, 96, 256), (2060, 896, 256), (2060, 896, 160), (100, 2528, 256), (4100, 1056, 256),
+                                   (4100, 1056, 160)], ids=str)
 def test_activations(act, shape):
     _check(Operands(*shape, seed=3), act=act, alpha=3.0, fmts=("e5m2", "e4m3"), what=act)
 
 
 @pytest.mark.parametrize("fa,fb", [("e4m3", "e5m2"), ("e5m2", "e5m2")])
-@pytest.mark.parametrize("shape", [(9, 64, 288), (2060, 896, 384), (2060, 896, 288)], ids=str)
+@pytest.mark.parametrize("shape", [(9, 64, 288), (2060, 896, 384), (2060, 896, 288), (100, 2528, 288), (4100, 1056, 384),
+                                   (4100, 1056, 288)], ids=str)
 def test_formats(fa, fb, shape):
     _check(Operands(*shape, fa, fb, seed=4), what=f"{fa} {fb}")
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
-@pytest.mark.parametrize("shape", [(5, 160, 512), (2060, 896, 256), (2060, 896, 96)], ids=str)
+@pytest.mark.parametrize("shape", [(5, 160, 512), (2060, 896, 256), (2060, 896, 96), (100, 2528, 512), (4100, 1056, 256),
+                                   (4100, 1056, 96)], ids=str)
 def test_hadamard_tensor_scales_and_alpha(fmt, shape):
     _check(Operands(*shape, fmt, fmt, hadamard=True, two_level=True, seed=5), alpha=0.75, what="all factors")
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
-@pytest.mark.parametrize("shape", [(5, 96, 512), (2060, 896, 256), (2060, 896, 160)], ids=str)
+@pytest.mark.parametrize("shape", [(5, 96, 512), (2060, 896, 256), (2060, 896, 160), (100, 2528, 512), (4100, 1056, 256),
+                                   (4100, 1056, 160)], ids=str)
 def test_unaligned_scales(fmt, shape):
     _check(Operands(*shape, fmt, fmt, unaligned=True, seed=6), what="scales from an odd address on")
 
 
-@pytest.mark.parametrize("M,F,K", [(3, 77, 256), (1, 40, 256), (2060, 911, 256), (2060, 911, 96)])
+@pytest.mark.parametrize("M,F,K", [(3, 77, 256), (1, 40, 256), (2060, 911, 256), (2060, 911, 96), (70, 2817, 256),
+                                   (4099, 1043, 256), (4099, 1043, 96)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_strided_outputs_stay_inside(M, F, K, dtype):
     op = Operands(M, F, K, seed=7)
@@ -137,7 +145,8 @@ def test_strided_outputs_stay_inside(M, F, K, dtype):
         v.check(k)
 
 
-@pytest.mark.parametrize("M,F,K", [(3, 96, 256), (2060, 928, 256), (2060, 928, 96)])
+@pytest.mark.parametrize("M,F,K", [(3, 96, 256), (2060, 928, 256), (2060, 928, 96), (70, 2816, 256), (4099, 1056, 256),
+                                   (4099, 1056, 96)])
 def test_copies_stay_inside(M, F, K):
     op = Operands(M, F, K, seed=8)
     want = op.run(h_fmt="e4m3", ckpt_fmt="e4m3")
@@ -153,7 +162,8 @@ def test_copies_stay_inside(M, F, K):
         assert torch.all(bs[:3] == 9) and torch.all(bs[3 + M * F // 32:] == 9)
 
 
-@pytest.mark.parametrize("M,F,K", [(4, 96, 512), (4, 96, 160), (2060, 896, 512), (2060, 896, 160)])
+@pytest.mark.parametrize("M,F,K", [(4, 96, 512), (4, 96, 160), (2060, 896, 512), (2060, 896, 160), (70, 2816, 512),
+                                   (4099, 1056, 512), (4099, 1056, 160)])
 def test_non_finite_rows_and_columns(M, F, K):
     """A NaN block makes its row (of A) or its column (of a weight) NaN, and nothing else."""
     op = Operands(M, F, K, seed=9)
@@ -182,7 +192,7 @@ def test_zero_operands():
         assert not r.h.any() and not r.gate.any() and not r.qh.bitwise_and(0x7F).any() and not r.sh.any()
 
 
-@pytest.mark.parametrize("M,F", [(1, 96), (24, 96), (2060, 896)])
+@pytest.mark.parametrize("M,F", [(1, 96), (24, 96), (2060, 896), (70, 2816), (4099, 1056)])
 def test_graph_on_a_side_stream(M, F):
     op = Operands(M, F, 512, seed=11)
     qh, sh = (torch.empty(M, n, dtype=torch.uint8, device=DEV) for n in (F, F // 32))
