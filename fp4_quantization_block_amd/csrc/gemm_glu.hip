@@ -355,7 +355,8 @@ hipError_t launch_gemm_glu(const GemmGluJob& j, hipStream_t s)
     // multiple of 128 bytes n = 896 69 and 82, n = 1792 100 and 98.
     bool half;
     const int64_t rounds = gemm_glu_rounds(j, half);
-    if (n > (half ? 640 : 1024 * rounds)) return launch_gemm_glu_tiles(j, s);
+    // (The launch counts its threads with 32 bits, and pads tiles_f to eight.)
+    if (n > (half ? 640 : 1024 * rounds) || n > 1 << 20) return launch_gemm_glu_tiles(j, s);
     return narrow ? launch_rows<1>(j, s) : launch_rows<2>(j, s);
 }
 

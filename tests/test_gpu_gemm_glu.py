@@ -242,6 +242,19 @@ def test_full_size_entries(M, F, K, fmt):
             check_model(got, rule, bound, K, "entries")
 
 
+def test_very_many_rows_of_few_columns():
+    """More rows than the kernel for few of them could be launched with (8 workgroups of 256 threads for 64 rows here)."""
+    M, F, K, base = (1 << 27) + 5, 32, 32, 1 << 20
+    op = Operands(base, F, K, seed=13)
+    want = op.run().h
+    reps = M // base
+    qa, sa = (torch.cat([x.repeat(reps, 1), x[:M - reps * base]]) for x in op.a[:2])
+    got = mx.mx_gemm_glu(qa, sa, None, "e4m3", *op.gate, *op.up, "e4m3", M, F, K).h
+    for i in range(reps):
+        assert torch.equal(got[i * base:(i + 1) * base], want), i
+    assert torch.equal(got[reps * base:], want[:M - reps * base])
+
+
 def test_backward_reads_what_it_keeps():
     """The backward from the checkpoints, and from the tensors, is the one of mx_glu_forward's."""
     op = Operands(2080, 896, 512, seed=14)
