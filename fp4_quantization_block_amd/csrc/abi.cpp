@@ -715,7 +715,7 @@ mx_status mx_gemm_glu(const void* qa, const uint8_t* sa, const float* ta, int32_
     g_msg[0] = '\0';
     mx_status s = check_gemm_operands(qa, sa, ta, fa, qg, sg, tg, fb, M, F, K, hadamard_k);
     if (s != MX_OK || (s = check_gemm_operands(qa, sa, ta, fa, qu, su, tu, fb, M, F, K, hadamard_k)) != MX_OK) return s;
-    // (a launch counts its threads with 32 bits: at most 512 to a tile, or 256 to 32 x 32 of it, six at most)
+    // (a launch counts its threads with 32 bits: 512 to a tile at most)
     if (((M + 255) / 256) * ((F + 127) / 128) >= (int64_t)1 << 21)
         return fail(MX_ERR_INVALID_ARG, "M x F must be fewer than 2^21 output tiles of 256 x 128");
     if ((s = check_act(act)) != MX_OK) return s;
@@ -807,6 +807,9 @@ mx_status mx_grad_norm(const mx_tensor* tensors, int32_t count, double max_norm,
         return fail(MX_ERR_INVALID_ARG, "work is smaller than mx_grad_norm_workspace_bytes()");
     if ((reinterpret_cast<uintptr_t>(work) & 7u) != 0 || off4(out))
         return fail(MX_ERR_ALIGNMENT, "work must be 8-byte and out 4-byte aligned");
+    const uint8_t *w = (const uint8_t*)work, *o = (const uint8_t*)out;
+    if (o + 2 * sizeof(float) > w && o < w + mx_grad_norm_workspace_bytes(count))
+        return fail(MX_ERR_INVALID_ARG, "out must not lie in work");
     for (int32_t i = 0; i < count; i++) {
         if ((s = check_length(tensors[i].n)) != MX_OK || (s = check_source_dtype(tensors[i].dtype)) != MX_OK) return s;
         if (tensors[i].reserved != 0) return fail(MX_ERR_INVALID_ARG, "reserved field must be 0");

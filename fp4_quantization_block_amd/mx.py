@@ -902,7 +902,7 @@ def mx_grad_norm(grads, max_norm: float = float("inf"), out: Optional[torch.Tens
     if n == 0:
         at = _device() if out is None else out.get_device()
     if out is None:
-        out = torch.empty(2, dtype=torch.float32, device=f"cuda:{at}") if n == 0 or at < 0 else \
+        out = torch.empty(2, dtype=torch.float32, device=f"cuda:{at}") if n == 0 else \
             grads.tensors[0].new_empty_strided((2,), (1,), dtype=torch.float32)
     if work is None:
         nbytes = grads.nbytes

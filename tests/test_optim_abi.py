@@ -32,6 +32,7 @@ def _norm(lib, x=P, n=64, count=2, src=0, reserved=0, max_norm=1.0, work=P * 2, 
     (dict(nbytes=16383), INV), (dict(work=P + 4), ALI), (dict(out=P + 2), ALI), (dict(n=-1), INV),
     (dict(n=(1 << 35) + 1), INV), (dict(x=None), INV), (dict(x=P + 2), ALI), (dict(x=P + 1, src=1), ALI),
     (dict(x=P * 2), INV), (dict(x=P * 3), INV),
+    (dict(out=P * 2), INV), (dict(out=P * 2 + 16380), INV), (dict(out=P * 2 - 4), INV),
 ])
 def test_grad_norm_refuses(lib, kw, status):
     assert _norm(lib, **kw) == status

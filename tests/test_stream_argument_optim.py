@@ -1,0 +1,30 @@
+"""Calls with stream= of the fused projections and the gradient norm: their results and workspaces
+belong to the stream that the kernels run on (test_stream_argument.py says why)."""
+import pytest
+import torch
+
+from fp4_quantization_block_amd import mx
+from test_stream_argument import CODES, COLS, ROWS, SCALES, V, X, _check, world  # noqa: F401
+
+A = (CODES, SCALES, None)
+
+
+def _glu(stream, **kw):
+    return mx.mx_gemm_glu(*A, "e4m3", *A, *A, "e4m3", ROWS, ROWS, COLS, stream=stream, **kw)
+
+
+@pytest.mark.parametrize("kw,new", [
+    (dict(), 1), (dict(keep=True), 3), (dict(write_h=False, h_fmt="e4m3"), 2),
+    (dict(h_fmt="e4m3", keep=True, ckpt_fmt="e5m2"), 9),
+    (dict(h=torch.zeros(ROWS, ROWS, dtype=torch.bfloat16), ckpt_fmt="e4m3"), 4),
+])
+def test_gemm_glu(world, kw, new):                # noqa: F811
+    _check(world, lambda s: _glu(s, **kw), new)
+
+
+def test_grad_norm(world):                        # noqa: F811
+    _check(world, lambda s: mx.mx_grad_norm([X, V], stream=s), 1)
+
+
+def test_grad_norm_into_a_given_tensor(world):    # noqa: F811
+    _check(world, lambda s: mx.mx_grad_norm([X, V], out=torch.zeros(2), stream=s), 0)
