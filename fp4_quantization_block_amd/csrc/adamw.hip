@@ -31,6 +31,12 @@ constexpr int64_t SMALL_STEP = 1 << 22;  // elements of a launch below which it 
 // go to a launch of their own (2^25 + 5 in one tensor: 121 against 128 us; 2^24 +
 // 5: 65 against 59, the second launch).
 constexpr int64_t SPLIT_STEP = 1 << 25;
+// Below so many elements a launch, 4 or 8 elements a lane instead of 16, with
+// chunks of 1024 or 2048: a lane's chain of operations is shorter and more waves
+// share the chip.  One tensor of 2^16 + 5, 2^19 + 5, 2^20 + 5, 2^22 + 5 and 2^23 + 5
+// elements: 5.8, 7.0, 10.6, 28.4 and 50.0 us with 4; 7.2, 8.1, 8.9, 22.5 and 38.6
+// with 8; 10.2, 10.8, 11.9, 24.2 and 35.9 with 16.
+constexpr int64_t FEW_8 = 1 << 20, SMALL_8 = 6 << 20;
 constexpr int MOST_CHUNKS = 1 << 23;    // of a launch (a launch counts its threads with 32 bits)
 
 // ---------------------------------------------------------------------------
@@ -253,8 +259,8 @@ __global__ __launch_bounds__(256) void k_adamw32(const Tab table, const AdamComm
 }
 
 // ---------------------------------------------------------------------------
-// moments in FP8.  T = G / 16 neighbouring lanes hold a group; lane j of them
-// the float4s (and code words) j, j + T, j + 2 T, j + 3 T of it.  A group that
+// moments in FP8.  T = G / (4 NV) neighbouring lanes hold a group; lane j of them
+// the NV float4s (and code words) j, j + T, j + 2 T, ... of it.  A group that
 // the tensor's end cuts short is completed with zeros, which change neither
 // its largest nor its smallest nonzero magnitude; their codes are not written.
 // ---------------------------------------------------------------------------
@@ -284,11 +290,11 @@ __device__ __forceinline__ void store_codes(uint8_t* q, int at, int here, uint32
 // conversion of the one before
 struct Raw4 { uint32_t w[4]; };
 
-template <typename E>
-__device__ __forceinline__ void load_raw(const E* x, int at, int here, int stride, Raw4 (&r)[4])
+template <typename E, int NV>
+__device__ __forceinline__ void load_raw(const E* x, int at, int here, int stride, Raw4 (&r)[NV])
 {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < NV; i++) {
         const int k = at + i * stride;
         if (k + 4 <= here) {
             __builtin_memcpy(r[i].w, x + (uint32_t)k, 4 * sizeof(E));
@@ -301,14 +307,15 @@ __device__ __forceinline__ void load_raw(const E* x, int at, int here, int strid
     }
 }
 
-__device__ __forceinline__ void raw_values(int src, const Raw4 (&r)[4], float (&v)[16])
+template <int NV>
+__device__ __forceinline__ void raw_values(int src, const Raw4 (&r)[NV], float (&v)[4 * NV])
 {
     if (src == SRC_F32) {
 #pragma unroll
-        for (int e = 0; e < 16; e++) v[e] = __uint_as_float(r[e / 4].w[e % 4]);
+        for (int e = 0; e < 4 * NV; e++) v[e] = __uint_as_float(r[e / 4].w[e % 4]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
+        for (int e = 0; e < 4 * NV; e++) {
             const uint32_t w = r[e / 4].w[e % 4 / 2];
             v[e] = e % 2 ? bf16_hi(w) : bf16_lo(w);
         }
@@ -317,20 +324,20 @@ __device__ __forceinline__ void raw_values(int src, const Raw4 (&r)[4], float (&
 
 // One chunk of a workgroup; WHOLE: all of it lies inside the tensor.  The second
 // moment is done with before the first is begun, which holds fewer registers.
-template <int FMT, int G, bool WHOLE>
+template <int FMT, int G, bool WHOLE, int NV>
 __device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c, const float (&lg)[256], int64_t chunk, int psrc,
                                              int gsrc)
 {
-    constexpr int T = G / 16, STRIDE = 4 * T;    // the lane's words lie STRIDE elements apart
-    const int here = WHOLE ? CHUNK : (int)(t.n - chunk);
+    constexpr int E = 4 * NV, T = G / E, STRIDE = 4 * T;    // the lane's words lie STRIDE elements apart
+    const int here = WHOLE ? 256 * E : (int)(t.n - chunk);
     const uint32_t group = threadIdx.x / T;
     const int j = threadIdx.x % T, at = (int)group * G + 4 * j;
     const bool live = WHOLE || (int)group * G < here;     // lanes of groups past the end run along with zeros
     const int64_t groups = chunk / G;
-    Raw4 rp[4], rg[4];
-    uint32_t qm[4], qv[4];
+    Raw4 rp[NV], rg[NV];
+    uint32_t qm[NV], qv[NV];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < NV; i++) {
         qm[i] = load_codes(t.m + chunk, at + i * STRIDE, here);
         qv[i] = load_codes(t.v + chunk, at + i * STRIDE, here);
     }
@@ -345,42 +352,42 @@ __device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c
     else load_raw((const uint16_t*)t.p + chunk, at, here, STRIDE, rp);
     const float scale = c.scale ? *c.scale : 1.0f;
     const bool skip = !(__builtin_fabsf(scale) < __builtin_inff());
-    float p[16];
+    float p[E];
     if (!skip) {
         const AdamScalars s = scalars_of(c);
         // what lies past the end must not reach a group's extrema
-        auto cut = [&](float (&x)[16]) __attribute__((always_inline)) {
+        auto cut = [&](float (&x)[E]) __attribute__((always_inline)) {
             if (!WHOLE)
 #pragma unroll
-                for (int i = 0; i < 16; i++)
+                for (int i = 0; i < E; i++)
                     if (at + i / 4 * STRIDE + i % 4 >= here) x[i] = 0.0f;
         };
-        float g[16], x[16], r[16];
+        float g[E], x[E], r[E];
         raw_values(gsrc, rg, g);
 #pragma unroll
-        for (int i = 0; i < 16; i++) g[i] *= scale;
-        decode_state<FMT, 16, false>(qv, lg, va, vk, x);
-        second_moment<16>(s, g, x, r);
+        for (int i = 0; i < E; i++) g[i] *= scale;
+        decode_state<FMT, E, false>(qv, lg, va, vk, x);
+        second_moment<E>(s, g, x, r);
         cut(x);
-        encode_state<FMT, T, 16, false>(x, qv, va, vk);
-        decode_state<FMT, 16>(qm, lg, ma, mk, x);
+        encode_state<FMT, T, E, false>(x, qv, va, vk);
+        decode_state<FMT, E>(qm, lg, ma, mk, x);
         raw_values(psrc, rp, p);
-        first_moment<16>(s, g, r, p, x);
+        first_moment<E>(s, g, r, p, x);
         cut(x);
-        encode_state<FMT, T, 16>(x, qm, ma, mk);
+        encode_state<FMT, T, E>(x, qm, ma, mk);
     } else {
         raw_values(psrc, rp, p);
     }
     auto store = [&](int src, uint8_t* to) __attribute__((always_inline)) {
         to += chunk * (src == SRC_F32 ? 4 : 2);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < NV; i++) {
             const float x[4] = {p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]};
             store4(src, to, (uint32_t)(at + i * STRIDE), here, x);
         }
     };
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < NV; i++) {
         store_codes(t.mo + chunk, at + i * STRIDE, here, qm[i]);
         store_codes(t.vo + chunk, at + i * STRIDE, here, qv[i]);
     }
@@ -392,7 +399,7 @@ __device__ __forceinline__ void adamw8_chunk(const Adam8& t, const AdamCommon& c
     }
 }
 
-template <int FMT, int G, bool WHOLE>
+template <int FMT, int G, bool WHOLE, int NV>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WHOLE ? 4 : 3, WHOLE ? 4 : 3)))
 void k_adamw8(const Table8 table, const AdamCommon c, int psrc, int gsrc)
 {
@@ -401,10 +408,10 @@ void k_adamw8(const Table8 table, const AdamCommon c, int psrc, int gsrc)
     __syncthreads();
     const int ti = tensor_of(table, (int)blockIdx.x);
     const Adam8& t = table.t[ti];
-    const int64_t chunk = (int64_t)((int)blockIdx.x - table.first[ti]) * CHUNK;
-    if constexpr (WHOLE) adamw8_chunk<FMT, G, true>(t, c, lg, chunk, psrc, gsrc);
-    else if (chunk + CHUNK <= t.n) adamw8_chunk<FMT, G, true>(t, c, lg, chunk, psrc, gsrc);
-    else adamw8_chunk<FMT, G, false>(t, c, lg, chunk, psrc, gsrc);
+    const int64_t chunk = (int64_t)((int)blockIdx.x - table.first[ti]) * (1024 * NV);
+    if constexpr (WHOLE) adamw8_chunk<FMT, G, true, NV>(t, c, lg, chunk, psrc, gsrc);
+    else if (chunk + 1024 * NV <= t.n) adamw8_chunk<FMT, G, true, NV>(t, c, lg, chunk, psrc, gsrc);
+    else adamw8_chunk<FMT, G, false, NV>(t, c, lg, chunk, psrc, gsrc);
 }
 
 // ---------------------------------------------------------------------------
@@ -619,11 +626,11 @@ hipError_t run32(const AdamJob& j, const AdamCommon& c, hipStream_t s)
     return elements_of(j) < launches * SMALL_STEP ? run32<PS, GS, SMALL_CHUNK / 1024>(j, c, s) : run32<PS, GS, CHUNK / 1024>(j, c, s);
 }
 
-template <int FMT, int G, bool WHOLE, typename Piece>
+template <int FMT, int G, bool WHOLE, int NV, typename Piece>
 hipError_t run8(const AdamJob& j, const AdamCommon& c, Piece piece, hipStream_t s)
 {
-    return walk<Table8>(j.count, piece, CHUNK, MOST_CHUNKS, put8, [&](const Table8& t, int chunks) {
-        k_adamw8<FMT, G, WHOLE><<<chunks, 256, 0, s>>>(t, c, j.psrc, j.gsrc);
+    return walk<Table8>(j.count, piece, 1024 * NV, MOST_CHUNKS, put8, [&](const Table8& t, int chunks) {
+        k_adamw8<FMT, G, WHOLE, NV><<<chunks, 256, 0, s>>>(t, c, j.psrc, j.gsrc);
         return hipGetLastError();
     });
 }
@@ -631,12 +638,16 @@ hipError_t run8(const AdamJob& j, const AdamCommon& c, Piece piece, hipStream_t 
 template <int FMT, int G>
 hipError_t run8(const AdamJob& j, const AdamCommon& c, hipStream_t s)
 {
+    auto all = [&](int i) { return j.tensors[i]; };
+    const int64_t launches = (j.count + Table8::most - 1) / Table8::most, n = elements_of(j);
+    if (n < launches * FEW_8) return run8<FMT, G, false, 1>(j, c, all, s);
+    if (n < launches * SMALL_8) return run8<FMT, G, false, 2>(j, c, all, s);
     bool cut = false;
     for (int i = 0; i < j.count; i++) cut = cut || j.tensors[i].n % CHUNK != 0;
-    if (cut && elements_of(j) < SPLIT_STEP) return run8<FMT, G, false>(j, c, [&](int i) { return j.tensors[i]; }, s);
-    const hipError_t e = run8<FMT, G, true>(j, c, [&](int i) { return part_of(j.tensors[i], j, 0, j.tensors[i].n / CHUNK * CHUNK); }, s);
+    if (cut && n < SPLIT_STEP) return run8<FMT, G, false, 4>(j, c, all, s);
+    const hipError_t e = run8<FMT, G, true, 4>(j, c, [&](int i) { return part_of(j.tensors[i], j, 0, j.tensors[i].n / CHUNK * CHUNK); }, s);
     if (e != hipSuccess) return e;
-    return run8<FMT, G, false>(j, c, [&](int i) {
+    return run8<FMT, G, false, 4>(j, c, [&](int i) {
         const int64_t whole = j.tensors[i].n / CHUNK * CHUNK;
         return part_of(j.tensors[i], j, whole, j.tensors[i].n - whole);
     }, s);

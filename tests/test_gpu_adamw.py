@@ -225,18 +225,21 @@ def _fp8(sizes, fmt, group, p="f32", g="f32", seed=0):
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("group", [32, 64, 128, 256])
 @pytest.mark.parametrize("sizes", [[1], [31, 33], [127, 128, 129, 255, 257], [4096], [4095, 4097],
-                                   [5 + 131 * i for i in range(60)], [4096 * 300 + 77]])
+                                   [5 + 131 * i for i in range(60)], [4096 * 300 + 77], [(1 << 20) + 45, 4099],
+                                   [(7 << 20) + 45, 9000, 5], [7 << 20]])
 def test_fp8_moments(sizes, fmt, group):
     _check_fp8(_fp8(sizes, fmt, group, seed=group), fmt, group)
 
 
+@pytest.mark.parametrize("more", [0, 1 << 20, 7 << 20])           # 4, 8 and 16 elements a lane
 @pytest.mark.parametrize("p,g", [("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
-def test_fp8_types(p, g):
-    _check_fp8(_fp8([5000, 4097], "e4m3", 128, p, g), "e4m3", 128, scale=torch.tensor([0.4], device=DEV))
+def test_fp8_types(p, g, more):
+    _check_fp8(_fp8([more + 5000, 4097], "e4m3", 128, p, g), "e4m3", 128, scale=torch.tensor([0.4], device=DEV))
 
 
+@pytest.mark.parametrize("more", [0, 1 << 20, 7 << 20])
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
-def test_fp8_special_groups(fmt):
+def test_fp8_special_groups(fmt, more):
     """Groups of zeros, of one value, with NaN and Inf gradients, of huge and tiny spread, with odd parameters."""
     n, group = 128 * 12, 128
     p, g, m, v = _make([n], seed=9)
@@ -255,7 +258,12 @@ def test_fp8_special_groups(fmt):
     states = [[_quantized(x.flatten(), fmt, group)] for x in (m, v)]
     states[0][0][2][11] = 1e-3                       # k so small that 1/k is large
     states[1][0][2][11] = 1e3
-    _check_fp8((p, [g.flatten()], *states), fmt, group, step=2)
+    g = [g.flatten()]
+    if more:
+        rest = _fp8([more + 77], fmt, group, seed=10)
+        p, g = ([torch.cat([a[0], b[0]])] for a, b in ((p, rest[0]), (g, rest[1])))
+        states = [[tuple(torch.cat(x) for x in zip(a[0], b[0]))] for a, b in zip(states, rest[2:])]
+    _check_fp8((p, g, *states), fmt, group, step=2)
 
 
 def test_fp8_first_steps_from_zero():
